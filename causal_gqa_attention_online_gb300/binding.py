@@ -27,7 +27,9 @@ _DTYPE_CODE = {torch.float32: ATTN_F32, torch.float16: ATTN_F16, torch.bfloat16:
 EXPORTED = ("attn_fwd", "attn_fwd_varlen", "attn_fwd_algo", "attn_fwd_varlen_algo",
             "attn_fwd_ex", "attn_fwd_varlen_ex", "attn_fwd_paged", "attn_fwd_masked",
             "attn_bwd", "attn_bwd_varlen", "attn_lse_combine", "attn_lse_combine_ex",
-            "attn_fwd_decode_noalloc", "attn_fwd_staged", "attn_last_error",
+            "attn_fwd_decode_noalloc", "attn_fwd_staged", "attn_cache_append",
+            "attn_cache_append_varlen", "attn_fwd_paged_q8", "attn_pages_copy",
+            "attn_pages_fork", "attn_pages_compact", "attn_last_error",
             "attn_device_status", "attn_set_wait_limit", "attn_kernel_launches", "attn_version")
 
 _lock = threading.Lock()
@@ -89,6 +91,18 @@ def load_library(path: str | None = None):
         lib.attn_lse_combine.restype = ip
         lib.attn_lse_combine_ex.argtypes = [vp, vp, vp, vp, ip, ctypes.c_longlong, ip, ip, ip, vp]
         lib.attn_lse_combine_ex.restype = ip
+        cache = [ip, ip, ip, ip, ip]  # max_pages, page_size, num_pages, block_size, cache_dtype
+        lib.attn_cache_append.argtypes = [vp] * 6 + [ip] * 5 + [vp] * 3 + cache + [ip, vp]
+        lib.attn_cache_append_varlen.argtypes = [vp] * 6 + [ip] * 6 + [vp] * 3 + cache + [ip, vp]
+        lib.attn_fwd_paged_q8.argtypes = ([vp] * 7 + [ip] * 6 + [vp] + cache +
+                                          [vp, vp, ip, fp, ip, ip, ip, vp])
+        lib.attn_pages_copy.argtypes = [vp] * 3 + [ip] * 3 + [vp, vp, ip, vp]
+        lib.attn_pages_fork.argtypes = ([vp, vp, ip, vp, vp, vp] + [ip] * 4 + [vp, vp, ip] +
+                                        [vp] * 5)
+        lib.attn_pages_compact.argtypes = [vp, vp, ip, vp, vp, ip, ip, ip] + [vp] * 5
+        for f in (lib.attn_cache_append, lib.attn_cache_append_varlen, lib.attn_fwd_paged_q8,
+                  lib.attn_pages_copy, lib.attn_pages_fork, lib.attn_pages_compact):
+            f.restype = ip
         lib.attn_last_error.argtypes = []
         lib.attn_last_error.restype = ctypes.c_char_p
         lib.attn_device_status.argtypes = [ctypes.POINTER(ctypes.c_int)]

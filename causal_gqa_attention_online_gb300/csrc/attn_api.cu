@@ -56,8 +56,6 @@ int sm_count(int device) {
     return g_sm_count[device];
 }
 
-namespace {
-
 int current_device(int *dev) {
     const cudaError_t e = cudaGetDevice(dev);
     if (e != cudaSuccess || *dev < 0 || *dev >= kMaxDevices) {
@@ -112,8 +110,6 @@ int pool_for(int dev, cudaMemPool_t *out) {
 }
 
 bool ptr_aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-}  // namespace
 
 // Host-side validation shared by both layouts.
 int validate(const void *q, const void *k, const void *v, const void *o, const float *lse,
@@ -200,9 +196,7 @@ int launch_split_kv(const AttnParams &p, int chosen, int dtype, cudaStream_t str
     return rc;
 }
 
-namespace {
-
-int run(AttnParams &p, int dtype, int algo, cudaStream_t stream) {
+int run_forward(AttnParams &p, int dtype, int algo, cudaStream_t stream) {
     int dev = 0;
     int rc = current_device(&dev);
     if (rc) return rc;
@@ -298,6 +292,8 @@ int run(AttnParams &p, int dtype, int algo, cudaStream_t stream) {
     return rc;
 }
 
+namespace {
+
 int fwd_common(const void *q, const void *k, const void *v, void *o, float *lse, int B, int Hq,
                int Hkv, long long Tq, long long Tk, int Q, int K, int D, int Dv,
                const int32_t *seqlens_q,
@@ -357,7 +353,7 @@ int fwd_common(const void *q, const void *k, const void *v, void *o, float *lse,
     p.nsplit = 1;
     p.split_len = K > 0 ? K : 1;
     p.wait_ns = wait_limit_ns();
-    return run(p, dtype, algo, stream);
+    return run_forward(p, dtype, algo, stream);
 }
 
 int bwd_common(const void *q, const void *k, const void *v, const void *o, const float *lse,

@@ -1,0 +1,578 @@
+// kernel_pages.cu -- management of a paged cache's pages: copying pages of
+// several pools, the next version of a block table (fork), and compaction.
+//
+// Block tables and reference counts are versions: an operation reads one and
+// writes the next, so a call that does not fit its pool leaves the caller's
+// version as it was, and every call can be captured into a graph.  The integer
+// work is latency bound (a few thousand entries); it runs as one cluster of
+// kPlanCtas blocks that meet at cluster barriers, so a plan is one launch
+// whatever its phases, and the copies and the table follow in a second one.
+// Page numbers are handed out lowest first and the results do not depend on
+// the order of any atomic: counts and minima only.
+//
+// Copies move 2 bytes for each byte of a page.  A warp moves a chunk of a page
+// with 16-byte loads, all issued before the first store, and the chunks of all
+// pools form one index space, so that small pools (scales) and large ones fill
+// the same launch.
+#include <climits>
+
+#include <cooperative_groups.h>
+
+#include "common.cuh"
+#include "launch.h"
+
+namespace attn {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kPlanCtas = 8;       // blocks of the planning cluster (the portable size)
+constexpr int kPlanThreads = 1024;
+constexpr int kCopyThreads = 256;
+constexpr int kChunk = 4096;       // bytes a warp moves at a time: 8 x 16 bytes a lane
+
+struct PoolTable {
+    const uint8_t *src[kMaxPools];
+    uint8_t *dst[kMaxPools];
+    long long bytes[kMaxPools];      // bytes of a page
+    int first_chunk[kMaxPools + 1];  // chunks of a page before this pool's
+    int n;
+};
+
+// ------------------------------------------------------------------- copies
+
+template <typename V> __device__ __forceinline__ void copy_units(uint8_t *dst, const uint8_t *src, int n, int lane) {
+    constexpr int U = kChunk / 32 / 16;  // units a lane keeps in flight
+    const V *s = reinterpret_cast<const V *>(src);
+    V *d = reinterpret_cast<V *>(dst);
+    for (int i0 = 0; i0 < n; i0 += 32 * U) {
+        V v[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (i0 + i * 32 + lane < n) v[i] = __ldcs(s + i0 + i * 32 + lane);
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (i0 + i * 32 + lane < n) __stcs(d + i0 + i * 32 + lane, v[i]);
+    }
+}
+
+// Pages src[i] -> dst[i] (src_back: src[n - 1 - i] -> dst[i]) of every pool, by
+// the warps of the grid.  Entries outside the pools are skipped.
+__device__ void copy_pages(const PoolTable &t, const int32_t *src, const int32_t *dst, int n,
+                           int src_pages, int dst_pages, bool src_back = false) {
+    const int per_page = t.first_chunk[t.n];
+    const long long total = (long long)n * per_page;
+    const int lane = threadIdx.x & 31;
+    const long long step = (long long)gridDim.x * (blockDim.x / 32);
+    for (long long c = (long long)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); c < total;
+         c += step) {
+        const int i = (int)(c / per_page), r = (int)(c - (long long)i * per_page);
+        const int sp = __ldg(src + (src_back ? n - 1 - i : i)), dp = __ldg(dst + i);
+        if (sp < 0 || sp >= src_pages || dp < 0 || dp >= dst_pages) continue;
+        int pool = 0;
+        while (r >= t.first_chunk[pool + 1]) ++pool;
+        const long long off = (long long)(r - t.first_chunk[pool]) * kChunk;
+        const long long bytes = t.bytes[pool];
+        const int len = (int)min((long long)kChunk, bytes - off);
+        const uint8_t *s = t.src[pool] + sp * bytes + off;
+        uint8_t *d = t.dst[pool] + dp * bytes + off;
+        const uintptr_t low = reinterpret_cast<uintptr_t>(s) | reinterpret_cast<uintptr_t>(d) | (uintptr_t)len;
+        if ((low & 15) == 0) copy_units<uint4>(d, s, len / 16, lane);
+        else if ((low & 3) == 0) copy_units<uint32_t>(d, s, len / 4, lane);
+        else copy_units<uint8_t>(d, s, len, lane);
+    }
+}
+
+__global__ void __launch_bounds__(kCopyThreads)
+    copy_pages_kernel(const __grid_constant__ PoolTable t, const int32_t *src, const int32_t *dst,
+                      int n, int src_pages, int dst_pages) {
+    copy_pages(t, src, dst, n, src_pages, dst_pages);
+}
+
+// The same with the number of pages, and whether src runs from the back,
+// decided by an earlier kernel.
+__global__ void __launch_bounds__(kCopyThreads)
+    copy_counted_kernel(const __grid_constant__ PoolTable t, const int32_t *src, const int32_t *dst,
+                        const int32_t *count, int pages, bool src_back) {
+    copy_pages(t, src, dst, __ldg(count), pages, pages, src_back);
+}
+
+// --------------------------------------------------------------- block scans
+
+// Exclusive sum of v over the block's threads; *total gets the block's sum.
+// `warps`: 32 ints of shared memory.
+__device__ __forceinline__ int block_scan(int v, int *warps, int *total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    __syncthreads();
+    if (lane == 31) warps[warp] = incl;
+    __syncthreads();
+    if (warp == 0) {
+        int w = warps[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w += y;
+        }
+        warps[lane] = w;
+    }
+    __syncthreads();
+    *total = warps[31];
+    return incl - v + (warp > 0 ? warps[warp - 1] : 0);
+}
+
+// --------------------------------------------------------------------- fork
+
+struct ForkArgs {
+    const int32_t *table, *lens, *refs, *parents, *grow;
+    int S, M, P, N, page_shift;
+    int32_t *table_out, *lens_out, *refs_out, *status;
+    // workspace: per page, references by the old table, by full entries of the
+    // new one, the lowest claiming entry, and whether an entry holds it
+    int32_t *was, *full, *held;
+    unsigned long long *claim;
+    int32_t *src, *dst;  // pages to copy (N at most)
+    int32_t *list;       // the free pages in use, in ascending order
+    int32_t *count;      // [0] pages to copy, [1] free pages
+};
+
+struct Slot {
+    int parent;       // row of the old table, -1: empty
+    int len;          // tokens
+    long long want;   // table entries of the new version
+    int nfull;        // of them, pages full of tokens (shared)
+};
+
+__device__ __forceinline__ Slot slot_of(const ForkArgs &a, int i) {
+    Slot s;
+    s.parent = __ldg(a.parents + i);
+    s.len = 0;
+    s.want = 0;
+    s.nfull = 0;
+    if (s.parent < 0 || s.parent >= a.S) {
+        s.parent = -1;
+        return s;
+    }
+    const long long cap = (long long)a.M << a.page_shift;
+    s.len = (int)min(max((long long)__ldg(a.lens + s.parent), 0LL), cap);
+    const long long grow = a.grow ? max(__ldg(a.grow + i), 0) : 0;
+    s.want = (s.len + grow + (1LL << a.page_shift) - 1) >> a.page_shift;
+    s.nfull = s.len >> a.page_shift;
+    return s;
+}
+
+__device__ __forceinline__ int cand_of(const ForkArgs &a, const Slot &s, int j) {
+    return __ldg(a.table + (long long)s.parent * a.M + j);
+}
+
+// Whether entry j (not full) of slot i keeps its parent's page: the page is
+// live, no full entry and nobody outside the tables holds it, and this entry is
+// the first that wants it.
+__device__ __forceinline__ bool keeps(const ForkArgs &a, int i, int j, int c) {
+    if (c < 0 || c >= a.P) return false;
+    const int refs = __ldg(a.refs + c);
+    return refs > 0 && __ldcg(a.full + c) == 0 && refs <= __ldcg(a.was + c) &&
+           __ldcg(a.claim + c) == (unsigned long long)i * a.M + j;
+}
+
+__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
+    fork_plan_kernel(const ForkArgs a) {
+    __shared__ int warps[32];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int gt = blockIdx.x * kPlanThreads + threadIdx.x;
+    const int gn = kPlanCtas * kPlanThreads;
+    // 1. clear the per-page workspace
+    for (int p = gt; p < a.P; p += gn) {
+        a.was[p] = 0;
+        a.full[p] = 0;
+        a.held[p] = 0;
+        a.claim[p] = ~0ull;
+    }
+    if (gt < 2) a.count[gt] = 0;
+    __threadfence();
+    cluster.sync();
+    // 2. references by the old table; full entries and claims of the new one
+    for (long long e = gt; e < (long long)a.S * a.M; e += gn) {
+        const int c = __ldg(a.table + e);
+        if (c >= 0 && c < a.P) atomicAdd(a.was + c, 1);
+    }
+    int nfree = 0;
+    for (int p = gt; p < a.P; p += gn) nfree += __ldg(a.refs + p) == 0;
+    if (nfree) atomicAdd(a.count + 1, nfree);
+    const int lane = threadIdx.x & 31;
+    for (int i = gt >> 5; i < a.N; i += gn >> 5) {
+        const Slot s = slot_of(a, i);
+        if (s.parent < 0) continue;
+        const int last = (int)min(s.want, (long long)a.M);
+        for (int j = lane; j < last; j += 32) {
+            const int c = cand_of(a, s, j);
+            if (c < 0 || c >= a.P) continue;
+            if (j < s.nfull) atomicAdd(a.full + c, 1);
+            else atomicMin(a.claim + c, (unsigned long long)i * a.M + j);
+        }
+    }
+    __threadfence();
+    cluster.sync();
+    if (blockIdx.x != 0) return;
+    // 3. one block: entries that need a page, in slot order, take the free pages
+    // in ascending order
+    int wide = 0;
+    long long need = 0;
+    const int warp = threadIdx.x >> 5;
+    constexpr int NW = kPlanThreads / 32;
+    for (int i = warp; i < a.N; i += NW) {
+        const Slot s = slot_of(a, i);
+        if (s.parent < 0) continue;
+        if (lane == 0 && s.want > a.M) ++wide;
+        const int last = (int)min(s.want, (long long)a.M);
+        for (int j = s.nfull + lane; j < last; j += 32) need += !keeps(a, i, j, cand_of(a, s, j));
+    }
+    __shared__ unsigned long long sum_need;
+    __shared__ int sum_wide;
+    if (threadIdx.x == 0) {
+        sum_need = 0;
+        sum_wide = 0;
+    }
+    __syncthreads();
+    if (need) atomicAdd(&sum_need, (unsigned long long)need);
+    if (wide) atomicAdd(&sum_wide, wide);
+    __syncthreads();
+    const long long total = (long long)sum_need, missing = total - __ldcg(a.count + 1);
+    const bool fine = missing <= 0 && sum_wide == 0;
+    if (threadIdx.x == 0) {
+        a.status[0] = missing > 0 ? (int)min(missing, (long long)INT_MAX) : 0;
+        a.status[1] = sum_wide;
+        a.status[2] = fine ? (int)total : 0;
+        if (!fine) a.status[3] = 0;
+    }
+    if (!fine) return;
+    // the first `total` free pages in ascending order, eight pages a thread
+    int base = 0;
+    for (long long p0 = 0; p0 < a.P && base < total; p0 += 8 * kPlanThreads) {
+        const long long p = p0 + 8 * threadIdx.x;
+        unsigned f = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (p + k < a.P && __ldg(a.refs + p + k) == 0) f |= 1u << k;
+        int tot;
+        int at = base + block_scan(__popc(f), warps, &tot);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if ((f >> k) & 1u) a.list[at++] = (int)(p + k);
+        base += tot;
+    }
+    __syncthreads();
+    // slots in order, 32 at a time (one a warp): count, scan, assign
+    __shared__ int copies;
+    if (threadIdx.x == 0) copies = 0;
+    int taken = 0;
+    for (int i0 = 0; i0 < a.N; i0 += NW) {
+        const int i = i0 + warp;
+        Slot s;
+        s.parent = -1;
+        s.nfull = s.len = 0;
+        s.want = 0;
+        if (i < a.N) s = slot_of(a, i);
+        const int last = s.parent < 0 ? 0 : (int)min(s.want, (long long)a.M);
+        int cnt = 0;
+        for (int j = s.nfull + lane; j < last; j += 32) cnt += !keeps(a, i, j, cand_of(a, s, j));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) cnt += __shfl_xor_sync(0xffffffffu, cnt, o);
+        int tot;
+        int at = block_scan(lane == 0 ? cnt : 0, warps, &tot);
+        at = taken + __shfl_sync(0xffffffffu, at, 0);
+        taken += tot;
+        for (int j0 = s.nfull; j0 < last; j0 += 32) {
+            const int j = j0 + lane;
+            int c = -1;
+            bool get = false;
+            if (j < last) {
+                c = cand_of(a, s, j);
+                get = !keeps(a, i, j, c);
+            }
+            const unsigned m = __ballot_sync(0xffffffffu, get);
+            int pg = c;
+            if (get) pg = a.list[at + __popc(m & ((1u << lane) - 1u))];
+            at += __popc(m);
+            if (j < last) {
+                a.table_out[(long long)i * a.M + j] = pg;
+                a.held[pg] = 1;
+                if (get && c >= 0 && c < a.P && j == s.nfull && (s.len & ((1 << a.page_shift) - 1))) {
+                    const int k = atomicAdd(&copies, 1);
+                    a.src[k] = c;
+                    a.dst[k] = pg;
+                }
+            }
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        a.status[3] = copies;
+        a.count[0] = copies;
+    }
+}
+
+// The new version's remaining entries, lengths and counts, and the page copies.
+__global__ void __launch_bounds__(kCopyThreads)
+    fork_finish_kernel(const ForkArgs a, const __grid_constant__ PoolTable t) {
+    const bool fine = __ldg(a.status) == 0 && __ldg(a.status + 1) == 0;
+    const long long gt = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    const long long gn = (long long)gridDim.x * blockDim.x;
+    for (long long p = gt; p < a.P; p += gn) {
+        const int r = __ldg(a.refs + p);
+        a.refs_out[p] = fine ? r - __ldg(a.was + p) + __ldg(a.full + p) + __ldg(a.held + p) : r;
+    }
+    const int lane = threadIdx.x & 31;
+    for (long long i = gt >> 5; i < a.N; i += gn >> 5) {
+        const Slot s = slot_of(a, (int)i);
+        if (lane == 0) a.lens_out[i] = fine ? s.len : 0;
+        const int last = fine ? (int)min(s.want, (long long)a.M) : 0;
+        for (int j = lane; j < a.M; j += 32) {
+            int v = -1;
+            if (fine && j < s.nfull) {
+                const int c = cand_of(a, s, j);
+                v = c >= 0 && c < a.P ? c : -1;
+            } else if (j < last) {
+                continue;  // the plan wrote it
+            }
+            a.table_out[i * a.M + j] = v;
+        }
+    }
+    if (t.n > 0) copy_pages(t, a.src, a.dst, __ldg(a.count), a.P, a.P);
+}
+
+// ------------------------------------------------------------------ compact
+
+struct CompactArgs {
+    const int32_t *table, *refs;
+    int S, M, P;
+    int32_t *table_out, *refs_out, *remap, *n_live;
+    int32_t *src, *dst;  // pages to move (src from the back) and the holes they fill
+    int32_t *count;      // [0] pages to move
+};
+
+__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
+    compact_plan_kernel(const CompactArgs a) {
+    __shared__ int warps[32];
+    __shared__ int mine;  // live pages of this block's part
+    cg::cluster_group cluster = cg::this_cluster();
+    const int per = (a.P + kPlanCtas - 1) / kPlanCtas;
+    const int p0 = min(blockIdx.x * per, (unsigned)a.P), p1 = min(p0 + per, a.P);
+    int cnt = 0;
+    for (int p = p0 + threadIdx.x; p < p1; p += kPlanThreads) cnt += __ldg(a.refs + p) > 0;
+    int tot;
+    block_scan(cnt, warps, &tot);
+    if (threadIdx.x == 0) mine = tot;
+    cluster.sync();
+    int before = 0, n = 0;
+    for (int r = 0; r < kPlanCtas; ++r) {
+        const int c = *cluster.map_shared_rank(&mine, r);
+        if (r < (int)blockIdx.x) before += c;
+        n += c;
+    }
+    // Holes (free pages before n) take the live pages at or behind n, both in
+    // ascending order.  A hole's rank is its index less the live pages before
+    // it; a mover's is counted from the back (n - 1 less the live pages before
+    // it), so that one scan ranks both.
+    int live_before = before;
+    for (int q0 = p0; q0 < p1; q0 += kPlanThreads) {
+        const int p = q0 + threadIdx.x;
+        const bool in = p < p1;
+        const int r = in ? __ldg(a.refs + p) : 0;
+        const int live = r > 0;
+        const int at = live_before + block_scan(live, warps, &tot);
+        if (in) {
+            if (p == n) a.count[0] = n - at;  // pages to move
+            if (live && p >= n) a.src[n - 1 - at] = p;
+            if (!live && p < n) a.dst[p - at] = p;
+            // (a mover's number and a hole's count follow below)
+            if (!live || p < n) a.remap[p] = live ? p : -1;
+            if (live || p >= n) a.refs_out[p] = p < n ? r : 0;
+        }
+        live_before += tot;
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        *a.n_live = n;
+        if (n == a.P) a.count[0] = 0;  // no hole
+    }
+    __threadfence();
+    cluster.sync();  // (also: every block has read `mine` before any leaves)
+    const int moves = __ldcg(a.count);
+    for (int k = blockIdx.x * kPlanThreads + threadIdx.x; k < moves; k += kPlanCtas * kPlanThreads) {
+        const int d = __ldcg(a.dst + k), s = __ldcg(a.src + moves - 1 - k);
+        a.remap[s] = d;
+        a.refs_out[d] = __ldg(a.refs + s);
+    }
+}
+
+__global__ void __launch_bounds__(kCopyThreads)
+    compact_finish_kernel(const CompactArgs a, const __grid_constant__ PoolTable t) {
+    const long long gt = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    const long long gn = (long long)gridDim.x * blockDim.x;
+    for (long long e = gt; e < (long long)a.S * a.M; e += gn) {
+        const int c = __ldg(a.table + e);
+        a.table_out[e] = c >= 0 && c < a.P ? __ldg(a.remap + c) : -1;
+    }
+    if (t.n > 0) copy_pages(t, a.src, a.dst, __ldg(a.count), a.P, a.P, true);
+}
+
+// --------------------------------------------------------------------- host
+
+// 0, or 2 when a page has more chunks than the index holds.
+int fill_pools(PoolTable &t, const void *const *src, void *const *dst, const long long *bytes,
+               int n) {
+    long long chunks = 0;
+    t.n = n;
+    for (int i = 0; i < n; ++i) {
+        t.src[i] = static_cast<const uint8_t *>(src[i]);
+        t.dst[i] = static_cast<uint8_t *>(dst[i]);
+        t.bytes[i] = bytes[i];
+        t.first_chunk[i] = (int)chunks;
+        chunks += (bytes[i] + kChunk - 1) / kChunk;
+        if (chunks >= (1LL << 30)) {
+            set_error("pages: a page of more than 2^30 chunks");
+            return 2;
+        }
+    }
+    t.first_chunk[n] = (int)chunks;
+    return 0;
+}
+
+// Blocks for `chunks` warps' worth of copies beside `other` threads' worth of
+// table work: four blocks an SM at most.
+unsigned grid_for(long long chunks, long long other) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const int nsm = sm_count(dev);
+    const long long most = 4LL * (nsm < 1 ? 1 : nsm);
+    long long want = (chunks + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
+    const long long w2 = (other + kCopyThreads - 1) / kCopyThreads;
+    want = want > w2 ? want : w2;
+    return (unsigned)(want < 1 ? 1 : want > most ? most : want);
+}
+
+int launched(const char *what) {
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) {
+        set_error("%s launch: %s", what, cudaGetErrorString(e));
+        return 3;
+    }
+    count_launch();
+    return 0;
+}
+
+// The pools past the first kMaxPools, in launches of their own.
+template <typename F> int for_pool_groups(const void *const *src, void *const *dst, const long long *bytes, int n, F f) {
+    int rc = 0;
+    int at = 0;
+    do {
+        PoolTable t;
+        const int m = n - at < kMaxPools ? n - at : kMaxPools;
+        rc = fill_pools(t, src + at, dst + at, bytes + at, m);
+        if (rc == 0) rc = f(t, at == 0);
+        at += m;
+    } while (rc == 0 && at < n);
+    return rc;
+}
+
+}  // namespace
+
+int launch_pages_copy(const void *const *src_pools, void *const *dst_pools, const long long *bytes,
+                      int npools, int src_pages, int dst_pages, const int32_t *src,
+                      const int32_t *dst, int n, cudaStream_t stream) {
+    return for_pool_groups(src_pools, dst_pools, bytes, npools, [&](const PoolTable &t, bool) {
+        const long long chunks = (long long)n * t.first_chunk[t.n];
+        if (chunks == 0) return 0;
+        copy_pages_kernel<<<grid_for(chunks, 0), kCopyThreads, 0, stream>>>(t, src, dst, n, src_pages,
+                                                                           dst_pages);
+        return launched("page copy kernel");
+    });
+}
+
+unsigned long long pages_fork_workspace(int N, int P) {
+    return 8ull * P + 4ull * (4ull * P + 2ull * N + 2ull);
+}
+
+int launch_pages_fork(void *const *pools, const long long *bytes, int npools,
+                      const int32_t *block_table, const int32_t *seqlens, const int32_t *refcount,
+                      int S, int M, int P, int page_shift, const int32_t *parents,
+                      const int32_t *new_tokens, int N, int32_t *table_out, int32_t *seqlens_out,
+                      int32_t *refcount_out, int32_t *status, void *ws, cudaStream_t stream) {
+    ForkArgs a = {};
+    a.table = block_table;
+    a.lens = seqlens;
+    a.refs = refcount;
+    a.parents = parents;
+    a.grow = new_tokens;
+    a.S = S;
+    a.M = M;
+    a.P = P;
+    a.N = N;
+    a.page_shift = page_shift;
+    a.table_out = table_out;
+    a.lens_out = seqlens_out;
+    a.refs_out = refcount_out;
+    a.status = status;
+    a.claim = static_cast<unsigned long long *>(ws);
+    a.was = reinterpret_cast<int32_t *>(a.claim + P);
+    a.full = a.was + P;
+    a.held = a.full + P;
+    a.list = a.held + P;
+    a.src = a.list + P;
+    a.dst = a.src + N;
+    a.count = a.dst + N;
+    fork_plan_kernel<<<kPlanCtas, kPlanThreads, 0, stream>>>(a);
+    int rc = launched("page fork kernel");
+    if (rc) return rc;
+    return for_pool_groups(pools, pools, bytes, npools, [&](const PoolTable &t, bool first) {
+        const long long chunks = (long long)N * t.first_chunk[t.n];
+        if (!first) {
+            copy_counted_kernel<<<grid_for(chunks, 0), kCopyThreads, 0, stream>>>(t, a.src, a.dst, a.count, P, false);
+            return launched("page copy kernel");
+        }
+        const long long other = (long long)N * 32 > P ? (long long)N * 32 : P;
+        fork_finish_kernel<<<grid_for(chunks, other), kCopyThreads, 0, stream>>>(a, t);
+        return launched("page fork kernel");
+    });
+}
+
+unsigned long long pages_compact_workspace(int P) { return 4ull * (2ull * P + 2ull); }
+
+int launch_pages_compact(void *const *pools, const long long *bytes, int npools,
+                         const int32_t *block_table, const int32_t *refcount, int S, int M, int P,
+                         int32_t *table_out, int32_t *refcount_out, int32_t *remap,
+                         int32_t *n_live, void *ws, cudaStream_t stream) {
+    CompactArgs a = {};
+    a.table = block_table;
+    a.refs = refcount;
+    a.S = S;
+    a.M = M;
+    a.P = P;
+    a.table_out = table_out;
+    a.refs_out = refcount_out;
+    a.remap = remap;
+    a.n_live = n_live;
+    a.src = static_cast<int32_t *>(ws);
+    a.dst = a.src + P;
+    a.count = a.dst + P;
+    compact_plan_kernel<<<kPlanCtas, kPlanThreads, 0, stream>>>(a);
+    int rc = launched("page compact kernel");
+    if (rc) return rc;
+    return for_pool_groups(pools, pools, bytes, npools, [&](const PoolTable &t, bool first) {
+        // at most half of the pages move
+        const long long chunks = (long long)(P / 2) * t.first_chunk[t.n];
+        if (!first) {
+            copy_counted_kernel<<<grid_for(chunks, 0), kCopyThreads, 0, stream>>>(t, a.src, a.dst, a.count, P, true);
+            return launched("page copy kernel");
+        }
+        compact_finish_kernel<<<grid_for(chunks, (long long)S * M), kCopyThreads, 0, stream>>>(a, t);
+        return launched("page compact kernel");
+    });
+}
+
+}  // namespace attn

@@ -16,6 +16,16 @@ void count_launch();  // one successful kernel launch
 int sm_count(int device);  // 0 if the device index or the query is bad
 unsigned long long wait_limit_ns();  // limit of the tcgen05 kernels' mbarrier waits
 
+// The current device, its status word, the library's stream-ordered pool on it;
+// 0 or an attn_status code with a message.
+int current_device(int *dev);
+int status_ptr(int dev, int **out);
+int pool_for(int dev, cudaMemPool_t *out);
+bool ptr_aligned16(const void *p);
+
+// Kernel choice, workspace and launches of one forward problem (algo: attn_algo).
+int run_forward(AttnParams &p, int dtype, int algo, cudaStream_t stream);
+
 // Host-side argument checks shared by the entry points (dtype, algo, sizes,
 // pointers, 16-byte alignment); 0 or an attn_status code with a message.
 int validate(const void *q, const void *k, const void *v, const void *o, const float *lse,
@@ -93,5 +103,38 @@ int launch_bwd_dkdv_tc(const BwdParams &bp, int dtype, cudaStream_t stream, bool
 // and runs first), the mma.sync one otherwise.
 bool bwd_mma_supported(const AttnParams &p, int dtype);
 int launch_bwd(const BwdParams &bp, int dtype, int mode, cudaStream_t stream);
+
+// ---- the 8-bit paged cache (q8.cuh) and its pages
+
+struct Q8Cache;
+
+// New rows into the cache; every size is positive (checked by the entry point).
+int launch_cache_append(const void *k, const void *v, void *k_pages, void *v_pages, float *k_scale,
+                        float *v_scale, int B, int N, int Hkv, int D, int Dv,
+                        const int32_t *seqlens_new, const int32_t *cu_new, long long total,
+                        const int32_t *seqlens_k, const int32_t *block_table, int max_pages,
+                        int page_shift, int num_pages, int nblk, int blk_shift, int code,
+                        int dtype, cudaStream_t stream);
+// The keys and values of p's sequences as contiguous rows [B][K][Hkv][D | Dv] of
+// dtype (p.B <= 65535).
+int launch_q8_expand(const AttnParams &p, const Q8Cache &c, void *k_out, void *v_out, int dtype,
+                     cudaStream_t stream);
+
+constexpr int kMaxPools = 64;  // pools one launch copies
+int launch_pages_copy(const void *const *src_pools, void *const *dst_pools, const long long *bytes,
+                      int npools, int src_pages, int dst_pages, const int32_t *src,
+                      const int32_t *dst, int n, cudaStream_t stream);
+// ws: the given number of bytes at an 8-byte aligned address.
+unsigned long long pages_fork_workspace(int N, int P);
+int launch_pages_fork(void *const *pools, const long long *bytes, int npools,
+                      const int32_t *block_table, const int32_t *seqlens, const int32_t *refcount,
+                      int S, int M, int P, int page_shift, const int32_t *parents,
+                      const int32_t *new_tokens, int N, int32_t *table_out, int32_t *seqlens_out,
+                      int32_t *refcount_out, int32_t *status, void *ws, cudaStream_t stream);
+unsigned long long pages_compact_workspace(int P);
+int launch_pages_compact(void *const *pools, const long long *bytes, int npools,
+                         const int32_t *block_table, const int32_t *refcount, int S, int M, int P,
+                         int32_t *table_out, int32_t *refcount_out, int32_t *remap,
+                         int32_t *n_live, void *ws, cudaStream_t stream);
 
 }  // namespace attn

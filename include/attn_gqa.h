@@ -98,6 +98,9 @@ enum attn_mask {
     ATTN_MASK_NONE = 2             /* every key k < Kb (no window allowed) */
 };
 
+/* Element types of an 8-bit paged cache's codes (attn_cache_append). */
+enum attn_cache_dtype { ATTN_CACHE_E4M3 = 0, ATTN_CACHE_INT8 = 1 };
+
 /*
  * attn_fwd -- padded layout.
  *   q   [B, Q, Hq, D]    o   [B, Q, Hq, Dv]    lse [B, Q, Hq] (float32, may be NULL)
@@ -353,6 +356,140 @@ ATTN_API int attn_bwd_varlen(const void *q, const void *k, const void *v, const 
                              int max_K, int D, int Dv, const int32_t *cu_seqlens_q,
                              const int32_t *cu_seqlens_k, int window, float scale, int mask,
                              int dtype, int algo, attn_stream_t stream);
+
+/*
+ * The 8-bit paged cache.  A serving layout of this library (the pages have no
+ * counterpart): the pools of attn_fwd_paged with one byte an element,
+ *   k_pages  [num_pages, page_size, Hkv, D]   v_pages [num_pages, page_size, Hkv, Dv]
+ *   k_scale, v_scale  float32 [num_pages, page_size / block_size, Hkv]
+ * where an element of row r of a page stands for code * scale[page, r / block_size,
+ * head]: one scale for each block of block_size tokens (a power of two up to
+ * page_size) and head.  cache_dtype ATTN_CACHE_INT8 holds -127..127,
+ * ATTN_CACHE_E4M3 the e4m3 values up to +-448 (the NaN code is never written and
+ * reads as +-480).  Block tables and lengths as in attn_fwd_paged.
+ *
+ * attn_cache_append -- writes N new rows of each sequence behind the seqlens_k
+ * rows it has (seqlens_k is not changed: the caller adds the new rows to it).
+ *   k [B, N, Hkv, D], v [B, N, Hkv, Dv]   the new rows, in `dtype` (attn_dtype)
+ *   seqlens_new  int32 [B] on the device, new rows of each sequence (clamped to
+ *                [0, N]), or NULL for N of each
+ *   block_table  int32 [B, max_pages]: every page that gets rows must be there
+ *                already and belong to one sequence only (attn_pages_fork sees
+ *                to both).  Rows whose entry is outside [0, num_pages), or past
+ *                the table, are dropped.
+ * A block's scale is the smallest power of two s >= 2^-100 with |x| <= qmax * s
+ * (qmax 127 or 448) for its rows, and codes are round-to-nearest-even(x / s).  In
+ * a block that has rows already the scale is max(old, needed), and where it
+ * grows the block's earlier codes are rounded again under it (e4m3: exactly, down
+ * to its subnormals; int8: the roundings sum to at most one step).  Rows and
+ * scales of blocks behind the new rows are left as they were.  A block that
+ * receives an infinity or a NaN gets the scale NaN and codes 0, and rows that
+ * attend to it are what attn_fwd gives for NaN keys and values; it stays so
+ * until its page is used afresh.
+ * attn_cache_append_varlen takes the new rows packed: k [total_new, Hkv, D],
+ * sequence b's rows [cu_seqlens_new[b], cu_seqlens_new[b + 1]), max_new an upper
+ * bound of their number.
+ * Widths in [1, 512].  Returns ATTN_OK, ATTN_ERR_INVALID, ATTN_ERR_UNSUPPORTED
+ * (more than 2^31 blocks of rows) or ATTN_ERR_CUDA; asynchronous on `stream`.
+ */
+ATTN_API int attn_cache_append(const void *k, const void *v, void *k_pages, void *v_pages,
+                               float *k_scale, float *v_scale, int B, int N, int Hkv, int D,
+                               int Dv, const int32_t *seqlens_new, const int32_t *seqlens_k,
+                               const int32_t *block_table, int max_pages, int page_size,
+                               int num_pages, int block_size, int cache_dtype, int dtype,
+                               attn_stream_t stream);
+ATTN_API int attn_cache_append_varlen(const void *k, const void *v, void *k_pages, void *v_pages,
+                                      float *k_scale, float *v_scale, int B, int total_new,
+                                      int max_new, int Hkv, int D, int Dv,
+                                      const int32_t *cu_seqlens_new, const int32_t *seqlens_k,
+                                      const int32_t *block_table, int max_pages, int page_size,
+                                      int num_pages, int block_size, int cache_dtype, int dtype,
+                                      attn_stream_t stream);
+
+/*
+ * attn_fwd_paged_q8 -- attn_fwd_paged over an 8-bit paged cache: the attention of
+ * the values code * scale.  q [B, Q, Hq, D], o [B, Q, Hq, Dv], lse as in
+ * attn_fwd_paged; seqlens_k counts the rows to attend to, the new ones among
+ * them (append first, then attend).  Codes and scales past a sequence's length
+ * are never used as values.
+ * Kernels (`algo`): the copy of the keys and values in q's type that the others
+ * read is made in a workspace from the library's pool, one group of sequences
+ * after the other; with the powers of two that attn_cache_append writes it is
+ * exact (fp16: within +-65504), other scales round once.  algo then chooses as in
+ * attn_fwd_ex.
+ * Return codes as attn_fwd.
+ */
+ATTN_API int attn_fwd_paged_q8(const void *q, const void *k_pages, const void *v_pages,
+                               const float *k_scale, const float *v_scale, void *o, float *lse,
+                               int B, int Hq, int Hkv, int Q, int D, int Dv,
+                               const int32_t *block_table, int max_pages, int page_size,
+                               int num_pages, int block_size, int cache_dtype,
+                               const int32_t *seqlens_q, const int32_t *seqlens_k, int window,
+                               float scale, int mask, int dtype, int algo, attn_stream_t stream);
+
+/*
+ * Pages of a cache.  A pool is any array whose first axis counts pages: the K or
+ * V pages of a layer, or their scales.  `pools` is a HOST array of npools device
+ * pointers, page_bytes the bytes of one page of each (any number, also more than
+ * one launch takes).  All pools share the block tables.
+ *
+ * attn_pages_copy -- copies page src[i] of src_pools[p] to page dst[i] of
+ * dst_pools[p] for i < n and every p.  src and dst are device int32; pairs with a
+ * number outside [0, src_pages) or [0, dst_pages) are skipped.  The dst pages must
+ * be distinct and, in the same pool, none of them a src page.
+ */
+ATTN_API int attn_pages_copy(const void *const *src_pools, void *const *dst_pools,
+                             const long long *page_bytes, int npools, int src_pages,
+                             int dst_pages, const int32_t *src, const int32_t *dst, int n,
+                             attn_stream_t stream);
+
+/*
+ * attn_pages_fork -- the next version of a block table: slot i of the new table
+ * goes on from slot parents[i] of the old one (beams and branches share a parent,
+ * -1 is an empty slot, and an old slot that nobody names is freed), with pages
+ * for new_tokens[i] more tokens (NULL: none) behind its seqlens tokens.
+ *   block_table int32 [S, max_pages], entries without a page negative;
+ *   seqlens int32 [S]; refcount int32 [num_pages]: references to each page by the
+ *   table's entries, and by anyone else who holds it (a page of count 0 is free)
+ *   parents, new_tokens  int32 [N]
+ *   block_table_out [N, max_pages], seqlens_out [N] (tokens, new ones not counted),
+ *   refcount_out [num_pages]: the new version; may not alias the old
+ *   status int32 [4]: pages that were missing, slots whose tokens do not fit
+ *   max_pages, pages newly taken, pages copied
+ * Pages full of tokens are shared.  The entries that the slot's next rows go to
+ * (from the partly filled page on) are its own: the parent's page goes to the
+ * first slot that wants it, unless an entry uses it as a full page or someone
+ * outside the table holds it; the others take free pages (those of count 0 in
+ * `refcount`), lowest first in the order of slots and entries, and the tokens of a
+ * partly filled page are copied into them in every pool.  When pages are missing
+ * or a slot is too wide (status[0] or status[1] not 0) nothing is copied,
+ * refcount_out equals refcount and the new table is empty: the old version still
+ * stands.  Tables that break the rules above give wrong pages, never a bad
+ * address.  Runs on `stream` without synchronising; workspace from the library's
+ * pool.  The result is deterministic.
+ */
+ATTN_API int attn_pages_fork(void *const *pools, const long long *page_bytes, int npools,
+                             const int32_t *block_table, const int32_t *seqlens,
+                             const int32_t *refcount, int S, int max_pages, int num_pages,
+                             int page_size, const int32_t *parents, const int32_t *new_tokens,
+                             int N, int32_t *block_table_out, int32_t *seqlens_out,
+                             int32_t *refcount_out, int32_t *status, attn_stream_t stream);
+
+/*
+ * attn_pages_compact -- moves the live pages (refcount > 0) to the front of every
+ * pool: with n of them, those at or behind n go to the free pages before n, both
+ * in ascending order; the others stay.
+ *   block_table_out [S, max_pages] (may alias block_table), refcount_out
+ *   [num_pages]: renumbered; remap int32 [num_pages]: the new number of each live
+ *   page, -1 for free ones; n_live int32 [1].
+ * Entries of pages that are not live become -1.  Runs on `stream` without
+ * synchronising; workspace from the library's pool.
+ */
+ATTN_API int attn_pages_compact(void *const *pools, const long long *page_bytes, int npools,
+                                const int32_t *block_table, const int32_t *refcount, int S,
+                                int max_pages, int num_pages, int32_t *block_table_out,
+                                int32_t *refcount_out, int32_t *remap, int32_t *n_live,
+                                attn_stream_t stream);
 
 /* Message for the calling thread's most recent failed call ("" if none). */
 ATTN_API const char *attn_last_error(void);
