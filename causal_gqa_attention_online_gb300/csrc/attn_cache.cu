@@ -150,6 +150,40 @@ int run_expanded(const AttnParams &p, const Q8Cache &c, int dtype, int algo, cud
     return rc;
 }
 
+// Split-KV decode over the codes, with its partials in the library's pool.
+int run_decode(AttnParams &p, const Q8Cache &c, int dtype, cudaStream_t stream) {
+    int dev = 0;
+    int rc = current_device(&dev);
+    if (rc) return rc;
+    rc = status_ptr(dev, &p.status);
+    if (rc) return rc;
+    p.split_len = q8_decode_split_len(p, sm_count(dev));
+    p.nsplit = p.K > 0 ? (int)(((long long)p.K + p.split_len - 1) / p.split_len) : 1;
+    void *ws = nullptr;
+    if (p.nsplit > 1) {
+        const size_t bytes = (size_t)split_workspace_bytes(p);
+        cudaMemPool_t pool = nullptr;
+        rc = pool_for(dev, &pool);
+        if (rc) return rc;
+        const cudaError_t e = cudaMallocFromPoolAsync(&ws, bytes, pool, stream);
+        if (e != cudaSuccess) {
+            set_error("workspace cudaMallocFromPoolAsync(%zu): %s", bytes, cudaGetErrorString(e));
+            return ATTN_ERR_CUDA;
+        }
+        set_split_workspace(p, ws);
+    }
+    rc = launch_q8_decode(p, c, dtype, stream);
+    if (rc == 0 && p.nsplit > 1) rc = launch_combine_rows(p, dtype, stream);
+    if (ws != nullptr) {
+        const cudaError_t e = cudaFreeAsync(ws, stream);
+        if (e != cudaSuccess && rc == 0) {
+            set_error("workspace cudaFreeAsync: %s", cudaGetErrorString(e));
+            rc = ATTN_ERR_CUDA;
+        }
+    }
+    return rc;
+}
+
 int validate_pools(const void *const *src, void *const *dst, const long long *bytes, int n,
                    const char *what) {
     if (n < 0 || (n > 0 && (src == nullptr || dst == nullptr || bytes == nullptr))) {
@@ -298,6 +332,16 @@ int attn_fwd_paged_q8(const void *q, const void *k_pages, const void *v_pages,
     c.code = cache_dtype;
     c.nblk = page_size / block_size;
     c.blk_shift = log2_of(block_size);
+    // few rows read the codes; ATTN_ALGO_DECODE is that kernel, the others' names
+    // choose among the kernels that read the expanded rows
+    const bool decode = q8_decode_supported(p, dtype);
+    if (algo == ATTN_ALGO_DECODE && !decode) {
+        set_error("the 8-bit decode kernel takes bf16/fp16, Q * Hq / Hkv <= 16, D and Dv multiples of "
+                  "16 up to 256 and pages of 8 rows or more");
+        return ATTN_ERR_UNSUPPORTED;
+    }
+    if (decode && (algo == ATTN_ALGO_AUTO || algo == ATTN_ALGO_DECODE))
+        return run_decode(p, c, dtype, reinterpret_cast<cudaStream_t>(stream));
     return run_expanded(p, c, dtype, algo, reinterpret_cast<cudaStream_t>(stream));
 }
 

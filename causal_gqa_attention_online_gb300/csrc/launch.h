@@ -4,6 +4,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -79,6 +80,8 @@ int launch_prefill_wide512_tc(const AttnParams &p, int dtype, cudaStream_t strea
 bool fwd_mma_supported(const AttnParams &p, int dtype);
 int launch_fwd_mma(const AttnParams &p, int dtype, cudaStream_t stream);
 
+// The driver's cuTensorMapEncodeTiled, or null.
+PFN_cuTensorMapEncodeTiled_v12000 tma_encode_fn();
 // 4-D TMA map over 16-bit elements [d3][d2][d1][d0] (d0 innermost), box
 // {64, b1, b2, 1}, 128-byte swizzle; returns 0 or an attn_status code.
 int make_tma_map_4d(CUtensorMap *map, const void *ptr, bool bf16, uint64_t d0, uint64_t d1,
@@ -119,6 +122,12 @@ int launch_cache_append(const void *k, const void *v, void *k_pages, void *v_pag
 // dtype (p.B <= 65535).
 int launch_q8_expand(const AttnParams &p, const Q8Cache &c, void *k_out, void *v_out, int dtype,
                      cudaStream_t stream);
+
+// Split-KV decode that reads the codes themselves (bf16/fp16, Q * G <= 16, widths
+// multiples of 16 up to 256, pages of 8 rows or more).  Honours p.nsplit.
+bool q8_decode_supported(const AttnParams &p, int dtype);
+int q8_decode_split_len(const AttnParams &p, int nsm);
+int launch_q8_decode(const AttnParams &p, const Q8Cache &c, int dtype, cudaStream_t stream);
 
 constexpr int kMaxPools = 64;  // pools one launch copies
 int launch_pages_copy(const void *const *src_pools, void *const *dst_pools, const long long *bytes,

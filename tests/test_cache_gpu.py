@@ -74,6 +74,20 @@ class Cache:
         scales = [torch.from_numpy(s.copy()).to(DEV) for s in self.scales]
         return pages[0], pages[1], scales[0], scales[1]
 
+    def finest(self, K):
+        """[B, H, D]: 2^-39 of the sequence's largest value scale times its codes'
+        magnitudes -- half a step of the decode kernel's smallest probabilities
+        (fp16 steps of 2^-24 under 2^14 at the row's largest, relative to the
+        largest scale), added up over the keys."""
+        ones = np.ones_like(self.scales[1])
+        c = cache_ref.gather(np.abs(cache_ref.as_values(self.codes[1], ones, self.kind)), self.table,
+                             self.lens, K)
+        B, _, H, _ = c.shape
+        nb = self.scales[1].shape[1]
+        s = np.nan_to_num(self.scales[1]).repeat(self.page // nb, axis=1)
+        s = cache_ref.gather(s[..., None], self.table, self.lens, K).max(1)
+        return 2.0 ** -39 * c.sum(1) * s
+
     def dense(self, K):
         """[B, K, H, D] float32 values (exact for powers of two) of the valid keys."""
         out = []
@@ -83,7 +97,7 @@ class Cache:
         return out
 
 
-def attention_bounds(q, k, v, B, Hq, Hkv, Q, K, D, Dv, lens, sq, window, scale, mask, dtype):
+def attention_bounds(q, k, v, B, Hq, Hkv, Q, K, D, Dv, lens, sq, window, scale, mask, dtype, finest=0):
     """Oracle outputs and how far the kernels may be from them.
 
     With A = sum p |v| of a row: a score's fp32 accumulation is off by at most
@@ -92,7 +106,8 @@ def attention_bounds(q, k, v, B, Hq, Hkv, Q, K, D, Dv, lens, sq, window, scale, 
     K 2^-24 each, ex2 by 2^-22; p is rounded to q's type (or finer) for the
     second product, O once at the end.  Below 2^-14 an fp16 p (at most 1 at the
     row's largest score, so that sum p >= 1) has steps of 2^-24: off by 2^-25,
-    which times |v| adds up over the keys."""
+    which times |v| adds up over the keys; the decode kernel's probabilities reach
+    further down (``finest``)."""
     kw = dict(B=B, Hq=Hq, Hkv=Hkv, Q=Q, K=K, D=D, Dv=Dv, seqlens_q=sq, seqlens_k=lens,
               window=window, scale=scale, mask=mask)
     f = lambda x: np.ascontiguousarray(x, np.float32)  # noqa: E731
@@ -111,6 +126,8 @@ def attention_bounds(q, k, v, B, Hq, Hkv, Q, K, D, Dv, lens, sq, window, scale, 
     tol_o = half * np.abs(o) + (half + rel[..., None]) * a + 1e-30
     if dtype == "f16":  # subnormal outputs and probabilities
         tol_o = tol_o + 2.0 ** -25 * (1 + np.abs(v).sum(1).repeat(G, axis=1)[:, None])
+    if not np.isscalar(finest):
+        tol_o = tol_o + finest.repeat(G, axis=1)[:, None]
     tol_l = ds + K * 2.0 ** -24 + 2.0 ** -20 + 2.0 ** -22 * np.abs(np.where(np.isfinite(lse), lse, 0))
     return o, lse, tol_o, tol_l
 
@@ -134,7 +151,7 @@ def check_attention(g, dtype, kind, B, Hq, Hkv, Q, D, Dv, lens, page, block, *, 
     ro, rl, to, tl = attention_bounds(
         q.float().numpy().astype(np.float64), kd, vd, B, Hq, Hkv, Q, K, D, Dv, c.lens,
         None if sq is None else np.asarray(sq, np.int32), window, scale,
-        {"causal": 0, "causal_top_left": 1, "none": 2}[mask], dtype)
+        {"causal": 0, "causal_top_left": 1, "none": 2}[mask], dtype, c.finest(K))
     o, lse = o.float().cpu().numpy(), lse.cpu().numpy()
     empty = rl == -math.inf
     assert np.all(o[empty] == 0) and not np.signbit(o[empty]).any() and np.all(lse[empty] == -math.inf)
@@ -187,10 +204,29 @@ def test_attention_over_the_cache(i):
                     lens, page, block, **kw)
 
 
-@pytest.mark.parametrize("algo", ["generic", "tcgen05", "mma"])
+@pytest.mark.parametrize("algo", ["generic", "tcgen05", "mma", "decode"])
 def test_attention_with_a_chosen_kernel(algo):
     check_attention(np.random.default_rng(7), "bf16", "int8", 2, 8, 2, 3, 128, 128, [300, 41], 64,
                     16, algo=algo)
+
+
+def test_attention_ignores_scales_of_pages_behind_the_window():
+    # a page that every row's window has left may be anyone's: its scales (finite
+    # and huge, or NaN) take no part
+    g = np.random.default_rng(8)
+    for bad in (1e30, math.nan):
+        c = Cache(g, [200, 120], 64, 64, 2, 128, 128, "int8")
+        for b, n in enumerate((200, 120)):
+            for s in c.scales:  # keys up to n - 41 are outside
+                s[c.table[b, (n - 40) // 64 - 1]] = 2.0 ** -5
+        q = torch.from_numpy(g.standard_normal((2, 1, 8, 128)).astype(np.float32)).bfloat16().to(DEV)
+        kp, vp, ks, vs = c.gpu()
+        good = attn.attn_fwd_paged_q8(q, kp, vp, ks, vs, i32(c.table), i32(c.lens), window=40)
+        for b, n in enumerate((200, 120)):
+            for s in (ks, vs):
+                s[int(c.table[b, (n - 40) // 64 - 1])] = bad
+        got = attn.attn_fwd_paged_q8(q, kp, vp, ks, vs, i32(c.table), i32(c.lens), window=40)
+        assert torch.equal(got[0], good[0]) and torch.equal(got[1], good[1])
 
 
 def test_attention_without_pages():

@@ -110,6 +110,13 @@ def test_attention_refuses(lib, kw, needle):
     assert needle in lib.attn_last_error().decode()
 
 
+@pytest.mark.parametrize("kw", [dict(D=40), dict(Dv=8), dict(D=272, Dv=272), dict(page=4, block=4),
+                                dict(Q=9), dict(dtype=0)])
+def test_decode_kernel_refuses_what_it_does_not_take(lib, kw):
+    assert _fwd(lib, algo=3, **kw) == 2
+    assert "8-bit decode kernel" in lib.attn_last_error().decode()
+
+
 def test_attention_of_nothing_is_a_noop(lib):
     assert _fwd(lib, B=0, q=0, o=0, table=0, lens=0) == 0
     assert _fwd(lib, Q=0, q=0, o=0, table=0, lens=0) == 0
