@@ -88,6 +88,29 @@ int append_common(const void *k, const void *v, void *k_pages, void *v_pages, fl
                                log2_of(block_size), cache_dtype, dtype, stream);
 }
 
+// f's launches with a workspace from the library's pool.
+template <typename F> int with_workspace(unsigned long long bytes, cudaStream_t stream, F f) {
+    int dev = 0;
+    int rc = current_device(&dev);
+    if (rc) return rc;
+    cudaMemPool_t pool = nullptr;
+    rc = pool_for(dev, &pool);
+    if (rc) return rc;
+    void *ws = nullptr;
+    cudaError_t e = cudaMallocFromPoolAsync(&ws, (size_t)bytes, pool, stream);
+    if (e != cudaSuccess) {
+        set_error("workspace cudaMallocFromPoolAsync(%llu): %s", bytes, cudaGetErrorString(e));
+        return ATTN_ERR_CUDA;
+    }
+    rc = f(ws);
+    e = cudaFreeAsync(ws, stream);
+    if (e != cudaSuccess && rc == 0) {
+        set_error("workspace cudaFreeAsync: %s", cudaGetErrorString(e));
+        rc = ATTN_ERR_CUDA;
+    }
+    return rc;
+}
+
 // Bytes of expanded keys and values that one group of sequences may take: the
 // rows stay in the L2 cache between the expansion and the kernel that reads
 // them (a longer sequence than this is a group of its own).
@@ -150,40 +173,6 @@ int run_expanded(const AttnParams &p, const Q8Cache &c, int dtype, int algo, cud
     return rc;
 }
 
-// Split-KV decode over the codes, with its partials in the library's pool.
-int run_decode(AttnParams &p, const Q8Cache &c, int dtype, cudaStream_t stream) {
-    int dev = 0;
-    int rc = current_device(&dev);
-    if (rc) return rc;
-    rc = status_ptr(dev, &p.status);
-    if (rc) return rc;
-    p.split_len = q8_decode_split_len(p, sm_count(dev));
-    p.nsplit = p.K > 0 ? (int)(((long long)p.K + p.split_len - 1) / p.split_len) : 1;
-    void *ws = nullptr;
-    if (p.nsplit > 1) {
-        const size_t bytes = (size_t)split_workspace_bytes(p);
-        cudaMemPool_t pool = nullptr;
-        rc = pool_for(dev, &pool);
-        if (rc) return rc;
-        const cudaError_t e = cudaMallocFromPoolAsync(&ws, bytes, pool, stream);
-        if (e != cudaSuccess) {
-            set_error("workspace cudaMallocFromPoolAsync(%zu): %s", bytes, cudaGetErrorString(e));
-            return ATTN_ERR_CUDA;
-        }
-        set_split_workspace(p, ws);
-    }
-    rc = launch_q8_decode(p, c, dtype, stream);
-    if (rc == 0 && p.nsplit > 1) rc = launch_combine_rows(p, dtype, stream);
-    if (ws != nullptr) {
-        const cudaError_t e = cudaFreeAsync(ws, stream);
-        if (e != cudaSuccess && rc == 0) {
-            set_error("workspace cudaFreeAsync: %s", cudaGetErrorString(e));
-            rc = ATTN_ERR_CUDA;
-        }
-    }
-    return rc;
-}
-
 int validate_pools(const void *const *src, void *const *dst, const long long *bytes, int n,
                    const char *what) {
     if (n < 0 || (n > 0 && (src == nullptr || dst == nullptr || bytes == nullptr))) {
@@ -201,29 +190,6 @@ int validate_pools(const void *const *src, void *const *dst, const long long *by
         }
     }
     return ATTN_OK;
-}
-
-// A plan's launches with its workspace from the library's pool.
-template <typename F> int with_workspace(unsigned long long bytes, cudaStream_t stream, F f) {
-    int dev = 0;
-    int rc = current_device(&dev);
-    if (rc) return rc;
-    cudaMemPool_t pool = nullptr;
-    rc = pool_for(dev, &pool);
-    if (rc) return rc;
-    void *ws = nullptr;
-    cudaError_t e = cudaMallocFromPoolAsync(&ws, (size_t)bytes, pool, stream);
-    if (e != cudaSuccess) {
-        set_error("workspace cudaMallocFromPoolAsync(%llu): %s", bytes, cudaGetErrorString(e));
-        return ATTN_ERR_CUDA;
-    }
-    rc = f(ws);
-    e = cudaFreeAsync(ws, stream);
-    if (e != cudaSuccess && rc == 0) {
-        set_error("workspace cudaFreeAsync: %s", cudaGetErrorString(e));
-        rc = ATTN_ERR_CUDA;
-    }
-    return rc;
 }
 
 }  // namespace
@@ -340,8 +306,17 @@ int attn_fwd_paged_q8(const void *q, const void *k_pages, const void *v_pages,
                   "16 up to 256 and pages of 8 rows or more");
         return ATTN_ERR_UNSUPPORTED;
     }
-    if (decode && (algo == ATTN_ALGO_AUTO || algo == ATTN_ALGO_DECODE))
-        return run_decode(p, c, dtype, reinterpret_cast<cudaStream_t>(stream));
+    int dev = 0;
+    rc = current_device(&dev);
+    if (rc == 0) rc = status_ptr(dev, &p.status);
+    if (rc) return rc;
+    if (decode && (algo == ATTN_ALGO_AUTO || algo == ATTN_ALGO_DECODE)) {
+        const int nsm = sm_count(dev);
+        return with_workspace(q8_decode_workspace(p, nsm), reinterpret_cast<cudaStream_t>(stream),
+                              [&](void *ws) {
+            return launch_q8_decode(p, c, dtype, nsm, ws, reinterpret_cast<cudaStream_t>(stream));
+        });
+    }
     return run_expanded(p, c, dtype, algo, reinterpret_cast<cudaStream_t>(stream));
 }
 

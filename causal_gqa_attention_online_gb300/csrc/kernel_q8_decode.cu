@@ -32,6 +32,17 @@
 // all completing on the stage's mbarrier; consumers free a stage with one
 // arrival a warp, so no warp waits for another within a tile.  V rows past the
 // last key need no zeroing: any byte is a finite f16 here, and its p is 0.
+//
+// Work: the 128-key tiles of all sequences, in order, are cut into equal shares
+// whatever the lengths, and a CTA takes one share for one KV head -- as many
+// shares as give every resident CTA one, so that the heads of a page are read at
+// the same time (with the heads one after the other, the 256-byte reads of
+// 128-byte head rows brought in 719 MB for 547).  The producer runs from one
+// sequence into the next without draining the ring.  A sequence that lies in one
+// share is written out by its CTA; shares that begin or end inside one leave a
+// partial each (at most two a CTA, so the workspace does not grow with the
+// keys), and the merge kernel, a block for each place where a share begins
+// inside a sequence, head and row, joins those.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -57,15 +68,29 @@ struct Q8Args {
     int box_rows;  // rows of a TMA box: min(page_size, 64)
     int box_shift;
     bool bf16;
+    int shares;    // shares at most (no more than there are tiles are used)
+    // workspace: for each share {sequence, its first share, its last} where the
+    // merge of a sequence is found (its second share; {-1} elsewhere), partials
+    // [CTA][2][R] of normalised rows and log2 sums
+    int4 *seam;
+    float *part_o, *part_lse;
 };
 
-template <int DP> struct Ring {
+template <int DP, int NT> struct Ring {
     static constexpr int HALF = DP > 128 ? 128 : DP;  // bytes of a box row
     static constexpr int TILE = kTile * DP;
     static constexpr int STAGE = 2 * TILE + 2 * kTile * 4;
     static constexpr int NS = DP == 64 ? 5 : 3;
-    static constexpr int BARS = NS * STAGE;
-    static constexpr int SMEM = BARS + 16 * NS + 16;
+    // the warps' O are merged MC columns at a time through two warps' buffers
+    static constexpr int R = NT * 8;
+    static constexpr int MC = DP == 64 ? 64 : DP / NT;
+    static constexpr int PITCH = MC + 4;
+    static constexpr int MERGE = NS * STAGE;
+    static constexpr int STATS = MERGE + 2 * R * PITCH * 4;  // m, l [4][R], u [4]
+    static constexpr int BARS = STATS + (2 * 4 * R + 4) * 4;
+    static constexpr int SHARE = BARS + 16 * NS;  // {left, sequence, tile}, abort flag
+    static constexpr int SMEM = SHARE + 32;
+    static_assert(SMEM <= (DP > 128 ? 227 : 113) * 1024, "one or two CTAs an SM");
 };
 
 // Byte offset of 16-byte chunk c of row r: rows of 64 bytes in the 64-byte
@@ -79,125 +104,222 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
 }
 
+// The keys some row of sequence b attends to, [lo, hi), from a multiple of the
+// box on, so that a box is one page's; and how many tiles they take.
+struct UnitKeys {
+    SeqInfo si;
+    int klo, kbeg, kend, ntiles;
+};
+__device__ __forceinline__ UnitKeys unit_of(const Q8Args &a, int b) {
+    UnitKeys u;
+    u.si = seq_info(a.p, b);
+    unit_keys(u.si.Qb, u.si.Kb, a.p.window, a.p.mask, u.klo, u.kend);
+    u.kbeg = u.klo & ~(a.box_rows - 1);
+    u.ntiles = (int)(((long long)u.kend - u.kbeg + kTile - 1) / kTile);
+    return u;
+}
+
+// The first tile of share i of n <= T (so that no share is empty), and the share
+// of tile t.
+__device__ __forceinline__ long long share_begin(long long i, long long T, long long n) {
+    return i * T / n;
+}
+__device__ __forceinline__ long long share_at(long long t, long long T, long long n) {
+    return ((t + 1) * n - 1) / T;
+}
+
 template <int CODE, int DP, int NT>
 __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
     q8_decode_kernel(const __grid_constant__ Q8Args a, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV) {
     using Op = CodeOps<CODE>;
-    using L = Ring<DP>;
+    using L = Ring<DP, NT>;
     constexpr int NS = L::NS;
-    constexpr int R = NT * 8;
-    constexpr int OPITCH = DP + 4;
-    static_assert(4 * R * OPITCH * 4 + 3 * 4 * R * 4 <= NS * L::STAGE, "merge buffer");
+    constexpr int R = L::R;
     extern __shared__ __align__(1024) uint8_t smem[];
     const AttnParams &p = a.p;
-
-    const int split = blockIdx.x;
-    const int b = blockIdx.y / p.Hkv, kvh = blockIdx.y % p.Hkv;
-    const SeqInfo si = seq_info(p, b);
-    const int G = p.G;
-    const int nrows = p.Q * G;  // rows this unit writes (<= R)
-    const int nvalid = si.Qb * G;
-
-    // Block-uniform: key range of this split and whether it owns any row.
-    int lo_min = INT_MAX, hi_max = 0;
-    bool mine = false;
-    for (int qi = 0; qi < p.Q; ++qi) {
-        int lo = 0, hi = 0;
-        if (qi < si.Qb) legal_range(qi, si.Qb, si.Kb, p.window, p.mask, lo, hi);
-        const SplitSpan sp = split_span(lo, hi, p.split_len);
-        if (sp.direct ? sp.first == split : (split >= sp.first && split <= sp.last)) mine = true;
-        if (hi > lo) {
-            lo_min = min(lo_min, lo);
-            hi_max = max(hi_max, hi);
-        }
-    }
-    // let the combine grid (a programmatic dependent launch) be scheduled
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-    if (!mine) return;
-    // tiles start on a multiple of the box, so that a box is one page's
-    // (a unit without keys has no tile: lo_min is still INT_MAX there)
-    const int klo = hi_max > 0 ? max(lo_min, split * p.split_len) : 0;
-    const int kbeg = klo & ~(a.box_rows - 1);
-    const int kend = (int)min((long long)hi_max, (split + 1LL) * p.split_len);
-    const int ntiles = kend > kbeg ? (kend - kbeg + kTile - 1) / kTile : 0;
-
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, tig = lane & 3;
+    const int share_i = blockIdx.x / p.Hkv, kvh = blockIdx.x - share_i * p.Hkv;
     const uint32_t sbase = smem_u32(smem);
     const uint32_t full = sbase + L::BARS, empty = full + 8 * NS;
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::BARS + 16 * NS);
-    if (tid == 0) {
-        for (int s = 0; s < NS; ++s) {
-            sm100::mbar_init(full + 8 * s, 33);  // the bytes, and each producer lane's scales
-            sm100::mbar_init(empty + 8 * s, 4);
+    long long *share = reinterpret_cast<long long *>(smem + L::SHARE);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(share + 3);
+
+    // let the merge grid (a programmatic dependent launch) be scheduled
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    if (warp == 4) {
+        if (lane == 0) {
+            for (int s = 0; s < NS; ++s) {
+                sm100::mbar_init(full + 8 * s, 33);  // the bytes, and each producer lane's scales
+                sm100::mbar_init(empty + 8 * s, 4);
+            }
+            *abort_flag = 0;
+            sm100::fence_mbar_init();
+            sm100::tma_prefetch_desc(&tmK);
+            sm100::tma_prefetch_desc(&tmV);
         }
-        *abort_flag = 0;
-        sm100::fence_mbar_init();
+        // this CTA's share of the tiles of all sequences, and where it begins
+        long long T = 0;
+        int n0 = 0;  // of the first 32 sequences
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            const int n = b0 + lane < p.B ? unit_of(a, b0 + lane).ntiles : 0;
+            if (b0 == 0) n0 = n;
+            T += __reduce_add_sync(0xffffffffu, (unsigned)n);
+        }
+        const long long shares = min((long long)a.shares, T);
+        long long t0 = 0, left = 0;
+        if (share_i < shares) {
+            t0 = share_begin(share_i, T, shares);
+            left = share_begin(share_i + 1, T, shares) - t0;
+        }
+        long long before = 0;
+        bool found = left == 0;
+        for (int b0 = 0; !found && b0 < p.B; b0 += 32) {
+            const int n = b0 == 0 ? n0 : b0 + lane < p.B ? unit_of(a, b0 + lane).ntiles : 0;
+            int incl = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            const long long first = before + incl - n;
+            const bool here = t0 >= first && t0 < first + n;
+            if (here) {
+                share[1] = b0 + lane;
+                share[2] = t0 - first;
+                if (kvh == 0) {
+                    // where the sequence's first seam is this share's beginning
+                    int4 v = make_int4(-1, 0, 0, 0);
+                    const int c0 = (int)share_at(first, T, shares);
+                    if (t0 > first && c0 == share_i - 1)
+                        v = make_int4(b0 + lane, c0, (int)share_at(first + n - 1, T, shares),
+                                      share_begin(c0, T, shares) < first ? 1 : 0);
+                    a.seam[share_i] = v;
+                }
+            }
+            found = __any_sync(0xffffffffu, here);
+            before += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (lane == 0) {
+            share[0] = left;
+            if (left == 0 && kvh == 0) a.seam[share_i] = make_int4(-1, 0, 0, 0);
+        }
+    } else {
+        // meanwhile: the rows of sequences without keys, +0 and -inf (each lane
+        // looks at one of the CTA's sequences and heads, the warp writes)
+        const long long units = (long long)p.B * p.Hkv;
+        for (long long x0 = blockIdx.x + (long long)warp * 32 * gridDim.x; x0 < units; x0 += 128LL * gridDim.x) {
+            const long long x = x0 + (long long)lane * gridDim.x;
+            unsigned todo = __ballot_sync(0xffffffffu, x < units && unit_of(a, (int)(x / p.Hkv)).ntiles == 0);
+            for (; todo; todo &= todo - 1) {
+                const long long y = x0 + (long long)(__ffs(todo) - 1) * gridDim.x;
+                const int b = (int)(y / p.Hkv), h0 = (int)(y - (long long)b * p.Hkv) * p.G, c8 = p.Dv / 8;
+                for (int i = lane; i < p.Q * p.G * c8; i += 32) {
+                    const int row = i / c8, c = i - row * c8;
+                    const long long orow = ((long long)b * p.Q + row / p.G) * p.Hq + h0 + row % p.G;
+                    reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.o) + orow * p.Dv)[c] = make_uint4(0, 0, 0, 0);
+                    if (c == 0 && p.lse) p.lse[orow] = -INFINITY;
+                }
+            }
+        }
     }
     __syncthreads();
-
-    float m[NT][2], l[NT][2], u = 0.f;
-    float oacc[DP / 16][NT][4];
+    long long left = share[0];
+    if (left == 0) return;
+    int b = (int)share[1], tile = (int)share[2];
+    UnitKeys un = unit_of(a, b);
+    // the next sequence that has tiles
+    auto advance = [&]() {
+        tile = 0;
+        do {
+            ++b;
+            un = unit_of(a, b);
+        } while (un.ntiles == 0);
+    };
 
     if (warp == 4) {
         // ------------------------------------------------------------ producer
         const int nblk = a.c.nblk, nbox = kTile >> a.box_shift;
         const int pmask = p.page_size - 1;
-        const int32_t *table = p.block_table + (long long)b * p.max_pages;
-        auto page_of = [&](int t) -> int {  // lane i: the page of box i of tile t
-            const unsigned key = (unsigned)(kbeg + t * kTile) + ((unsigned)lane << a.box_shift);
-            int pg = 0;
-            if (t < ntiles && lane < nbox && key < (unsigned)kend) pg = __ldg(table + (key >> p.page_shift));
-            return min(max(pg, 0), p.num_pages - 1);
-        };
-        int pg_next = page_of(0);
-        int t = 0;
-        for (; t < ntiles; ++t) {
-            const int s = t % NS;
-            const uint32_t fb = full + 8 * s, st = sbase + s * L::STAGE;
-            const int pg = pg_next;
-            pg_next = page_of(t + 1);
-            if (t >= NS) {
-                const bool got = sm100::mbar_wait(empty + 8 * s, (uint32_t)(t / NS - 1) & 1u, abort_flag,
-                                                  p.wait_ns);
-                if (!__all_sync(0xffffffffu, got)) break;
-            }
-            const int key0 = kbeg + t * kTile;
-            const int boxes = min(nbox, (kend - key0 + a.box_rows - 1) >> a.box_shift);
-            if (lane == 0)
-                sm100::mbar_arrive_expect_tx(fb, (uint32_t)boxes * a.box_rows * DP * 2);
-            __syncwarp();
-            if (lane < boxes) {
-                const int row = (pg << p.page_shift) + ((key0 + (lane << a.box_shift)) & pmask);
-                const uint32_t at = st + (lane << a.box_shift) * L::HALF;
-#pragma unroll
-                for (int h = 0; h < DP / L::HALF; ++h) {
-                    sm100::tma_load_4d(at + h * kTile * 128, &tmK, fb, h * 128, kvh, row, 0);
-                    sm100::tma_load_4d(at + L::TILE + h * kTile * 128, &tmV, fb, h * 128, kvh, row, 0);
+        uint32_t it = 0;  // tiles issued by this CTA
+        bool ok = true;
+        while (left > 0 && ok) {
+            const int n = (int)min((long long)(un.ntiles - tile), left);
+            const int32_t *table = p.block_table + (long long)b * p.max_pages;
+            auto page_of = [&](int t) -> int {  // lane i: the page of box i of tile t
+                const unsigned key = (unsigned)(un.kbeg + t * kTile) + ((unsigned)lane << a.box_shift);
+                int pg = 0;
+                if (t < un.ntiles && lane < nbox && key < (unsigned)un.kend)
+                    pg = __ldg(table + (key >> p.page_shift));
+                return min(max(pg, 0), p.num_pages - 1);
+            };
+            int pg_next = page_of(tile);
+            for (int t = tile; t < tile + n; ++t, ++it) {
+                const uint32_t s = it % NS;
+                const uint32_t fb = full + 8 * s, st = sbase + s * L::STAGE;
+                const int pg = pg_next;
+                pg_next = page_of(t + 1);
+                if (it >= (uint32_t)NS) {
+                    const bool got = sm100::mbar_wait(empty + 8 * s, (it / NS - 1) & 1u, abort_flag, p.wait_ns);
+                    if (!__all_sync(0xffffffffu, got)) {
+                        ok = false;
+                        break;
+                    }
                 }
-            }
+                const int key0 = un.kbeg + t * kTile;
+                const int boxes = min(nbox, (un.kend - key0 + a.box_rows - 1) >> a.box_shift);
+                if (lane == 0)
+                    sm100::mbar_arrive_expect_tx(fb, (uint32_t)boxes * a.box_rows * DP * 2);
+                __syncwarp();
+                if (lane < boxes) {
+                    const int row = (pg << p.page_shift) + ((key0 + (lane << a.box_shift)) & pmask);
+                    const uint32_t at = st + (lane << a.box_shift) * L::HALF;
 #pragma unroll
-            for (int j = 0; j < kTile / 32; ++j) {
-                const int i = lane + 32 * j, key = key0 + i;
-                const int pk = __shfl_sync(0xffffffffu, pg, i >> a.box_shift);
-                const bool ok = (unsigned)key < (unsigned)kend;
-                const long long at = ok ? ((long long)pk * nblk + ((key & pmask) >> a.c.blk_shift)) * p.Hkv + kvh : 0;
-                cp_async4(st + 2 * L::TILE + 4 * i, a.c.ks + at, ok ? 4 : 0);
-                cp_async4(st + 2 * L::TILE + 4 * (kTile + i), a.c.vs + at, ok ? 4 : 0);
+                    for (int h = 0; h < DP / L::HALF; ++h) {
+                        sm100::tma_load_4d(at + h * kTile * 128, &tmK, fb, h * 128, kvh, row, 0);
+                        sm100::tma_load_4d(at + L::TILE + h * kTile * 128, &tmV, fb, h * 128, kvh, row, 0);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kTile / 32; ++j) {
+                    const int i = lane + 32 * j;
+                    const unsigned key = (unsigned)key0 + i;
+                    const int pk = __shfl_sync(0xffffffffu, pg, i >> a.box_shift);
+                    const bool in = key < (unsigned)un.kend;
+                    const long long at =
+                        in ? ((long long)pk * nblk + ((key & pmask) >> a.c.blk_shift)) * p.Hkv + kvh : 0;
+                    cp_async4(st + 2 * L::TILE + 4 * i, a.c.ks + at, in ? 4 : 0);
+                    cp_async4(st + 2 * L::TILE + 4 * (kTile + i), a.c.vs + at, in ? 4 : 0);
+                }
+                cp_async_arrive(fb);
             }
-            cp_async_arrive(fb);
+            left -= n;
+            if (left > 0 && ok) advance();
         }
-        if (t < ntiles && lane == 0) {  // a wait ran out
+        if (!ok && lane == 0) {  // a wait ran out
             *abort_flag = 1;
             report_status(p.status, kStatusTimeoutDecode);
         }
-        // every copy issued lands before the block goes on, also after an abort
+        // every copy issued lands before the block exits, also after an abort
         cp_async_wait<0>();
-        for (int k = max(0, t - NS); k < t; ++k)
-            sm100::mbar_wait_drain(full + 8 * (k % NS), (uint32_t)(k / NS) & 1u);
-    } else {
-        // ----------------------------------------------------------- consumers
+        for (uint32_t k = it > (uint32_t)NS ? it - NS : 0; k < it; ++k)
+            sm100::mbar_wait_drain(full + 8 * (k % NS), (k / NS) & 1u);
+        return;
+    }
+
+    // --------------------------------------------------------------- consumers
+    const int G = p.G;
+    const int nrows = p.Q * G;  // rows of a unit (<= R)
+    const int kw0 = warp * 32;
+    float *stat_m = reinterpret_cast<float *>(smem + L::STATS), *stat_l = stat_m + 4 * R;
+    float *stat_u = stat_l + 4 * R;
+    float *mbuf = reinterpret_cast<float *>(smem + L::MERGE);
+    uint32_t it = 0;
+    bool ok = true;
+    for (bool first_seg = true; left > 0; first_seg = false) {
+        const int n = (int)min((long long)(un.ntiles - tile), left);
+        const int nvalid = un.si.Qb * G;
         // Q^T fragments (B operand of S^T): column n = row g; in each 16 columns
         // lane tig holds columns 4 tig + {0, 2} and 4 tig + {1, 3}, as the codes'
         // even and odd bytes pair.
@@ -208,19 +330,15 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
             const int row = nt * 8 + g;
             float amax = 0.f;
             uint2 raw[DP / 16];
+#pragma unroll
+            for (int kk = 0; kk < DP / 16; ++kk) raw[kk] = make_uint2(0, 0);
             if (row < nvalid) {
                 const int qi = row / G, h = kvh * G + row % G;
-                const long long at = ((si.q_off + qi) * p.Hq + h) * (long long)p.D;
+                const uint16_t *src = static_cast<const uint16_t *>(p.q) +
+                                      ((un.si.q_off + qi) * p.Hq + h) * (long long)p.D + 4 * tig;
 #pragma unroll
-                for (int kk = 0; kk < DP / 16; ++kk) {
-                    raw[kk] = make_uint2(0, 0);
-                    if (kk * 16 < p.D)
-                        raw[kk] = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.q) +
-                                                                        at + kk * 16 + 4 * tig));
-                }
-            } else {
-#pragma unroll
-                for (int kk = 0; kk < DP / 16; ++kk) raw[kk] = make_uint2(0, 0);
+                for (int kk = 0; kk < DP / 16; ++kk)
+                    if (kk * 16 < p.D) raw[kk] = __ldg(reinterpret_cast<const uint2 *>(src + kk * 16));
             }
             auto val = [&](int kk, int j) -> float {
                 const uint32_t w = j < 2 ? raw[kk].x : raw[kk].y;
@@ -236,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
             // 2^ea <= amax < 2^(ea + 1); the row is multiplied by 2^(14 - ea)
             const int ea = max((int)(__float_as_uint(amax) >> 23) - 127, -112);
             const float up = __uint_as_float((uint32_t)(127 + 14 - ea) << 23);
-            const float f = p.scale_log2 * Op::kUnit * __uint_as_float((uint32_t)(max(127 + ea - 14, 1)) << 23);
+            const float f = p.scale_log2 * Op::kUnit * __uint_as_float((uint32_t)max(127 + ea - 14, 1) << 23);
 #pragma unroll
             for (int kk = 0; kk < DP / 16; ++kk) {
                 qf[kk][nt][0] = MmaOp<__half>::pack(val(kk, 0) * up, val(kk, 2) * up);
@@ -247,15 +365,17 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
         }
         // Legal keys of the two rows (per n-tile) this thread's columns hold.
         int rlo[NT][2], rhi[NT][2];
+        float m[NT][2], l[NT][2], u = 0.f;
+        float oacc[DP / 16][NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int row = nt * 8 + 2 * tig + e;
                 int lo = 0, hi = 0;
-                if (row < nvalid) legal_range(row / G, si.Qb, si.Kb, p.window, p.mask, lo, hi);
-                rlo[nt][e] = max(lo, split * p.split_len);
-                rhi[nt][e] = min(hi, kend);
+                if (row < nvalid) legal_range(row / G, un.si.Qb, un.si.Kb, p.window, p.mask, lo, hi);
+                rlo[nt][e] = lo;
+                rhi[nt][e] = hi;
                 m[nt][e] = -INFINITY;
                 l[nt][e] = 0.f;
             }
@@ -266,19 +386,19 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) oacc[mt][nt][j] = 0.f;
 
-        const int kw0 = warp * 32;
-        for (int t = 0; t < ntiles; ++t) {
-            const int s = t % NS;
-            const bool got = sm100::mbar_wait(full + 8 * s, (uint32_t)(t / NS) & 1u, abort_flag, p.wait_ns);
+        for (int t = tile; t < tile + n && ok; ++t, ++it) {
+            const uint32_t s = it % NS;
+            const bool got = sm100::mbar_wait(full + 8 * s, (it / NS) & 1u, abort_flag, p.wait_ns);
             if (!__all_sync(0xffffffffu, got)) {
                 if (lane == 0) {
                     *abort_flag = 1;
                     report_status(p.status, kStatusTimeoutDecode);
                 }
+                ok = false;
                 break;
             }
-            const int key0 = kbeg + t * kTile + kw0;
-            if (key0 < kend) {
+            const int key0 = un.kbeg + t * kTile + kw0;
+            if (key0 < un.kend) {
                 const uint32_t ks = sbase + s * L::STAGE, vs = ks + L::TILE;
                 const float *sc = reinterpret_cast<const float *>(smem + s * L::STAGE + 2 * L::TILE) + kw0;
 
@@ -309,12 +429,12 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
 
                 // the largest finite value scale so far, of keys some row attends to
                 const int uk = key0 + lane;
-                uint32_t ub = uk >= klo && uk < kend ? __float_as_uint(sc[kTile + lane]) & 0x7fffffffu : 0u;
+                uint32_t ub = uk >= un.klo && uk < un.kend ? __float_as_uint(sc[kTile + lane]) & 0x7fffffffu : 0u;
                 if (ub >= 0x7f800000u) ub = 0u;
-                const float un = fmaxf(u, __uint_as_float(__reduce_max_sync(0xffffffffu, ub)));
-                const float inv_u = un > 0.f ? 1.f / un : 0.f;
-                const float ru = un > u ? u * inv_u : 1.f;
-                u = un;
+                const float unew = fmaxf(u, __uint_as_float(__reduce_max_sync(0xffffffffu, ub)));
+                const float inv_u = unew > 0.f ? 1.f / unew : 0.f;
+                const float ru = unew > u ? u * inv_u : 1.f;
+                u = unew;
 
                 float kscale[4], vw[4];  // keys g, g + 8, g + 16, g + 24
 #pragma unroll
@@ -395,14 +515,10 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
             __syncwarp();
             if (lane == 0) sm100::mbar_arrive(empty + 8 * s);
         }
-    }
-    __syncthreads();  // ring drained (or given up): reuse it as the merge buffer
-    if (*abort_flag) return;
 
-    // Merge the four warps' states: [warp][row][dv], then (m, l, u) a warp and row.
-    float *obuf = reinterpret_cast<float *>(smem);
-    float *mbuf = obuf + 4 * R * OPITCH, *lbuf = mbuf + 4 * R, *ubuf = lbuf + 4 * R;
-    if (warp < 4) {
+        // Merge the four warps: their maxima, sums and scale units through shared
+        // memory, then O, brought to the common ones: warps 2 and 3 hand theirs to
+        // 0 and 1, warp 1 to warp 0.
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -411,70 +527,187 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
                 ls += __shfl_xor_sync(0xffffffffu, ls, 4);
                 ls += __shfl_xor_sync(0xffffffffu, ls, 8);
                 ls += __shfl_xor_sync(0xffffffffu, ls, 16);
-                const int row = nt * 8 + 2 * tig + e;
                 if (g == 0) {
-                    mbuf[warp * R + row] = m[nt][e];
-                    lbuf[warp * R + row] = ls;
-                    ubuf[warp * R + row] = u * Op::kUnit;
+                    stat_m[warp * R + nt * 8 + 2 * tig + e] = m[nt][e];
+                    stat_l[warp * R + nt * 8 + 2 * tig + e] = ls;
                 }
-#pragma unroll
-                for (int mt = 0; mt < DP / 16; ++mt)
-                    *reinterpret_cast<float2 *>(obuf + (warp * R + row) * OPITCH + mt * 16 + 2 * g) =
-                        make_float2(oacc[mt][nt][e], oacc[mt][nt][2 + e]);
             }
-    }
-    __syncthreads();
+        if (lane == 0) stat_u[warp] = u;
+        // the four warps go on or give up together
+        ok = sm100::bar_red_and(1, 128, ok);
+        if (!ok) return;
+        const float U = fmaxf(fmaxf(stat_u[0], stat_u[1]), fmaxf(stat_u[2], stat_u[3]));
+        const float to_u = U > 0.f ? u / U : 1.f;
+        float M[NT][2], Lsum[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float *sm = stat_m + nt * 8 + 2 * tig + e, *sl = stat_l + nt * 8 + 2 * tig + e;
+                const float mx = fmaxf(fmaxf(sm[0], sm[R]), fmaxf(sm[2 * R], sm[3 * R]));
+                const float mref = mx == -INFINITY ? 0.f : mx;
+                float ls = 0.f;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) ls += sl[w * R] * exp2f(sm[w * R] - mref);
+                M[nt][e] = mx;
+                Lsum[nt][e] = ls;
+                const float f = exp2f(m[nt][e] - mref) * to_u;
+#pragma unroll
+                for (int mt = 0; mt < DP / 16; ++mt) {
+                    oacc[mt][nt][e] *= f;
+                    oacc[mt][nt][2 + e] *= f;
+                }
+            }
+#pragma unroll
+        for (int c0 = 0; c0 < DP / 16; c0 += L::MC / 16) {
+            auto at = [&](int w, int mt, int nt, int e) -> float2 * {
+                return reinterpret_cast<float2 *>(mbuf + (w * R + nt * 8 + 2 * tig + e) * L::PITCH + mt * 16 + 2 * g);
+            };
+            auto put = [&](int w) {
+#pragma unroll
+                for (int mt = 0; mt < L::MC / 16; ++mt)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            *at(w, mt, nt, e) = make_float2(oacc[c0 + mt][nt][e], oacc[c0 + mt][nt][2 + e]);
+            };
+            auto add = [&](int w) {
+#pragma unroll
+                for (int mt = 0; mt < L::MC / 16; ++mt)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float2 v = *at(w, mt, nt, e);
+                            oacc[c0 + mt][nt][e] += v.x;
+                            oacc[c0 + mt][nt][2 + e] += v.y;
+                        }
+            };
+            if (c0 > 0) sm100::named_bar_sync(1, 128);
+            if (warp >= 2) put(warp - 2);
+            sm100::named_bar_sync(1, 128);
+            if (warp < 2) add(warp);
+            if (warp == 1) put(1);
+            sm100::named_bar_sync(1, 128);
+            if (warp == 0) add(1);
+        }
 
-    const int C4 = p.Dv / 4;
-    for (int idx = tid; idx < nrows * C4; idx += kThreads) {
-        const int row = idx / C4, c = (idx - row * C4) * 4;
-        int lo = 0, hi = 0;
-        if (row < nvalid) legal_range(row / G, si.Qb, si.Kb, p.window, p.mask, lo, hi);
-        const SplitSpan sp = split_span(lo, hi, p.split_len);
-        if (sp.direct ? sp.first != split : (split < sp.first || split > sp.last)) continue;
-        float M = -INFINITY;
+        // A whole unit goes out; a piece of one becomes a partial, the CTA's first
+        // or its last.
+        if (warp == 0) {
+            const bool whole = n == un.ntiles;
+            const long long slot = 2LL * blockIdx.x + (first_seg ? 0 : 1);
 #pragma unroll
-        for (int w = 0; w < 4; ++w) M = fmaxf(M, mbuf[w * R + row]);
-        const float mref = M == -INFINITY ? 0.f : M;
-        float L_ = 0.f, f[4];
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            f[w] = exp2f(mbuf[w * R + row] - mref);
-            L_ += lbuf[w * R + row] * f[w];
+                for (int e = 0; e < 2; ++e) {
+                    const int row = nt * 8 + 2 * tig + e;
+                    if (row >= nrows) continue;
+                    // a row without keys: +0 and -inf; one with a NaN key: NaN
+                    const float ls = Lsum[nt][e];
+                    const float inv = ls == 0.f ? 0.f : 1.f / ls;
+                    const float unit = U * Op::kUnit;
+                    const float lse2 = ls != ls ? ls : ls > 0.f ? M[nt][e] - kPOff + __log2f(ls) : -INFINITY;
+                    if (whole) {
+                        const int qi = row / G, h = kvh * G + row % G;
+                        const long long orow = (un.si.q_off + qi) * p.Hq + h;
+                        uint16_t *dst = static_cast<uint16_t *>(p.o) + orow * p.Dv + 2 * g;
+#pragma unroll
+                        for (int mt = 0; mt < DP / 16; ++mt)
+                            if (mt * 16 < p.Dv) {
+                                const float x = oacc[mt][nt][e] * inv * unit, y = oacc[mt][nt][2 + e] * inv * unit;
+                                *reinterpret_cast<uint32_t *>(dst + mt * 16) =
+                                    a.bf16 ? MmaOp<__nv_bfloat16>::pack(x, y) : MmaOp<__half>::pack(x, y);
+                            }
+                        if (g == 0 && p.lse) p.lse[orow] = lse2 * kLn2;
+                    } else {
+                        const long long prow = slot * R + row;
+                        float *dst = a.part_o + prow * p.Dv + 2 * g;
+#pragma unroll
+                        for (int mt = 0; mt < DP / 16; ++mt)
+                            if (mt * 16 < p.Dv)
+                                *reinterpret_cast<float2 *>(dst + mt * 16) = make_float2(
+                                    oacc[mt][nt][e] * inv * unit, oacc[mt][nt][2 + e] * inv * unit);
+                        // (+inf, so that the merge's maximum does not pass a NaN by)
+                        if (g == 0) a.part_lse[prow] = lse2 != lse2 ? INFINITY : lse2;
+                    }
+                }
         }
-        // a row without keys: +0 and -inf; one with a NaN key: NaN
-        const float inv = L_ == 0.f ? 0.f : 1.f / L_;
-        float o4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const float4 v = *reinterpret_cast<const float4 *>(obuf + (w * R + row) * OPITCH + c);
-            const float k = f[w] * inv, uw = ubuf[w * R + row];
-            o4[0] += v.x * k * uw;
-            o4[1] += v.y * k * uw;
-            o4[2] += v.z * k * uw;
-            o4[3] += v.w * k * uw;
+        left -= n;
+        if (left > 0) advance();
+    }
+}
+
+// Joins the partials of a sequence that spans several shares, one row a block:
+// groups of Dv / 4 threads take every ngrp-th partial, four loads in flight each,
+// then the groups are added up.
+constexpr int kMergeThreads = 128;
+
+__global__ void __launch_bounds__(kMergeThreads) q8_merge_kernel(const __grid_constant__ Q8Args a, int R) {
+    __shared__ float4 red[kMergeThreads];
+    const AttnParams &p = a.p;
+    const int nrows = p.Q * p.G, per_share = p.Hkv * nrows;
+    const int x = blockIdx.x / per_share, y = blockIdx.x - x * per_share;
+    const int kvh = y / nrows, row = y - kvh * nrows;
+    const int tid = threadIdx.x;
+    // launched as a programmatic dependent of the decode kernel
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    const int4 seam = __ldcg(a.seam + x + 1);
+    if (seam.x < 0) return;
+    const int np = seam.z - seam.y + 1;
+    const int C4 = p.Dv / 4, ngrp = kMergeThreads / C4, grp = tid / C4, c = tid - grp * C4;
+    // the first share's last partial (unless it begins with the sequence), the
+    // others' first
+    auto part = [&](int i) -> long long {
+        const long long cta = (long long)(seam.y + i) * p.Hkv + kvh;
+        return (2 * cta + (i == 0 ? seam.w : 0)) * R + row;
+    };
+    float mx = -INFINITY;
+    for (int i = tid & 31; i < np; i += 32) mx = fmaxf(mx, __ldcg(a.part_lse + part(i)));
+    mx = warp_max(mx);
+    const float mref = mx == -INFINITY ? 0.f : mx;
+    float sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (grp < ngrp) {
+#pragma unroll 4
+        for (int i = grp; i < np; i += ngrp) {
+            const long long at = part(i);
+            const float w = exp2f(__ldcg(a.part_lse + at) - mref);
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * p.Dv) + c);
+            sum += w;
+            acc.x = fmaf(w, v.x, acc.x);
+            acc.y = fmaf(w, v.y, acc.y);
+            acc.z = fmaf(w, v.z, acc.z);
+            acc.w = fmaf(w, v.w, acc.w);
         }
-        const bool nan = L_ != L_;
-        const float lse = nan ? L_ : L_ > 0.f ? (M - kPOff + __log2f(L_)) * kLn2 : -INFINITY;
-        const int qi = row / G, h = kvh * G + row % G;
-        if (sp.direct) {
-            const long long at = ((si.q_off + qi) * p.Hq + h) * (long long)p.Dv + c;
-            uint2 w;
-            if (a.bf16) {
-                w.x = MmaOp<__nv_bfloat16>::pack(o4[0], o4[1]);
-                w.y = MmaOp<__nv_bfloat16>::pack(o4[2], o4[3]);
-            } else {
-                w.x = MmaOp<__half>::pack(o4[0], o4[1]);
-                w.y = MmaOp<__half>::pack(o4[2], o4[3]);
-            }
-            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) + at) = w;
-            if (c == 0 && p.lse) p.lse[(si.q_off + qi) * p.Hq + h] = lse;
+    }
+    __shared__ float rsum[kMergeThreads];
+    red[tid] = acc;
+    rsum[tid] = sum;
+    __syncthreads();
+    if (tid < C4) {
+        for (int k = 1; k < ngrp; ++k) {
+            const float4 v = red[k * C4 + tid];
+            sum += rsum[k * C4 + tid];
+            acc.x += v.x;
+            acc.y += v.y;
+            acc.z += v.z;
+            acc.w += v.w;
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const long long orow = ((long long)seam.x * p.Q + row / p.G) * p.Hq + kvh * p.G + row % p.G;
+        uint2 w;
+        if (a.bf16) {
+            w.x = MmaOp<__nv_bfloat16>::pack(acc.x * inv, acc.y * inv);
+            w.y = MmaOp<__nv_bfloat16>::pack(acc.z * inv, acc.w * inv);
         } else {
-            const long long prow = (((long long)split * p.B + b) * p.Q + qi) * p.Hq + h;
-            *reinterpret_cast<float4 *>(p.part_o + prow * p.Dv + c) = make_float4(o4[0], o4[1], o4[2], o4[3]);
-            // (+inf, so that the merge's maximum does not pass a NaN by)
-            if (c == 0) p.part_lse[prow] = nan ? INFINITY : lse;
+            w.x = MmaOp<__half>::pack(acc.x * inv, acc.y * inv);
+            w.y = MmaOp<__half>::pack(acc.z * inv, acc.w * inv);
         }
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) + orow * p.Dv + 4 * tid) = w;
+        if (tid == 0 && p.lse)
+            p.lse[orow] = sum != sum ? sum : sum > 0.f ? (mx + __log2f(sum)) * kLn2 : -INFINITY;
     }
 }
 
@@ -503,7 +736,7 @@ int pool_map(CUtensorMap *map, const void *ptr, int D, int Hkv, uint64_t rows, i
 
 template <int CODE, int DP, int NT>
 int launch_t(const Q8Args &a, cudaStream_t stream) {
-    using L = Ring<DP>;
+    using L = Ring<DP, NT>;
     CUtensorMap tk, tv;
     const uint64_t rows = (uint64_t)a.p.num_pages * a.p.page_size;
     int rc = pool_map(&tk, a.c.k, a.p.D, a.p.Hkv, rows, L::HALF, a.box_rows);
@@ -515,11 +748,27 @@ int launch_t(const Q8Args &a, cudaStream_t stream) {
         set_error("8-bit decode kernel: cudaFuncSetAttribute: %s", cudaGetErrorString(e));
         return 3;
     }
-    const dim3 grid((unsigned)a.p.nsplit, (unsigned)(a.p.B * a.p.Hkv));
-    kern<<<grid, kThreads, L::SMEM, stream>>>(a, tk, tv);
+    kern<<<(unsigned)(a.shares * a.p.Hkv), kThreads, L::SMEM, stream>>>(a, tk, tv);
     e = cudaGetLastError();
     if (e != cudaSuccess) {
         set_error("8-bit decode kernel launch: %s", cudaGetErrorString(e));
+        return 3;
+    }
+    count_launch();
+    if (a.shares == 1) return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((a.shares - 1) * a.p.Hkv * a.p.Q * a.p.G));
+    cfg.blockDim = dim3(kMergeThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, q8_merge_kernel, a, (int)L::R);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) {
+        set_error("8-bit decode merge launch: %s", cudaGetErrorString(e));
         return 3;
     }
     count_launch();
@@ -527,7 +776,8 @@ int launch_t(const Q8Args &a, cudaStream_t stream) {
 }
 
 template <int CODE, int DP> int launch_nt(const Q8Args &a, cudaStream_t stream) {
-    return a.p.Q * a.p.G <= 8 ? launch_t<CODE, DP, 1>(a, stream) : launch_t<CODE, DP, 2>(a, stream);
+    return a.p.Q * a.p.G <= 8 ? launch_t<CODE, DP, 1>(a, stream)
+                              : launch_t<CODE, DP, 2>(a, stream);
 }
 
 template <int CODE> int launch_code(const Q8Args &a, cudaStream_t stream) {
@@ -537,6 +787,19 @@ template <int CODE> int launch_code(const Q8Args &a, cudaStream_t stream) {
     return launch_nt<CODE, 256>(a, stream);
 }
 
+// Shares: as many as give each resident CTA (two an SM up to widths of 128, one
+// above) one of a head; where that is few of them and leaves CTAs over (more
+// than a 40th), four times as many.  No more than the tables' capacity has
+// tiles.
+int shares_of(const AttnParams &p, int nsm) {
+    const int w = p.D > p.Dv ? p.D : p.Dv;
+    const long long ctas = (long long)(nsm < 1 ? 1 : nsm) * (w <= 128 ? 2 : 1);
+    long long n = ctas / p.Hkv;
+    if ((ctas - n * p.Hkv) * 40 > ctas) n = (4 * ctas + p.Hkv - 1) / p.Hkv;
+    const long long tiles = (long long)p.B * (((long long)p.K + kTile - 1) / kTile);
+    return (int)(tiles < 1 ? 1 : tiles < n ? tiles : n);
+}
+
 }  // namespace
 
 bool q8_decode_supported(const AttnParams &p, int dtype) {
@@ -544,24 +807,17 @@ bool q8_decode_supported(const AttnParams &p, int dtype) {
     // TMA copies rows of D bytes from 16-byte boundaries, and whole 8-row swizzle atoms
     if (p.D % 16 || p.Dv % 16 || p.D > 256 || p.Dv > 256 || p.page_size < 8) return false;
     if ((long long)p.Q * p.G > 16 || p.Q < 1) return false;
-    return (long long)p.B * p.Hkv <= 65535;
+    return p.Hkv <= 65535;  // CTAs and merge blocks are counted in 32 bits
 }
 
-int q8_decode_split_len(const AttnParams &p, int nsm) {
-    if (nsm < 1) nsm = 1;
-    const long long units = (long long)p.B * p.Hkv;
-    long long len = ((long long)p.K * units + 4LL * nsm - 1) / (4LL * nsm);
-    len = (len + kTile - 1) / kTile * kTile;
-    if (len < kTile) len = kTile;
-    if (len > 1024) len = 1024;
-    return (int)len;
+unsigned long long q8_decode_workspace(const AttnParams &p, int nsm) {
+    const unsigned long long shares = shares_of(p, nsm);
+    const unsigned long long rows = 2 * shares * p.Hkv * (p.Q * p.G <= 8 ? 8 : 16);
+    return shares * sizeof(int4) + rows * 4 * (p.Dv + 1ull);
 }
 
-int launch_q8_decode(const AttnParams &p, const Q8Cache &c, int dtype, cudaStream_t stream) {
-    if (p.nsplit > 0x7fffffff / 2) {
-        set_error("8-bit decode kernel: too many splits");
-        return 2;
-    }
+int launch_q8_decode(const AttnParams &p, const Q8Cache &c, int dtype, int nsm, void *ws,
+                     cudaStream_t stream) {
     Q8Args a;
     a.p = p;
     a.c = c;
@@ -569,7 +825,12 @@ int launch_q8_decode(const AttnParams &p, const Q8Cache &c, int dtype, cudaStrea
     a.box_rows = p.page_size < 64 ? p.page_size : 64;
     a.box_shift = 0;
     while ((1 << a.box_shift) < a.box_rows) ++a.box_shift;
-    return c.code == kCodeE4m3 ? launch_code<kCodeE4m3>(a, stream) : launch_code<kCodeInt8>(a, stream);
+    a.shares = shares_of(p, nsm);
+    a.seam = static_cast<int4 *>(ws);
+    a.part_o = reinterpret_cast<float *>(a.seam + a.shares);
+    a.part_lse = a.part_o + 2ull * a.shares * p.Hkv * (p.Q * p.G <= 8 ? 8 : 16) * p.Dv;
+    return c.code == kCodeE4m3 ? launch_code<kCodeE4m3>(a, stream)
+                               : launch_code<kCodeInt8>(a, stream);
 }
 
 }  // namespace attn

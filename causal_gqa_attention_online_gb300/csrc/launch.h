@@ -124,10 +124,12 @@ int launch_q8_expand(const AttnParams &p, const Q8Cache &c, void *k_out, void *v
                      cudaStream_t stream);
 
 // Split-KV decode that reads the codes themselves (bf16/fp16, Q * G <= 16, widths
-// multiples of 16 up to 256, pages of 8 rows or more).  Honours p.nsplit.
+// multiples of 16 up to 256, pages of 8 rows or more), with a workspace of the
+// given number of bytes at a 16-byte aligned address.
 bool q8_decode_supported(const AttnParams &p, int dtype);
-int q8_decode_split_len(const AttnParams &p, int nsm);
-int launch_q8_decode(const AttnParams &p, const Q8Cache &c, int dtype, cudaStream_t stream);
+unsigned long long q8_decode_workspace(const AttnParams &p, int nsm);
+int launch_q8_decode(const AttnParams &p, const Q8Cache &c, int dtype, int nsm, void *ws,
+                     cudaStream_t stream);
 
 constexpr int kMaxPools = 64;  // pools one launch copies
 int launch_pages_copy(const void *const *src_pools, void *const *dst_pools, const long long *bytes,

@@ -90,6 +90,17 @@ __host__ __device__ __forceinline__ AppendSpan append_span(int len, int n, long 
     return s;
 }
 
+// The keys that some row of a sequence attends to, [lo, hi) (0, 0 without any):
+// the union of legal_range over its Qb rows.
+__host__ __device__ __forceinline__ void unit_keys(int Qb, int Kb, int window, int mask, int &lo,
+                                                   int &hi) {
+    lo = hi = 0;
+    if (Qb <= 0 || Kb <= 0) return;
+    hi = mask == 1 && Qb < Kb ? Qb : Kb;
+    // bottom-right causal: the first row with a key is max(0, Qb - Kb)
+    if (mask == 0 && window > 0 && Kb - Qb - window + 1 > 0) lo = Kb - Qb - window + 1;
+}
+
 // The smallest power of two s >= 2^-100 with a <= qmax * s, for a >= 0; NaN when
 // a is infinite or NaN.
 __host__ __device__ __forceinline__ float append_scale(float a, int code) {

@@ -272,6 +272,19 @@ def test_attention_over_a_poisoned_block_is_not_a_number_or_empty():
     assert bad[1, :, 4:].all()
 
 
+@pytest.mark.parametrize("i", range(8))
+def test_attention_of_ragged_batches(i):
+    """Shares of the tiles that begin and end anywhere in units of any length:
+    empty sequences, single tiles, units over many shares."""
+    g = np.random.default_rng(600 + i)
+    B = int(g.integers(1, 70))
+    most = int([20, 130, 600, 5000][i % 4] if B < 8 or i % 4 < 3 else 600)
+    lens = [int(n) if g.random() < 0.8 else 0 for n in g.integers(0, most + 1, B)]
+    Hkv, G, Q = int(g.integers(1, 5)), int(g.integers(1, 5)), int(g.integers(1, 4))
+    check_attention(g, ["bf16", "f16"][i % 2], ["int8", "e4m3"][i // 2 % 2], B, Hkv * G, Hkv, Q, 64,
+                    64, lens, 64, 32, window=int(g.integers(0, 300)) if i % 3 == 0 else 0)
+
+
 # -------------------------------------------------------------------- append
 
 def run_append(g, dtype, kind, lens, new, N, Hkv, D, Dv, page, block, packed=False, extra_pages=0,

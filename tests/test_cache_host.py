@@ -284,6 +284,11 @@ int main() {
             std::scanf("%d %d %lld %d %d %d", &len, &n, &cap, &t, &ps, &bs);
             const attn::AppendSpan s = attn::append_span(len, n, cap, t, ps, bs);
             std::printf("%lld %lld %lld %d %d\n", s.first, s.last, s.start, s.entry, s.sub);
+        } else if (what == 'u') {
+            int Qb, Kb, w, m, lo, hi;
+            std::scanf("%d %d %d %d", &Qb, &Kb, &w, &m);
+            attn::unit_keys(Qb, Kb, w, m, lo, hi);
+            std::printf("%d %d\n", lo, hi);
         } else {
             unsigned bits;
             int code;
@@ -347,6 +352,22 @@ def test_append_spans_cover_exactly_the_new_rows(prog):
         assert seen == list(range(length, min(length + n, cap)))
     first, last, start, entry, sub = lines[-1]
     assert (first, last) == (big - 3, big) and entry == (big - 3) >> 6
+
+
+def test_unit_keys_are_the_union_of_the_rows_legal_keys(prog):
+    from tests.oracle_pins import mask_matrix
+    cs = [(Qb, Kb, w, m) for Qb in range(0, 8) for Kb in range(0, 9) for m in range(3)
+          for w in ((0,) if m == 2 else (0, 1, 2, 5, 9))]
+    r = subprocess.run([prog], input="\n".join("u %d %d %d %d" % c for c in cs), capture_output=True,
+                       text=True, timeout=60)
+    got = [tuple(int(x) for x in ln.split()) for ln in r.stdout.splitlines()]
+    assert len(got) == len(cs)
+    for (Qb, Kb, w, m), (lo, hi) in zip(cs, got):
+        keys = np.flatnonzero(mask_matrix(Qb, Kb, w, m).any(axis=0)) if Qb and Kb else np.zeros(0)
+        if keys.size == 0:
+            assert hi <= lo, (Qb, Kb, w, m)
+        else:
+            assert (lo, hi) == (keys[0], keys[-1] + 1), (Qb, Kb, w, m)
 
 
 @pytest.mark.parametrize("kind,code", [("e4m3", 0), ("int8", 1)])
