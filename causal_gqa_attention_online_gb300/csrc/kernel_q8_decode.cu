@@ -5,33 +5,35 @@
 // The products are those of the 16-bit decode, keys (or value columns) on M and
 // the rows of the KV group on N,
 //
-//     S^T[key, row] = code_K[key, :] . Q[row, :],   s = S^T * ks[key] * f[row]
-//     O^T[dv, row] += code_V^T[dv, key] . (p * vs[key] / u)^T[key, row]
+//     S^T[key, row] = code_K[key, :] . Q[row, :],   x = S^T * ks[key]
+//     p = 2^(x f[row] - m + 14),   O^T[dv, row] += code_V^T[dv, key] . (p * vs[key] / u)^T
 //
 // with m16n8k16 f16 products, fp32 accumulation.  Codes become f16 pairs in
 // registers, exactly (q8.cuh), and the scales multiply scores and probabilities
 // in fp32, so no key or value is rounded:
 //
-// * Q rows are brought to [2^14, 2^15) by a power of two (in f[row] again), so
-//   that bf16's 8 bits stay exact down to 2^-29 of the row's largest element.
-// * Probabilities are p = 2^(s - m + 14), in (0, 2^14]: f16's 11 bits down to
-//   2^-28 of the largest, steps of 2^-38 below.  u is the largest value scale a
-//   warp has seen, so p * vs / u stays in range; O is rescaled when m or u grow.
-//   The 2^14 cancels against the row sum, u and the codes' unit come back in the
-//   final normalisation.
-// * Which bytes pair up is chosen so that no byte is moved across lanes: the
-//   even and the odd bytes of a 32-bit word are the two halves of a k16 step
-//   (K: Q's columns are permuted to match) or the rows dv = 2g and 2g + 1 (V: a
-//   transposed ldmatrix of byte pairs gives two keys' pairs in one word).
+// * Q rows are brought to [2^14, 2^15) by a power of two (in f[row], with the
+//   softmax scale; its sign goes to Q), so that bf16's 8 bits stay exact down to
+//   2^-29 of the row's largest element.
+// * Probabilities are in (0, 2^14]: f16's 11 bits down to 2^-28 of the largest,
+//   steps of 2^-38 below.  u is the largest value scale a warp has seen, so
+//   p * vs / u stays in range; O is rescaled when m or u grow.  The 2^14 cancels
+//   against the row sum, u comes back in the final normalisation.
+// * Which bytes pair up is chosen so that no byte is moved across lanes: the two
+//   pairs of a 32-bit word are the two halves of a k16 step (K: Q's columns are
+//   permuted to match) or the rows dv = 2g and 2g + 1 (V: a transposed ldmatrix of
+//   byte pairs gives two keys' pairs in one word).
 //
 // Bound: HBM, one byte an element -- at 8 flops a byte, twice the 16-bit
-// decode's arithmetic per byte, the conversions (7 or 5 instructions for four
+// decode's arithmetic per byte, the conversions (4 to 5 instructions for four
 // codes) have to stay out of the way.  A CTA is four consumer warps of 32 keys
 // each and a producer warp: it looks pages up one tile ahead, issues one TMA
 // box per page piece (up to 64 rows) and the block scales as 4-byte cp.async,
 // all completing on the stage's mbarrier; consumers free a stage with one
-// arrival a warp, so no warp waits for another within a tile.  V rows past the
-// last key need no zeroing: any byte is a finite f16 here, and its p is 0.
+// arrival a warp, so no warp waits for another within a tile.  Tiles that every
+// row attends to whole take a step without tests; in the others masked scores
+// are -inf and V's words are cleared where a key takes no part (a code there may
+// be e4m3's NaN).
 //
 // Work: the 128-key tiles of all sequences, in order, are cut into equal shares
 // whatever the lengths, and a CTA takes one share for one KV head -- as many
@@ -48,12 +50,14 @@
 
 #include <climits>
 #include <cstring>
+#include <type_traits>
 
 #include "common.cuh"
 #include "launch.h"
 #include "mma_sync.cuh"
 #include "q8.cuh"
 #include "sm100_ptx.cuh"
+#include "tc_softmax.cuh"
 
 namespace attn {
 namespace {
@@ -321,8 +325,7 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
         const int n = (int)min((long long)(un.ntiles - tile), left);
         const int nvalid = un.si.Qb * G;
         // Q^T fragments (B operand of S^T): column n = row g; in each 16 columns
-        // lane tig holds columns 4 tig + {0, 2} and 4 tig + {1, 3}, as the codes'
-        // even and odd bytes pair.
+        // lane tig holds columns 4 tig to 4 tig + 3, paired as the codes' bytes are.
         uint32_t qf[DP / 16][NT][2];
         float rowf[NT][2];
 #pragma unroll
@@ -353,20 +356,24 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
             // 2^ea <= amax < 2^(ea + 1); the row is multiplied by 2^(14 - ea)
             const int ea = max((int)(__float_as_uint(amax) >> 23) - 127, -112);
-            const float up = __uint_as_float((uint32_t)(127 + 14 - ea) << 23);
-            const float f = p.scale_log2 * Op::kUnit * __uint_as_float((uint32_t)max(127 + ea - 14, 1) << 23);
+            const float up = copysignf(__uint_as_float((uint32_t)(127 + 14 - ea) << 23), p.scale_log2);
+            // (not 0, so that it orders -inf; x f is 0 all the same for a scale of 0)
+            const float f = fmaxf(fabsf(p.scale_log2) * __uint_as_float((uint32_t)max(127 + ea - 14, 1) << 23), 1e-37f);
+            constexpr int J1 = Op::kPerm ? 2 : 1, J2 = Op::kPerm ? 1 : 2;
 #pragma unroll
             for (int kk = 0; kk < DP / 16; ++kk) {
-                qf[kk][nt][0] = MmaOp<__half>::pack(val(kk, 0) * up, val(kk, 2) * up);
-                qf[kk][nt][1] = MmaOp<__half>::pack(val(kk, 1) * up, val(kk, 3) * up);
+                qf[kk][nt][0] = MmaOp<__half>::pack(val(kk, 0) * up, val(kk, J1) * up);
+                qf[kk][nt][1] = MmaOp<__half>::pack(val(kk, J2) * up, val(kk, 3) * up);
             }
             rowf[nt][0] = __shfl_sync(0xffffffffu, f, 8 * tig);
             rowf[nt][1] = __shfl_sync(0xffffffffu, f, 8 * tig + 4);
         }
-        // Legal keys of the two rows (per n-tile) this thread's columns hold.
+        // Legal keys of the two rows (per n-tile) this thread's columns hold, and
+        // of all rows.
         int rlo[NT][2], rhi[NT][2];
-        float m[NT][2], l[NT][2], u = 0.f;
+        float m[NT][2], l[NT][2], u = 0.f;  // m: the largest x
         float oacc[DP / 16][NT][4];
+        int lo_all = 0, hi_all = INT_MAX;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -376,15 +383,164 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
                 if (row < nvalid) legal_range(row / G, un.si.Qb, un.si.Kb, p.window, p.mask, lo, hi);
                 rlo[nt][e] = lo;
                 rhi[nt][e] = hi;
+                if (row < nrows) {
+                    lo_all = max(lo_all, lo);
+                    hi_all = min(hi_all, hi);
+                }
                 m[nt][e] = -INFINITY;
                 l[nt][e] = 0.f;
             }
+        lo_all = __reduce_max_sync(0xffffffffu, lo_all);
+        hi_all = __reduce_min_sync(0xffffffffu, hi_all);
 #pragma unroll
         for (int mt = 0; mt < DP / 16; ++mt)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) oacc[mt][nt][j] = 0.f;
+
+        // One step: the warp's 32 keys from key0 on, in stage s.  EDGE: some row may
+        // not attend to all of them.
+        auto step = [&](auto edge, int key0, uint32_t s) {
+            constexpr bool EDGE = decltype(edge)::value;
+            const uint32_t ks = sbase + s * L::STAGE, vs = ks + L::TILE;
+            const float *sc = reinterpret_cast<const float *>(smem + s * L::STAGE + 2 * L::TILE) + kw0;
+
+            // S^T = K Q^T
+            float sacc[2][NT][4];
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) sacc[mt][nt][j] = 0.f;
+#pragma unroll
+            for (int kk = 0; kk < DP / 16; kk += 2) {
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt) {
+                    uint32_t r[4];
+                    ldmatrix_x4(r, ks + chunk_at<DP>(kw0 + mt * 16 + (lane & 15), kk + (lane >> 4)));
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t f[4];
+                        Op::k_pairs(r[2 * h], f[0], f[2]);
+                        Op::k_pairs(r[2 * h + 1], f[1], f[3]);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            MmaOp<__half>::run(sacc[mt][nt], f, qf[kk + h][nt][0], qf[kk + h][nt][1]);
+                    }
+                }
+            }
+
+            // the largest finite value scale so far, of keys some row attends to
+            const int uk = key0 + lane;
+            uint32_t ub = __float_as_uint(sc[kTile + lane]) & 0x7fffffffu;
+            if (ub >= 0x7f800000u || (EDGE && !(uk >= un.klo && uk < un.kend))) ub = 0u;
+            const float unew = fmaxf(u, __uint_as_float(__reduce_max_sync(0xffffffffu, ub)));
+            const float inv_u = unew > 0.f ? 1.f / unew : 0.f;
+
+            float kscale[4], vw[4];  // keys g, g + 8, g + 16, g + 24
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                kscale[i] = sc[g + 8 * i];
+                vw[i] = sc[kTile + g + 8 * i] * inv_u;
+            }
+            float x[NT][2][4], mx[NT][2];
+            bool grew = unew > u;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        x[nt][e][i] = sacc[i >> 1][nt][2 * (i & 1) + e] * kscale[i];
+                        if (EDGE) {
+                            const int key = key0 + g + 8 * i;
+                            if (!(key >= rlo[nt][e] && key < rhi[nt][e])) x[nt][e][i] = -INFINITY;
+                        }
+                    }
+                    float v = tcfwd::fmax3(x[nt][e][0], x[nt][e][1], fmaxf(x[nt][e][2], x[nt][e][3]));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                    v = tcfwd::fmax3(v, __shfl_xor_sync(0xffffffffu, v, 16), m[nt][e]);
+                    mx[nt][e] = v;
+                    grew |= v > m[nt][e];
+                }
+            if (__any_sync(0xffffffffu, grew)) {
+                const float ru = unew > u ? u * inv_u : 1.f;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        // (no key yet: both -inf, and nothing to rescale)
+                        const float alpha =
+                            mx[nt][e] > m[nt][e] ? tcfwd::ex2((m[nt][e] - mx[nt][e]) * rowf[nt][e]) : 1.f;
+                        m[nt][e] = mx[nt][e];
+                        l[nt][e] *= alpha;
+                        const float f = alpha * ru;
+#pragma unroll
+                        for (int mt = 0; mt < DP / 16; ++mt) {
+                            oacc[mt][nt][e] *= f;
+                            oacc[mt][nt][2 + e] *= f;
+                        }
+                    }
+                u = unew;
+            }
+            uint32_t pb[2][NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float pv[4][2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float ref = m[nt][e] == -INFINITY ? 0.f : kPOff - m[nt][e] * rowf[nt][e];
+                    float pe[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) pe[i] = tcfwd::ex2(fmaf(x[nt][e][i], rowf[nt][e], ref));
+                    l[nt][e] += (pe[0] + pe[1]) + (pe[2] + pe[3]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)  // (a scale that is no number counts only where its key does)
+                        pv[i][e] = EDGE && x[nt][e][i] == -INFINITY ? 0.f : pe[i] * vw[i];
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    pb[i >> 1][nt][i & 1] = movmatrix_trans(MmaOp<__half>::pack(pv[i][0], pv[i][1]));
+            }
+
+            // O^T += V^T P^T: rows g and g + 8 of a 16-column step are its columns
+            // 2 g and 2 g + 1
+            uint32_t vmask[2][2];
+            if (EDGE) {
+#pragma unroll
+                for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int k = key0 + kt * 16 + h * 8 + 2 * tig;
+                        vmask[kt][h] = (k >= un.klo && k < un.kend ? 0xffffu : 0u) |
+                                       (k + 1 >= un.klo && k + 1 < un.kend ? 0xffff0000u : 0u);
+                    }
+            }
+#pragma unroll
+            for (int cc = 0; cc < DP / 16; cc += 2) {
+#pragma unroll
+                for (int kt = 0; kt < 2; ++kt) {
+                    uint32_t r[4];
+                    ldmatrix_x4_trans(r, vs + chunk_at<DP>(kw0 + kt * 16 + (lane & 15), cc + (lane >> 4)));
+                    if (EDGE) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) r[i] &= vmask[kt][i & 1];
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t f[4];
+                        Op::even_odd(r[2 * h], f[0], f[1]);
+                        Op::even_odd(r[2 * h + 1], f[2], f[3]);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            MmaOp<__half>::run(oacc[cc + h][nt], f, pb[kt][nt][0], pb[kt][nt][1]);
+                    }
+                }
+            }
+        };
 
         for (int t = tile; t < tile + n && ok; ++t, ++it) {
             const uint32_t s = it % NS;
@@ -398,120 +554,8 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
                 break;
             }
             const int key0 = un.kbeg + t * kTile + kw0;
-            if (key0 < un.kend) {
-                const uint32_t ks = sbase + s * L::STAGE, vs = ks + L::TILE;
-                const float *sc = reinterpret_cast<const float *>(smem + s * L::STAGE + 2 * L::TILE) + kw0;
-
-                // S^T = K Q^T for this warp's 32 keys
-                float sacc[2][NT][4];
-#pragma unroll
-                for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) sacc[mt][nt][j] = 0.f;
-#pragma unroll
-                for (int kk = 0; kk < DP / 16; kk += 2) {
-#pragma unroll
-                    for (int mt = 0; mt < 2; ++mt) {
-                        uint32_t r[4];
-                        ldmatrix_x4(r, ks + chunk_at<DP>(kw0 + mt * 16 + (lane & 15), kk + (lane >> 4)));
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint32_t f[4] = {Op::even(r[2 * h]), Op::even(r[2 * h + 1]),
-                                                   Op::odd(r[2 * h]), Op::odd(r[2 * h + 1])};
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                MmaOp<__half>::run(sacc[mt][nt], f, qf[kk + h][nt][0], qf[kk + h][nt][1]);
-                        }
-                    }
-                }
-
-                // the largest finite value scale so far, of keys some row attends to
-                const int uk = key0 + lane;
-                uint32_t ub = uk >= un.klo && uk < un.kend ? __float_as_uint(sc[kTile + lane]) & 0x7fffffffu : 0u;
-                if (ub >= 0x7f800000u) ub = 0u;
-                const float unew = fmaxf(u, __uint_as_float(__reduce_max_sync(0xffffffffu, ub)));
-                const float inv_u = unew > 0.f ? 1.f / unew : 0.f;
-                const float ru = unew > u ? u * inv_u : 1.f;
-                u = unew;
-
-                float kscale[4], vw[4];  // keys g, g + 8, g + 16, g + 24
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    kscale[i] = sc[g + 8 * i];
-                    vw[i] = sc[kTile + g + 8 * i] * inv_u;
-                }
-                uint32_t pb[2][NT][2];
-                bool rescale = ru != 1.f;
-                float fac[NT][2];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float pv[4][2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float sv[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int key = key0 + g + 8 * i;
-                            const bool legal = key >= rlo[nt][e] && key < rhi[nt][e];
-                            sv[i] = legal ? sacc[i >> 1][nt][2 * (i & 1) + e] * kscale[i] * rowf[nt][e] : -INFINITY;
-                        }
-                        float mx = fmaxf(fmaxf(sv[0], sv[1]), fmaxf(sv[2], sv[3]));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                        const float mnew = fmaxf(m[nt][e], mx);
-                        const float mref = mnew == -INFINITY ? 0.f : mnew;  // no key yet: keep zeros
-                        const float alpha = exp2f(m[nt][e] - mref);
-                        m[nt][e] = mnew;
-                        fac[nt][e] = alpha * ru;
-                        rescale |= alpha != 1.f;
-                        float sum = 0.f;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float pe = exp2f(sv[i] - (mref - kPOff));
-                            sum += pe;
-                            // (a scale that is no number counts only where its key does)
-                            pv[i][e] = sv[i] == -INFINITY ? 0.f : pe * vw[i];
-                        }
-                        l[nt][e] = l[nt][e] * alpha + sum;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        pb[i >> 1][nt][i & 1] = movmatrix_trans(MmaOp<__half>::pack(pv[i][0], pv[i][1]));
-                }
-                if (__any_sync(0xffffffffu, rescale)) {
-#pragma unroll
-                    for (int mt = 0; mt < DP / 16; ++mt)
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            oacc[mt][nt][0] *= fac[nt][0];
-                            oacc[mt][nt][1] *= fac[nt][1];
-                            oacc[mt][nt][2] *= fac[nt][0];
-                            oacc[mt][nt][3] *= fac[nt][1];
-                        }
-                }
-
-                // O^T += V^T P^T: rows g and g + 8 of a 16-column step are its
-                // columns 2 g and 2 g + 1
-#pragma unroll
-                for (int cc = 0; cc < DP / 16; cc += 2) {
-#pragma unroll
-                    for (int kt = 0; kt < 2; ++kt) {
-                        uint32_t r[4];
-                        ldmatrix_x4_trans(r, vs + chunk_at<DP>(kw0 + kt * 16 + (lane & 15), cc + (lane >> 4)));
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint32_t f[4] = {Op::even(r[2 * h]), Op::odd(r[2 * h]),
-                                                   Op::even(r[2 * h + 1]), Op::odd(r[2 * h + 1])};
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                MmaOp<__half>::run(oacc[cc + h][nt], f, pb[kt][nt][0], pb[kt][nt][1]);
-                        }
-                    }
-                }
-            }
+            if (key0 >= lo_all && key0 + 32 <= hi_all) step(std::false_type{}, key0, s);
+            else if (key0 < un.kend) step(std::true_type{}, key0, s);
             __syncwarp();
             if (lane == 0) sm100::mbar_arrive(empty + 8 * s);
         }
@@ -527,6 +571,7 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
                 ls += __shfl_xor_sync(0xffffffffu, ls, 4);
                 ls += __shfl_xor_sync(0xffffffffu, ls, 8);
                 ls += __shfl_xor_sync(0xffffffffu, ls, 16);
+                m[nt][e] *= rowf[nt][e];  // in log2 units from here on
                 if (g == 0) {
                     stat_m[warp * R + nt * 8 + 2 * tig + e] = m[nt][e];
                     stat_l[warp * R + nt * 8 + 2 * tig + e] = ls;
@@ -607,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
                     // a row without keys: +0 and -inf; one with a NaN key: NaN
                     const float ls = Lsum[nt][e];
                     const float inv = ls == 0.f ? 0.f : 1.f / ls;
-                    const float unit = U * Op::kUnit;
+                    const float unit = U;
                     const float lse2 = ls != ls ? ls : ls > 0.f ? M[nt][e] - kPOff + __log2f(ls) : -INFINITY;
                     if (whole) {
                         const int qi = row / G, h = kvh * G + row % G;

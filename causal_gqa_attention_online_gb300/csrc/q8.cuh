@@ -3,8 +3,8 @@
 //
 // A page holds page_size rows [Hkv][D] of 8-bit codes and, for each block of
 // page_size / nblk tokens and each head, one fp32 scale: a row's value is
-// code * scale.  Codes are int8 (-127..127) or e4m3 (+-448; the NaN code is not
-// used and reads as +-480).
+// code * scale.  Codes are int8 (-127..127) or e4m3 (the NaN code is never
+// written).
 #pragma once
 
 #include <cuda_fp8.h>
@@ -23,22 +23,29 @@ struct Q8Cache {
     int blk_shift;            // log2(tokens a block)
 };
 
-// Two e4m3 codes in bytes 0 and 2 (even) or 1 and 3 (odd) of a word as a pair of
-// f16: the magnitude bits moved under f16's exponent read as value * 2^-8
-// (exponent bias 15 against 7), subnormals included, so the pair is exact and
-// the factor 2^8 goes into a scale.
+// Codes to f16 pairs, exactly.  k0 / k1: the four bytes of a word as two pairs in
+// any fixed order (kPerm: whether that is 0 2, 1 3 instead of 0 1, 2 3); even /
+// odd: bytes 0 and 2, 1 and 3.  e4m3 has an instruction for adjacent bytes, so
+// even / odd first bring those together.
 template <int CODE> struct CodeOps;
 template <> struct CodeOps<kCodeE4m3> {
-    static constexpr float kUnit = 256.f;  // value = f16 * kUnit
-    __device__ __forceinline__ static uint32_t even(uint32_t x) {
-        return ((x << 8) & 0x80008000u) | ((x << 7) & 0x3f803f80u);
+    static constexpr bool kPerm = false;
+    __device__ __forceinline__ static uint32_t pair(uint16_t x) {
+        uint32_t r;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(r) : "h"(x));
+        return r;
     }
-    __device__ __forceinline__ static uint32_t odd(uint32_t x) {
-        return (x & 0x80008000u) | ((x >> 1) & 0x3f803f80u);
+    __device__ __forceinline__ static void k_pairs(uint32_t x, uint32_t &k0, uint32_t &k1) {
+        k0 = pair((uint16_t)x);
+        k1 = pair((uint16_t)(x >> 16));
+    }
+    __device__ __forceinline__ static void even_odd(uint32_t x, uint32_t &even, uint32_t &odd) {
+        const uint32_t y = __byte_perm(x, 0, 0x3120);
+        even = pair((uint16_t)y);
+        odd = pair((uint16_t)(y >> 16));
     }
     __device__ __forceinline__ static float one(uint8_t c) {
-        return __half2float(__ushort_as_half((unsigned short)(((c & 0x80u) << 8) |
-                                                              ((c & 0x7fu) << 7)))) * kUnit;
+        return __half2float(__ushort_as_half((unsigned short)(pair(c) & 0xffffu)));
     }
     __device__ __forceinline__ static uint8_t code(float y) {
         return (uint8_t)__nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
@@ -48,19 +55,18 @@ template <> struct CodeOps<kCodeE4m3> {
 // int8: the code with its sign bit flipped in the low byte of 0x6400 is the f16
 // 1024 + (code + 128); subtracting 1152 leaves the code, exactly.
 template <> struct CodeOps<kCodeInt8> {
-    static constexpr float kUnit = 1.f;
+    static constexpr bool kPerm = true;
     __device__ __forceinline__ static uint32_t debias(uint32_t t) {
         const uint32_t b = 0x64806480u;  // 1152, 1152
         const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&t),
                                   *reinterpret_cast<const __half2 *>(&b));
         return *reinterpret_cast<const uint32_t *>(&r);
     }
-    __device__ __forceinline__ static uint32_t even(uint32_t x) {
-        return debias((x & 0x00ff00ffu) ^ 0x64806480u);
+    __device__ __forceinline__ static void even_odd(uint32_t x, uint32_t &even, uint32_t &odd) {
+        even = debias((x & 0x00ff00ffu) ^ 0x64806480u);
+        odd = debias(((x >> 8) & 0x00ff00ffu) ^ 0x64806480u);
     }
-    __device__ __forceinline__ static uint32_t odd(uint32_t x) {
-        return debias(((x >> 8) & 0x00ff00ffu) ^ 0x64806480u);
-    }
+    __device__ __forceinline__ static void k_pairs(uint32_t x, uint32_t &k0, uint32_t &k1) { even_odd(x, k0, k1); }
     __device__ __forceinline__ static float one(uint8_t c) { return (float)(int8_t)c; }
     __device__ __forceinline__ static uint8_t code(float y) {
         return (uint8_t)(int8_t)max(-127, min(127, __float2int_rn(y)));

@@ -365,8 +365,7 @@ ATTN_API int attn_bwd_varlen(const void *q, const void *k, const void *v, const 
  * where an element of row r of a page stands for code * scale[page, r / block_size,
  * head]: one scale for each block of block_size tokens (a power of two up to
  * page_size) and head.  cache_dtype ATTN_CACHE_INT8 holds -127..127,
- * ATTN_CACHE_E4M3 the e4m3 values up to +-448 (the NaN code is never written and
- * reads as +-480).  Block tables and lengths as in attn_fwd_paged.
+ * ATTN_CACHE_E4M3 the e4m3 values up to +-448 (the NaN code is never written).  Block tables and lengths as in attn_fwd_paged.
  *
  * attn_cache_append -- writes N new rows of each sequence behind the seqlens_k
  * rows it has (seqlens_k is not changed: the caller adds the new rows to it).
