@@ -51,6 +51,8 @@ def library_path() -> str:
 def load_library(path: str | None = None):
     """Load libattn_gqa.so (built in-tree by ``build_ext.build()``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

@@ -27,65 +27,74 @@ import math
 
 import torch
 
-from .binding import (_DTYPE_CODE, ALGOS, MASKS, _check, _check_tensor, _ptr, load_library)
+from .binding import _DTYPE_CODE, ALGOS, MASKS, _check, _check_tensor, load_library
 
 ATTN_CACHE_E4M3, ATTN_CACHE_INT8 = 0, 1
 _CACHE_CODE = {torch.float8_e4m3fn: ATTN_CACHE_E4M3, torch.int8: ATTN_CACHE_INT8}
 
 
-class _Launch:
-    """The device and stream of a call: ``dev`` is made current while the
-    library runs (it works on the current device), and outputs that the call
-    allocates belong to its stream."""
-
-    def __init__(self, dev, stream):
-        if dev.type != "cuda":
-            raise ValueError(f"the tensors are on {dev}: the library runs on CUDA devices only")
-        if stream is not None and stream.device != dev:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-        self.stream, self.guard, self.dev = stream, None, dev
-
-    def __enter__(self):
-        if self.stream is not None:  # makes its device current, too
-            self.guard = torch.cuda.stream(self.stream)
-            self.guard.__enter__()
-            return ctypes.c_void_p(self.stream.cuda_stream)
-        if torch.cuda.current_device() != self.dev.index:
-            self.guard = torch.cuda.device(self.dev)
-            self.guard.__enter__()
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _raw_stream(i):
+    """The handle of device ``i``'s current stream (what
+    torch.cuda.current_stream(i).cuda_stream is, without the object: 0.1 us
+    against 2.9)."""
+    return torch._C._cuda_getCurrentRawStream(i)
 
 
-def _check_cache(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, dev):
-    """Checks a cache; returns (P, page, block, Hkv, D, Dv, B, max_pages, code)."""
+def _here(dev, stream):
+    """Whether a call on ``dev`` can go to the current stream as it is.
+    (Otherwise the entry points call themselves with ``_elsewhere`` in force.)"""
+    return stream is None and dev.type == "cuda" and dev.index == torch.cuda.current_device()
+
+
+def _elsewhere(dev, stream):
+    """Makes ``dev`` and ``stream`` current: the library works on the current
+    device, and outputs that a call allocates belong to its stream."""
+    if dev.type != "cuda":
+        raise ValueError(f"the tensors are on {dev}: the library runs on CUDA devices only")
+    if stream is None:
+        return torch.cuda.device(dev)
+    if stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    return torch.cuda.stream(stream)
+
+
+def _tensor(name, t, dtype, shape, dev):
+    """Checks one tensor; returns its address."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == dev:
+        return t.data_ptr()
+    n = 1
+    for x in shape:
+        n *= x
+    _check_tensor(name, t, dtype, n, dev)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _cache(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, dev):
+    """Checks a cache; returns its addresses (k_pages, v_pages, k_scale,
+    v_scale, block_table, seqlens_k), sizes (P, page, block, Hkv, D, Dv, B,
+    max_pages) and code."""
+    code = _CACHE_CODE.get(k_pages.dtype)
+    if code is None:
+        raise TypeError(f"k_pages: dtype {k_pages.dtype}, expected torch.int8 or "
+                        "torch.float8_e4m3fn")
     if k_pages.dim() != 4 or v_pages.dim() != 4 or k_scale.dim() != 3 or block_table.dim() != 2:
         raise ValueError("pages are [P, page, Hkv, D], scales [P, page / block, Hkv] and the "
                          "block table [B, max_pages]")
-    if k_pages.dtype not in _CACHE_CODE:
-        raise TypeError(f"k_pages: dtype {k_pages.dtype}, expected torch.int8 or "
-                        "torch.float8_e4m3fn")
     P, page, Hkv, D = k_pages.shape
     Dv, nblk = v_pages.shape[3], k_scale.shape[1]
-    B, max_pages = block_table.shape
-    if tuple(v_pages.shape) != (P, page, Hkv, Dv):
-        raise ValueError(f"v_pages: shape {tuple(v_pages.shape)} beside k_pages "
-                         f"{tuple(k_pages.shape)}")
+    B, M = block_table.shape
     if nblk < 1 or page % nblk:
         raise ValueError(f"k_scale: {nblk} blocks do not divide a page of {page} tokens")
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if tuple(t.shape) != (P, nblk, Hkv):
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(P, nblk, Hkv)}")
-    _check_tensor("k_pages", k_pages, k_pages.dtype, P * page * Hkv * D, dev)
-    _check_tensor("v_pages", v_pages, k_pages.dtype, P * page * Hkv * Dv, dev)
-    _check_tensor("k_scale", k_scale, torch.float32, P * nblk * Hkv, dev)
-    _check_tensor("v_scale", v_scale, torch.float32, P * nblk * Hkv, dev)
-    _check_tensor("block_table", block_table, torch.int32, B * max_pages, dev)
-    _check_tensor("seqlens_k", seqlens_k, torch.int32, B, dev)
-    return P, page, page // nblk, Hkv, D, Dv, B, max_pages, _CACHE_CODE[k_pages.dtype]
+    scales = (P, nblk, Hkv)
+    ptrs = (_tensor("k_pages", k_pages, k_pages.dtype, (P, page, Hkv, D), dev),
+            _tensor("v_pages", v_pages, k_pages.dtype, (P, page, Hkv, Dv), dev),
+            _tensor("k_scale", k_scale, torch.float32, scales, dev),
+            _tensor("v_scale", v_scale, torch.float32, scales, dev),
+            _tensor("block_table", block_table, torch.int32, (B, M), dev),
+            _tensor("seqlens_k", seqlens_k, torch.int32, (B,), dev))
+    return ptrs, (P, page, page // nblk, Hkv, D, Dv, B, M), code
 
 
 def attn_cache_append(k, v, k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, *,
@@ -94,24 +103,27 @@ def attn_cache_append(k, v, k_pages, v_pages, k_scale, v_scale, block_table, seq
     the cache behind the ``seqlens_k`` rows each sequence has; ``seqlens_new``
     int32 [B]: how many of the N are there (default: all).  The pages they go to
     are in ``block_table`` already.  ``seqlens_k`` is not changed."""
-    lib = load_library()
     dev = k.device
-    P, page, block, Hkv, D, Dv, B, M, code = _check_cache(k_pages, v_pages, k_scale, v_scale,
-                                                          block_table, seqlens_k, dev)
-    if k.dim() != 4 or k.shape[0] != B or tuple(k.shape[2:]) != (Hkv, D):
+    (kp, vp, ks, vs, table, lens), (P, page, block, Hkv, D, Dv, B, M), code = _cache(
+        k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, dev)
+    if k.dim() != 4 or k.shape[0] != B or k.shape[2:] != (Hkv, D):
         raise ValueError(f"k: shape {tuple(k.shape)}, expected [{B}, N, {Hkv}, {D}]")
-    if k.dtype not in _DTYPE_CODE:
+    dtype = _DTYPE_CODE.get(k.dtype)
+    if dtype is None:
         raise TypeError(f"k: dtype {k.dtype}, expected float32, float16 or bfloat16")
     N = k.shape[1]
-    _check_tensor("k", k, k.dtype, B * N * Hkv * D, dev)
-    _check_tensor("v", v, k.dtype, B * N * Hkv * Dv, dev)
+    kx = _tensor("k", k, k.dtype, (B, N, Hkv, D), dev)
+    vx = _tensor("v", v, k.dtype, (B, N, Hkv, Dv), dev)
+    new = None
     if seqlens_new is not None:
-        _check_tensor("seqlens_new", seqlens_new, torch.int32, B, dev)
-    with _Launch(dev, stream) as st:
-        _check(lib.attn_cache_append(_ptr(k), _ptr(v), _ptr(k_pages), _ptr(v_pages),
-                                     _ptr(k_scale), _ptr(v_scale), B, N, Hkv, D, Dv,
-                                     _ptr(seqlens_new), _ptr(seqlens_k), _ptr(block_table), M,
-                                     page, P, block, code, _DTYPE_CODE[k.dtype], st))
+        new = _tensor("seqlens_new", seqlens_new, torch.int32, (B,), dev)
+    if not _here(dev, stream):
+        with _elsewhere(dev, stream):
+            return attn_cache_append(k, v, k_pages, v_pages, k_scale, v_scale, block_table,
+                                     seqlens_k, seqlens_new=seqlens_new)
+    _check(load_library().attn_cache_append(kx, vx, kp, vp, ks, vs, B, N, Hkv, D, Dv, new, lens,
+                                            table, M, page, P, block, code, dtype,
+                                            _raw_stream(dev.index)))
 
 
 def attn_cache_append_varlen(k, v, cu_seqlens_new, max_new, k_pages, v_pages, k_scale, v_scale,
@@ -119,24 +131,25 @@ def attn_cache_append_varlen(k, v, cu_seqlens_new, max_new, k_pages, v_pages, k_
     """attn_cache_append with the new rows packed: k [T,Hkv,D], v [T,Hkv,Dv],
     sequence b's rows [cu_seqlens_new[b], cu_seqlens_new[b + 1]), at most
     ``max_new`` of them."""
-    lib = load_library()
     dev = k.device
-    P, page, block, Hkv, D, Dv, B, M, code = _check_cache(k_pages, v_pages, k_scale, v_scale,
-                                                          block_table, seqlens_k, dev)
-    if k.dim() != 3 or tuple(k.shape[1:]) != (Hkv, D):
+    (kp, vp, ks, vs, table, lens), (P, page, block, Hkv, D, Dv, B, M), code = _cache(
+        k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, dev)
+    if k.dim() != 3 or k.shape[1:] != (Hkv, D):
         raise ValueError(f"k: shape {tuple(k.shape)}, expected [T, {Hkv}, {D}]")
-    if k.dtype not in _DTYPE_CODE:
+    dtype = _DTYPE_CODE.get(k.dtype)
+    if dtype is None:
         raise TypeError(f"k: dtype {k.dtype}, expected float32, float16 or bfloat16")
     T = k.shape[0]
-    _check_tensor("k", k, k.dtype, T * Hkv * D, dev)
-    _check_tensor("v", v, k.dtype, T * Hkv * Dv, dev)
-    _check_tensor("cu_seqlens_new", cu_seqlens_new, torch.int32, B + 1, dev)
-    with _Launch(dev, stream) as st:
-        _check(lib.attn_cache_append_varlen(_ptr(k), _ptr(v), _ptr(k_pages), _ptr(v_pages),
-                                            _ptr(k_scale), _ptr(v_scale), B, T, int(max_new),
-                                            Hkv, D, Dv, _ptr(cu_seqlens_new), _ptr(seqlens_k),
-                                            _ptr(block_table), M, page, P, block, code,
-                                            _DTYPE_CODE[k.dtype], st))
+    kx = _tensor("k", k, k.dtype, (T, Hkv, D), dev)
+    vx = _tensor("v", v, k.dtype, (T, Hkv, Dv), dev)
+    cu = _tensor("cu_seqlens_new", cu_seqlens_new, torch.int32, (B + 1,), dev)
+    if not _here(dev, stream):
+        with _elsewhere(dev, stream):
+            return attn_cache_append_varlen(k, v, cu_seqlens_new, max_new, k_pages, v_pages,
+                                            k_scale, v_scale, block_table, seqlens_k)
+    _check(load_library().attn_cache_append_varlen(kx, vx, kp, vp, ks, vs, B, T, int(max_new), Hkv,
+                                                   D, Dv, cu, lens, table, M, page, P, block, code,
+                                                   dtype, _raw_stream(dev.index)))
 
 
 def attn_fwd_paged_q8(q, k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, o=None,
@@ -145,40 +158,40 @@ def attn_fwd_paged_q8(q, k_pages, v_pages, k_scale, v_scale, block_table, seqlen
     """attn_fwd_paged over an 8-bit cache: q [B,Q,Hq,D]; ``seqlens_k`` counts the
     keys to attend to (append first).  Returns (o [B,Q,Hq,Dv], lse [B,Q,Hq] or
     None)."""
-    lib = load_library()
     dev = q.device
-    P, page, block, Hkv, D, Dv, B, M, code = _check_cache(k_pages, v_pages, k_scale, v_scale,
-                                                          block_table, seqlens_k, dev)
+    (kp, vp, ks, vs, table, lens), (P, page, block, Hkv, D, Dv, B, M), code = _cache(
+        k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, dev)
     if q.dim() != 4 or q.shape[0] != B or q.shape[3] != D:
         raise ValueError(f"q: shape {tuple(q.shape)}, expected [{B}, Q, Hq, {D}]")
-    if q.dtype not in _DTYPE_CODE:
+    dtype = _DTYPE_CODE.get(q.dtype)
+    if dtype is None:
         raise TypeError(f"q: dtype {q.dtype}, expected float32, float16 or bfloat16")
     Q, Hq = q.shape[1], q.shape[2]
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    with _Launch(dev, stream) as st:
-        if o is None:
-            o = torch.empty((B, Q, Hq, Dv), dtype=q.dtype, device=dev)
-        if lse is None and want_lse:
-            lse = torch.empty((B, Q, Hq), dtype=torch.float32, device=dev)
-        _check_tensor("q", q, q.dtype, B * Q * Hq * D, dev)
-        _check_tensor("o", o, q.dtype, B * Q * Hq * Dv, dev)
-        if lse is not None:
-            _check_tensor("lse", lse, torch.float32, B * Q * Hq, dev)
-        if seqlens_q is not None:
-            _check_tensor("seqlens_q", seqlens_q, torch.int32, B, dev)
-        _check(lib.attn_fwd_paged_q8(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale),
-                                     _ptr(v_scale), _ptr(o), _ptr(lse), B, Hq, Hkv, Q, D, Dv,
-                                     _ptr(block_table), M, page, P, block, code,
-                                     _ptr(seqlens_q), _ptr(seqlens_k), int(window), float(scale),
-                                     MASKS[mask], _DTYPE_CODE[q.dtype], ALGOS[algo], st))
+    if not _here(dev, stream):
+        with _elsewhere(dev, stream):
+            return attn_fwd_paged_q8(q, k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k,
+                                     o, lse, seqlens_q=seqlens_q, window=window, scale=scale,
+                                     algo=algo, mask=mask, want_lse=want_lse)
+    qx = _tensor("q", q, q.dtype, (B, Q, Hq, D), dev)
+    if o is None:
+        o = (torch.empty_like(q) if D == Dv else
+             torch.empty((B, Q, Hq, Dv), dtype=q.dtype, device=dev))
+    if lse is None and want_lse:
+        lse = torch.empty((B, Q, Hq), dtype=torch.float32, device=dev)
+    ox = _tensor("o", o, q.dtype, (B, Q, Hq, Dv), dev)
+    lx = None if lse is None else _tensor("lse", lse, torch.float32, (B, Q, Hq), dev)
+    sq = None if seqlens_q is None else _tensor("seqlens_q", seqlens_q, torch.int32, (B,), dev)
+    _check(load_library().attn_fwd_paged_q8(
+        qx, kp, vp, ks, vs, ox, lx, B, Hq, Hkv, Q, D, Dv, table, M, page, P, block, code, sq, lens,
+        int(window), 1.0 / math.sqrt(D) if scale is None else float(scale), MASKS[mask], dtype,
+        ALGOS[algo], _raw_stream(dev.index)))
     return o, lse
 
 
 def _pool_arrays(pools, pages, dev, what):
     """Pointers and page bytes of pools whose first axis counts ``pages`` pages."""
     n = len(pools)
-    ptrs, sizes = (ctypes.c_void_p * max(n, 1))(), (ctypes.c_longlong * max(n, 1))()
+    ptrs, sizes = [0] * n, [0] * n
     for i, t in enumerate(pools):
         if t.dim() < 1 or t.shape[0] != pages:
             raise ValueError(f"{what}[{i}]: shape {tuple(t.shape)}, expected {pages} pages first")
@@ -187,8 +200,8 @@ def _pool_arrays(pools, pages, dev, what):
         if t.device != dev:
             raise ValueError(f"{what}[{i}] is on {t.device}, expected {dev}")
         ptrs[i] = t.data_ptr()
-        sizes[i] = t.numel() // pages * t.element_size()
-    return ptrs, sizes, n
+        sizes[i] = t.nbytes // max(pages, 1)
+    return (ctypes.c_void_p * max(n, 1))(*ptrs), (ctypes.c_longlong * max(n, 1))(*sizes), n
 
 
 def attn_pages_copy(src_pools, dst_pools, src, dst, *, stream=None):
@@ -197,21 +210,26 @@ def attn_pages_copy(src_pools, dst_pools, src, dst, *, stream=None):
     ``src``, ``dst``: int32 [n]; the dst pages are distinct, and none of them is
     a src page of the same pool.  Pairs with a page that does not exist are
     skipped."""
-    lib = load_library()
     dev = src.device
     if len(src_pools) != len(dst_pools):
         raise ValueError(f"{len(src_pools)} source pools and {len(dst_pools)} destinations")
     n = src.numel()
-    _check_tensor("src", src, torch.int32, n, dev)
-    _check_tensor("dst", dst, torch.int32, n, dev)
+    sx = _tensor("src", src, torch.int32, (n,), dev)
+    dx = _tensor("dst", dst, torch.int32, (n,), dev)
     sp = src_pools[0].shape[0] if len(src_pools) else 0
     dp = dst_pools[0].shape[0] if len(dst_pools) else 0
     sptr, sbytes, npools = _pool_arrays(src_pools, sp, dev, "src_pools")
-    dptr, dbytes, _ = _pool_arrays(dst_pools, dp, dev, "dst_pools")
-    if any(sbytes[i] != dbytes[i] for i in range(npools)):
-        raise ValueError("the pages of a source pool and of its destination differ in size")
-    with _Launch(dev, stream) as st:
-        _check(lib.attn_pages_copy(sptr, dptr, sbytes, npools, sp, dp, _ptr(src), _ptr(dst), n, st))
+    if dst_pools is src_pools:
+        dptr = sptr
+    else:
+        dptr, dbytes, _ = _pool_arrays(dst_pools, dp, dev, "dst_pools")
+        if list(sbytes) != list(dbytes):
+            raise ValueError("the pages of a source pool and of its destination differ in size")
+    if not _here(dev, stream):
+        with _elsewhere(dev, stream):
+            return attn_pages_copy(src_pools, dst_pools, src, dst)
+    _check(load_library().attn_pages_copy(sptr, dptr, sbytes, npools, sp, dp, sx, dx, n,
+                                          _raw_stream(dev.index)))
 
 
 def attn_pages_fork(pools, block_table, seqlens, refcount, parents, page_size, *, new_tokens=None,
@@ -227,27 +245,27 @@ def attn_pages_fork(pools, block_table, seqlens, refcount, parents, page_size, *
     new tensors; status: pages that were missing, slots that do not fit
     max_pages, pages taken, pages copied.  Where one of the first two is not 0,
     nothing was copied, the new table is empty and the old version still stands."""
-    lib = load_library()
     dev = block_table.device
     S, M = block_table.shape
     P, N = refcount.numel(), parents.numel()
-    _check_tensor("block_table", block_table, torch.int32, S * M, dev)
-    _check_tensor("seqlens", seqlens, torch.int32, S, dev)
-    _check_tensor("refcount", refcount, torch.int32, P, dev)
-    _check_tensor("parents", parents, torch.int32, N, dev)
-    if new_tokens is not None:
-        _check_tensor("new_tokens", new_tokens, torch.int32, N, dev)
+    tx = _tensor("block_table", block_table, torch.int32, (S, M), dev)
+    lx = _tensor("seqlens", seqlens, torch.int32, (S,), dev)
+    rx = _tensor("refcount", refcount, torch.int32, (P,), dev)
+    px = _tensor("parents", parents, torch.int32, (N,), dev)
+    nx = None if new_tokens is None else _tensor("new_tokens", new_tokens, torch.int32, (N,), dev)
     ptrs, sizes, npools = _pool_arrays(pools, P, dev, "pools")
-    with _Launch(dev, stream) as st:
-        table_out = torch.empty((N, M), dtype=torch.int32, device=dev)
-        lens_out = torch.empty((N,), dtype=torch.int32, device=dev)
-        refs_out = torch.empty((P,), dtype=torch.int32, device=dev)
-        status = torch.empty((4,), dtype=torch.int32, device=dev)
-        _check(lib.attn_pages_fork(ptrs, sizes, npools, _ptr(block_table), _ptr(seqlens),
-                                   _ptr(refcount), S, M, P, int(page_size), _ptr(parents),
-                                   _ptr(new_tokens), N, _ptr(table_out), _ptr(lens_out),
-                                   _ptr(refs_out), _ptr(status), st))
-    return table_out, lens_out, refs_out, status
+    if not _here(dev, stream):
+        with _elsewhere(dev, stream):
+            return attn_pages_fork(pools, block_table, seqlens, refcount, parents, page_size,
+                                   new_tokens=new_tokens)
+    # one allocation: the new version's table, lengths, counts, and the status
+    out = torch.empty((N * M + N + P + 4,), dtype=torch.int32, device=dev)
+    table_out, lens_out, refs_out, status = out.split((N * M, N, P, 4))
+    at = out.data_ptr()
+    _check(load_library().attn_pages_fork(
+        ptrs, sizes, npools, tx, lx, rx, S, M, P, int(page_size), px, nx, N, at, at + 4 * N * M,
+        at + 4 * (N * M + N), at + 4 * (N * M + N + P), _raw_stream(dev.index)))
+    return table_out.view(N, M), lens_out, refs_out, status
 
 
 def attn_pages_compact(pools, block_table, refcount, *, stream=None):
@@ -255,19 +273,19 @@ def attn_pages_compact(pools, block_table, refcount, *, stream=None):
     pool, in place, and renumbers them: returns (block_table, refcount, remap
     [P], n_live []), new tensors; remap: a live page's new number, -1 for a free
     one."""
-    lib = load_library()
     dev = block_table.device
     S, M = block_table.shape
     P = refcount.numel()
-    _check_tensor("block_table", block_table, torch.int32, S * M, dev)
-    _check_tensor("refcount", refcount, torch.int32, P, dev)
+    tx = _tensor("block_table", block_table, torch.int32, (S, M), dev)
+    rx = _tensor("refcount", refcount, torch.int32, (P,), dev)
     ptrs, sizes, npools = _pool_arrays(pools, P, dev, "pools")
-    with _Launch(dev, stream) as st:
-        table_out = torch.empty((S, M), dtype=torch.int32, device=dev)
-        refs_out = torch.empty((P,), dtype=torch.int32, device=dev)
-        remap = torch.empty((P,), dtype=torch.int32, device=dev)
-        n_live = torch.empty((), dtype=torch.int32, device=dev)
-        _check(lib.attn_pages_compact(ptrs, sizes, npools, _ptr(block_table), _ptr(refcount), S, M,
-                                      P, _ptr(table_out), _ptr(refs_out), _ptr(remap),
-                                      _ptr(n_live), st))
-    return table_out, refs_out, remap, n_live
+    if not _here(dev, stream):
+        with _elsewhere(dev, stream):
+            return attn_pages_compact(pools, block_table, refcount)
+    out = torch.empty((S * M + 2 * P + 1,), dtype=torch.int32, device=dev)
+    table_out, refs_out, remap, n_live = out.split((S * M, P, P, 1))
+    at = out.data_ptr()
+    _check(load_library().attn_pages_compact(
+        ptrs, sizes, npools, tx, rx, S, M, P, at, at + 4 * S * M, at + 4 * (S * M + P),
+        at + 4 * (S * M + 2 * P), _raw_stream(dev.index)))
+    return table_out.view(S, M), refs_out, remap, n_live.view(())
