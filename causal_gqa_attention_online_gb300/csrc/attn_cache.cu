@@ -90,6 +90,7 @@ int append_common(const void *k, const void *v, void *k_pages, void *v_pages, fl
 
 // f's launches with a workspace from the library's pool.
 template <typename F> int with_workspace(unsigned long long bytes, cudaStream_t stream, F f) {
+    if (bytes == 0) return f(static_cast<void *>(nullptr));
     int dev = 0;
     int rc = current_device(&dev);
     if (rc) return rc;

@@ -44,11 +44,16 @@
 // share is written out by its CTA; shares that begin or end inside one leave a
 // partial each (at most two a CTA, so the workspace does not grow with the
 // keys), and the merge kernel, a block for each place where a share begins
-// inside a sequence, head and row, joins those.
+// inside a sequence, head and row, joins those.  Small problems (at most four
+// tiles a CTA with every CTA resident) give each (sequence, head) a cluster of up
+// to eight CTAs, which split its tiles and join their states through distributed
+// shared memory: one launch and no workspace.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
 #include <climits>
+
+#include <cooperative_groups.h>
 #include <cstring>
 #include <type_traits>
 
@@ -72,6 +77,7 @@ struct Q8Args {
     int box_rows;  // rows of a TMA box: min(page_size, 64)
     int box_shift;
     bool bf16;
+    int cluster;   // CTAs of a (sequence, head), or 0: shares
     int shares;    // shares at most (no more than there are tiles are used)
     // workspace: for each share {sequence, its first share, its last} where the
     // merge of a sequence is found (its second share; {-1} elsewhere), partials
@@ -132,6 +138,78 @@ __device__ __forceinline__ long long share_at(long long t, long long T, long lon
     return ((t + 1) * n - 1) / T;
 }
 
+// Four columns of a joined row: acc / sum, and its LSE from the log2 sums' maximum
+// (a row without keys: +0 and -inf; one with a NaN key: NaN).
+__device__ __forceinline__ void put_row(const Q8Args &a, int b, int kvh, int row, int c, const float4 &acc,
+                                        float sum, float mx) {
+    const AttnParams &p = a.p;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const long long orow = ((long long)b * p.Q + row / p.G) * p.Hq + kvh * p.G + row % p.G;
+    uint2 w;
+    if (a.bf16) {
+        w.x = MmaOp<__nv_bfloat16>::pack(acc.x * inv, acc.y * inv);
+        w.y = MmaOp<__nv_bfloat16>::pack(acc.z * inv, acc.w * inv);
+    } else {
+        w.x = MmaOp<__half>::pack(acc.x * inv, acc.y * inv);
+        w.y = MmaOp<__half>::pack(acc.z * inv, acc.w * inv);
+    }
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) + orow * p.Dv + 4 * c) = w;
+    if (c == 0 && p.lse)
+        p.lse[orow] = sum != sum ? sum : sum > 0.f ? (mx + __log2f(sum)) * kLn2 : -INFINITY;
+}
+
+// The rows of a sequence without keys, by a warp: +0 and -inf.
+__device__ __forceinline__ void empty_rows(const Q8Args &a, int b, int kvh, int lane) {
+    const AttnParams &p = a.p;
+    const int c8 = p.Dv / 8;
+    for (int i = lane; i < p.Q * p.G * c8; i += 32) {
+        const int row = i / c8, c = i - row * c8;
+        const long long orow = ((long long)b * p.Q + row / p.G) * p.Hq + kvh * p.G + row % p.G;
+        reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.o) + orow * p.Dv)[c] = make_uint4(0, 0, 0, 0);
+        if (c == 0 && p.lse) p.lse[orow] = -INFINITY;
+    }
+}
+
+// The joint rows of a cluster's CTAs, whose own are at xrow [R][DP] and xlse [R] of
+// each: four columns a thread, the (row, column) pairs spread over the CTAs.  (A
+// function of its own, so that its registers do not add to the main loop's.)
+template <int DP>
+__device__ __noinline__ void join_cluster(const Q8Args &a, int b, int kvh, int rank, int ntiles, float *xrow,
+                                          float *xlse) {
+    const AttnParams &p = a.p;
+    auto cluster = cooperative_groups::this_cluster();
+    const int C = a.cluster, C4 = p.Dv / 4;
+    for (int i = rank * kThreads + threadIdx.x; i < p.Q * p.G * C4; i += C * kThreads) {
+        const int row = i / C4, c = i - row * C4;
+        float lw[8], mx = -INFINITY;
+        float4 v[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            lw[r] = -INFINITY;
+            v[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+            // (a CTA without tiles has no rows)
+            if (r < C && (r + 1) * ntiles / C > r * ntiles / C) {
+                lw[r] = cluster.map_shared_rank(xlse, r)[row];
+                v[r] = *reinterpret_cast<const float4 *>(cluster.map_shared_rank(xrow, r) + row * DP + 4 * c);
+            }
+            mx = fmaxf(mx, lw[r]);
+        }
+        const float mref = mx == -INFINITY ? 0.f : mx;
+        float sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            const float w = exp2f(lw[r] - mref);
+            sum += w;
+            acc.x = fmaf(w, v[r].x, acc.x);
+            acc.y = fmaf(w, v[r].y, acc.y);
+            acc.z = fmaf(w, v[r].z, acc.z);
+            acc.w = fmaf(w, v[r].w, acc.w);
+        }
+        put_row(a, b, kvh, row, c, acc, sum, mx);
+    }
+}
+
 template <int CODE, int DP, int NT>
 __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
     q8_decode_kernel(const __grid_constant__ Q8Args a, const __grid_constant__ CUtensorMap tmK,
@@ -144,7 +222,11 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
     const AttnParams &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, tig = lane & 3;
-    const int share_i = blockIdx.x / p.Hkv, kvh = blockIdx.x - share_i * p.Hkv;
+    // shares: CTA (share, head); clusters: (sequence, head, rank)
+    const int C = a.cluster;
+    const int xi = C ? blockIdx.x / C : blockIdx.x;
+    const int share_i = xi / p.Hkv, kvh = xi - share_i * p.Hkv;
+    const int rank = C ? blockIdx.x - xi * C : 0;
     const uint32_t sbase = smem_u32(smem);
     const uint32_t full = sbase + L::BARS, empty = full + 8 * NS;
     long long *share = reinterpret_cast<long long *>(smem + L::SHARE);
@@ -163,6 +245,8 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
             sm100::tma_prefetch_desc(&tmK);
             sm100::tma_prefetch_desc(&tmV);
         }
+    }
+    if (C == 0 && warp == 4) {
         // this CTA's share of the tiles of all sequences, and where it begins
         long long T = 0;
         int n0 = 0;  // of the first 32 sequences
@@ -209,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
             share[0] = left;
             if (left == 0 && kvh == 0) a.seam[share_i] = make_int4(-1, 0, 0, 0);
         }
-    } else {
+    } else if (C == 0) {
         // meanwhile: the rows of sequences without keys, +0 and -inf (each lane
         // looks at one of the CTA's sequences and heads, the warp writes)
         const long long units = (long long)p.B * p.Hkv;
@@ -218,21 +302,30 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
             unsigned todo = __ballot_sync(0xffffffffu, x < units && unit_of(a, (int)(x / p.Hkv)).ntiles == 0);
             for (; todo; todo &= todo - 1) {
                 const long long y = x0 + (long long)(__ffs(todo) - 1) * gridDim.x;
-                const int b = (int)(y / p.Hkv), h0 = (int)(y - (long long)b * p.Hkv) * p.G, c8 = p.Dv / 8;
-                for (int i = lane; i < p.Q * p.G * c8; i += 32) {
-                    const int row = i / c8, c = i - row * c8;
-                    const long long orow = ((long long)b * p.Q + row / p.G) * p.Hq + h0 + row % p.G;
-                    reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.o) + orow * p.Dv)[c] = make_uint4(0, 0, 0, 0);
-                    if (c == 0 && p.lse) p.lse[orow] = -INFINITY;
-                }
+                empty_rows(a, (int)(y / p.Hkv), (int)(y % p.Hkv), lane);
             }
         }
     }
+    UnitKeys un;
+    if (C) un = unit_of(a, share_i);
     __syncthreads();
-    long long left = share[0];
-    if (left == 0) return;
-    int b = (int)share[1], tile = (int)share[2];
-    UnitKeys un = unit_of(a, b);
+    long long left;
+    int b, tile;
+    if (C) {
+        b = share_i;
+        if (un.ntiles == 0) {  // (so it is for the whole cluster)
+            if (rank == 0 && warp == 0) empty_rows(a, b, kvh, lane);
+            return;
+        }
+        tile = (int)share_begin(rank, un.ntiles, C);
+        left = (int)share_begin(rank + 1, un.ntiles, C) - tile;
+    } else {
+        left = share[0];
+        if (left == 0) return;
+        b = (int)share[1];
+        tile = (int)share[2];
+        un = unit_of(a, b);
+    }
     // the next sequence that has tiles
     auto advance = [&]() {
         tile = 0;
@@ -309,10 +402,12 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
         cp_async_wait<0>();
         for (uint32_t k = it > (uint32_t)NS ? it - NS : 0; k < it; ++k)
             sm100::mbar_wait_drain(full + 8 * (k % NS), (k / NS) & 1u);
-        return;
+        if (C <= 1) return;
     }
 
     // --------------------------------------------------------------- consumers
+    // (clusters: the CTA's rows and log2 sums in the drained ring)
+    float *xrow = reinterpret_cast<float *>(smem), *xlse = xrow + R * DP;
     const int G = p.G;
     const int nrows = p.Q * G;  // rows of a unit (<= R)
     const int kw0 = warp * 32;
@@ -321,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
     float *mbuf = reinterpret_cast<float *>(smem + L::MERGE);
     uint32_t it = 0;
     bool ok = true;
-    for (bool first_seg = true; left > 0; first_seg = false) {
+    for (bool first_seg = true; left > 0 && warp < 4; first_seg = false) {
         const int n = (int)min((long long)(un.ntiles - tile), left);
         const int nvalid = un.si.Qb * G;
         // Q^T fragments (B operand of S^T): column n = row g; in each 16 columns
@@ -580,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
         if (lane == 0) stat_u[warp] = u;
         // the four warps go on or give up together
         ok = sm100::bar_red_and(1, 128, ok);
-        if (!ok) return;
+        if (!ok) break;
         const float U = fmaxf(fmaxf(stat_u[0], stat_u[1]), fmaxf(stat_u[2], stat_u[3]));
         const float to_u = U > 0.f ? u / U : 1.f;
         float M[NT][2], Lsum[NT][2];
@@ -641,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
         // A whole unit goes out; a piece of one becomes a partial, the CTA's first
         // or its last.
         if (warp == 0) {
-            const bool whole = n == un.ntiles;
+            const bool whole = n == un.ntiles && C <= 1;
             const long long slot = 2LL * blockIdx.x + (first_seg ? 0 : 1);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -667,21 +762,26 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
                             }
                         if (g == 0 && p.lse) p.lse[orow] = lse2 * kLn2;
                     } else {
-                        const long long prow = slot * R + row;
-                        float *dst = a.part_o + prow * p.Dv + 2 * g;
+                        const long long prow = C ? row : slot * R + row;
+                        float *dst = C ? xrow + row * DP + 2 * g : a.part_o + prow * p.Dv + 2 * g;
 #pragma unroll
                         for (int mt = 0; mt < DP / 16; ++mt)
                             if (mt * 16 < p.Dv)
                                 *reinterpret_cast<float2 *>(dst + mt * 16) = make_float2(
                                     oacc[mt][nt][e] * inv * unit, oacc[mt][nt][2 + e] * inv * unit);
                         // (+inf, so that the merge's maximum does not pass a NaN by)
-                        if (g == 0) a.part_lse[prow] = lse2 != lse2 ? INFINITY : lse2;
+                        if (g == 0) (C ? xlse : a.part_lse)[prow] = lse2 != lse2 ? INFINITY : lse2;
                     }
                 }
         }
         left -= n;
         if (left > 0) advance();
     }
+    if (C <= 1) return;
+
+    cooperative_groups::this_cluster().sync();
+    join_cluster<DP>(a, b, kvh, rank, un.ntiles, xrow, xlse);
+    cooperative_groups::this_cluster().sync();  // every CTA's rows are read before it exits
 }
 
 // Joins the partials of a sequence that spans several shares, one row a block:
@@ -708,51 +808,64 @@ __global__ void __launch_bounds__(kMergeThreads) q8_merge_kernel(const __grid_co
         const long long cta = (long long)(seam.y + i) * p.Hkv + kvh;
         return (2 * cta + (i == 0 ? seam.w : 0)) * R + row;
     };
-    float mx = -INFINITY;
-    for (int i = tid & 31; i < np; i += 32) mx = fmaxf(mx, __ldcg(a.part_lse + part(i)));
-    mx = warp_max(mx);
-    const float mref = mx == -INFINITY ? 0.f : mx;
-    float sum = 0.f;
+    // a running maximum a thread, four partials loaded at a time
+    float mx = -INFINITY, sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (grp < ngrp) {
-#pragma unroll 4
-        for (int i = grp; i < np; i += ngrp) {
-            const long long at = part(i);
-            const float w = exp2f(__ldcg(a.part_lse + at) - mref);
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * p.Dv) + c);
-            sum += w;
-            acc.x = fmaf(w, v.x, acc.x);
-            acc.y = fmaf(w, v.y, acc.y);
-            acc.z = fmaf(w, v.z, acc.z);
-            acc.w = fmaf(w, v.w, acc.w);
+        for (int i0 = grp; i0 < np; i0 += 4 * ngrp) {
+            float lw[4];
+            float4 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int i = i0 + k * ngrp;
+                lw[k] = -INFINITY;
+                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i < np) {
+                    const long long at = part(i);
+                    lw[k] = __ldcg(a.part_lse + at);
+                    v[k] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * p.Dv) + c);
+                }
+            }
+            const float mnew = fmaxf(fmaxf(fmaxf(lw[0], lw[1]), fmaxf(lw[2], lw[3])), mx);
+            const float mref = mnew == -INFINITY ? 0.f : mnew;
+            const float f = exp2f(mx - mref);
+            mx = mnew;
+            sum *= f;
+            acc.x *= f;
+            acc.y *= f;
+            acc.z *= f;
+            acc.w *= f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float w = exp2f(lw[k] - mref);
+                sum += w;
+                acc.x = fmaf(w, v[k].x, acc.x);
+                acc.y = fmaf(w, v[k].y, acc.y);
+                acc.z = fmaf(w, v[k].z, acc.z);
+                acc.w = fmaf(w, v[k].w, acc.w);
+            }
         }
     }
-    __shared__ float rsum[kMergeThreads];
+    __shared__ float2 stat[kMergeThreads];  // maximum, sum
     red[tid] = acc;
-    rsum[tid] = sum;
+    stat[tid] = make_float2(mx, sum);
     __syncthreads();
     if (tid < C4) {
-        for (int k = 1; k < ngrp; ++k) {
+        for (int k = 1; k < ngrp; ++k) mx = fmaxf(mx, stat[k * C4 + tid].x);
+        const float mref = mx == -INFINITY ? 0.f : mx;
+        sum = 0.f;
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < ngrp; ++k) {
             const float4 v = red[k * C4 + tid];
-            sum += rsum[k * C4 + tid];
-            acc.x += v.x;
-            acc.y += v.y;
-            acc.z += v.z;
-            acc.w += v.w;
+            const float2 st = stat[k * C4 + tid];
+            const float f = exp2f(st.x - mref);
+            sum = fmaf(st.y, f, sum);
+            acc.x = fmaf(v.x, f, acc.x);
+            acc.y = fmaf(v.y, f, acc.y);
+            acc.z = fmaf(v.z, f, acc.z);
+            acc.w = fmaf(v.w, f, acc.w);
         }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const long long orow = ((long long)seam.x * p.Q + row / p.G) * p.Hq + kvh * p.G + row % p.G;
-        uint2 w;
-        if (a.bf16) {
-            w.x = MmaOp<__nv_bfloat16>::pack(acc.x * inv, acc.y * inv);
-            w.y = MmaOp<__nv_bfloat16>::pack(acc.z * inv, acc.w * inv);
-        } else {
-            w.x = MmaOp<__half>::pack(acc.x * inv, acc.y * inv);
-            w.y = MmaOp<__half>::pack(acc.z * inv, acc.w * inv);
-        }
-        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) + orow * p.Dv + 4 * tid) = w;
-        if (tid == 0 && p.lse)
-            p.lse[orow] = sum != sum ? sum : sum > 0.f ? (mx + __log2f(sum)) * kLn2 : -INFINITY;
+        put_row(a, seam.x, kvh, row, tid, acc, sum, mx);
     }
 }
 
@@ -793,22 +906,33 @@ int launch_t(const Q8Args &a, cudaStream_t stream) {
         set_error("8-bit decode kernel: cudaFuncSetAttribute: %s", cudaGetErrorString(e));
         return 3;
     }
-    kern<<<(unsigned)(a.shares * a.p.Hkv), kThreads, L::SMEM, stream>>>(a, tk, tv);
-    e = cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.cluster ? a.p.B * a.p.Hkv * a.cluster : a.shares * a.p.Hkv));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = L::SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    cfg.attrs = attr;
+    if (a.cluster > 1) {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = a.cluster;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.numAttrs = 1;
+    }
+    e = cudaLaunchKernelEx(&cfg, kern, a, tk, tv);
+    if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) {
         set_error("8-bit decode kernel launch: %s", cudaGetErrorString(e));
         return 3;
     }
     count_launch();
-    if (a.shares == 1) return 0;
-    cudaLaunchConfig_t cfg = {};
+    if (a.cluster || a.shares == 1) return 0;
     cfg.gridDim = dim3((unsigned)((a.shares - 1) * a.p.Hkv * a.p.Q * a.p.G));
     cfg.blockDim = dim3(kMergeThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cfg.dynamicSmemBytes = 0;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, q8_merge_kernel, a, (int)L::R);
     if (e == cudaSuccess) e = cudaGetLastError();
@@ -832,13 +956,25 @@ template <int CODE> int launch_code(const Q8Args &a, cudaStream_t stream) {
     return launch_nt<CODE, 256>(a, stream);
 }
 
+int resident_ctas(const AttnParams &p, int nsm) {
+    return (nsm < 1 ? 1 : nsm) * (p.D > 128 || p.Dv > 128 ? 1 : 2);
+}
+
+// CTAs of a (sequence, head) in cluster mode, 0 for shares: as many as are all
+// resident, and no more than its tiles, when that leaves a CTA at most four.
+int cluster_of(const AttnParams &p, int nsm) {
+    const long long units = (long long)p.B * p.Hkv, tiles = ((long long)p.K + kTile - 1) / kTile;
+    int c = 8;
+    while (c > 1 && (units * c > resident_ctas(p, nsm) || c >= 2 * tiles)) c /= 2;
+    return tiles <= 4 * c && units < (1LL << 31) ? c : 0;
+}
+
 // Shares: as many as give each resident CTA (two an SM up to widths of 128, one
 // above) one of a head; where that is few of them and leaves CTAs over (more
 // than a 40th), four times as many.  No more than the tables' capacity has
 // tiles.
 int shares_of(const AttnParams &p, int nsm) {
-    const int w = p.D > p.Dv ? p.D : p.Dv;
-    const long long ctas = (long long)(nsm < 1 ? 1 : nsm) * (w <= 128 ? 2 : 1);
+    const long long ctas = resident_ctas(p, nsm);
     long long n = ctas / p.Hkv;
     if ((ctas - n * p.Hkv) * 40 > ctas) n = (4 * ctas + p.Hkv - 1) / p.Hkv;
     const long long tiles = (long long)p.B * (((long long)p.K + kTile - 1) / kTile);
@@ -856,6 +992,7 @@ bool q8_decode_supported(const AttnParams &p, int dtype) {
 }
 
 unsigned long long q8_decode_workspace(const AttnParams &p, int nsm) {
+    if (cluster_of(p, nsm)) return 0;
     const unsigned long long shares = shares_of(p, nsm);
     const unsigned long long rows = 2 * shares * p.Hkv * (p.Q * p.G <= 8 ? 8 : 16);
     return shares * sizeof(int4) + rows * 4 * (p.Dv + 1ull);
@@ -870,6 +1007,7 @@ int launch_q8_decode(const AttnParams &p, const Q8Cache &c, int dtype, int nsm, 
     a.box_rows = p.page_size < 64 ? p.page_size : 64;
     a.box_shift = 0;
     while ((1 << a.box_shift) < a.box_rows) ++a.box_shift;
+    a.cluster = cluster_of(p, nsm);
     a.shares = shares_of(p, nsm);
     a.seam = static_cast<int4 *>(ws);
     a.part_o = reinterpret_cast<float *>(a.seam + a.shares);

@@ -285,6 +285,22 @@ def test_attention_of_ragged_batches(i):
                     64, lens, 64, 32, window=int(g.integers(0, 300)) if i % 3 == 0 else 0)
 
 
+@pytest.mark.parametrize("i", range(12))
+def test_attention_of_small_problems(i):
+    """Few tiles a sequence: one to eight CTAs share them in a cluster, some
+    without a tile; empty sequences, windows, fewer keys than rows."""
+    g = np.random.default_rng(700 + i)
+    page = int([8, 16, 64, 128][i % 4])
+    M = int(g.integers(1, max(2, 4000 // page // (1 + i % 5))))
+    B = int(g.integers(1, 5)) if i < 9 else 90
+    lens = [int(n) if g.random() < 0.85 else 0 for n in g.integers(0, M * page + 1, B)]
+    Hkv, G, Q = int(g.integers(1, 5)), int(g.integers(1, 5)), int(g.integers(1, 4))
+    D = int(g.choice([64, 96, 128, 256]))
+    check_attention(g, ["bf16", "f16"][i % 2], ["int8", "e4m3"][i // 2 % 2], B, Hkv * G, Hkv, Q, D,
+                    D, lens, page, 8, window=int(g.integers(1, 200)) if i % 3 == 0 else 0,
+                    max_pages=M, algo="decode")
+
+
 # -------------------------------------------------------------------- append
 
 def run_append(g, dtype, kind, lens, new, N, Hkv, D, Dv, page, block, packed=False, extra_pages=0,
