@@ -20,6 +20,8 @@
 // rows' vectors of eight elements in registers between the two passes, and
 // reads again (from L2) only what a block of more than kKeep vectors a thread
 // leaves over.  Units of few vectors take one warp, others four.
+#include <type_traits>
+
 #include "q8.cuh"
 #include "launch.h"
 
@@ -39,52 +41,103 @@ struct AppendArgs {
     const int32_t *seqlens_new, *seqlens_k, *block_table;
     int max_pages, page_shift, num_pages, nblk, blk_shift;
     int touch;             // blocks a sequence's new rows can touch
+    uint32_t nunits;       // (sequence, block, head, K | V)
 };
 
+// |x| as an unsigned integer of the type's bits: ordered as the magnitudes are,
+// infinity and NaN above every finite value.
+template <typename T> struct Bits;
+template <> struct Bits<float> {
+    static constexpr uint32_t kInf = 0x7f800000u;
+    __device__ __forceinline__ static float value(uint32_t m) { return __uint_as_float(m); }
+};
+template <> struct Bits<__nv_bfloat16> {
+    static constexpr uint32_t kInf = 0x7f80u;
+    __device__ __forceinline__ static float value(uint32_t m) { return __uint_as_float(m << 16); }
+};
+template <> struct Bits<__half> {
+    static constexpr uint32_t kInf = 0x7c00u;
+    __device__ __forceinline__ static float value(uint32_t m) {
+        return __half2float(__ushort_as_half((unsigned short)m));
+    }
+};
+
+// Eight elements.
 template <typename T> struct Vec8 {
-    uint4 r[sizeof(T) / 2];
+    static constexpr int NW = sizeof(T) * 2;  // 32-bit words
+    uint32_t w[NW];
     __device__ __forceinline__ void load(const T *p) {
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) r[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+        for (int i = 0; i < NW / 4; ++i) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+            w[4 * i] = v.x;
+            w[4 * i + 1] = v.y;
+            w[4 * i + 2] = v.z;
+            w[4 * i + 3] = v.w;
+        }
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < NW; ++i) w[i] = 0u;
+    }
+    // the largest magnitude, added to `m`: two 16-bit maxima in a word, or one
+    __device__ __forceinline__ uint32_t max_into(uint32_t m) const {
+#pragma unroll
+        for (int i = 0; i < NW; ++i)
+            m = sizeof(T) == 2 ? __vmaxu2(m, w[i] & 0x7fff7fffu) : max(m, w[i] & 0x7fffffffu);
+        return m;
     }
     __device__ __forceinline__ float at(int i) const {
-        return to_f32<T>(reinterpret_cast<const T *>(r)[i]);
+        return to_f32<T>(reinterpret_cast<const T *>(w)[i]);
     }
 };
 
-template <int TG> __device__ __forceinline__ float group_max(float a, float *red) {
-    a = warp_max(a);
-    if (TG == 32) return a;
-    const int warp = threadIdx.x >> 5;
-    if ((threadIdx.x & 31) == 0) red[warp] = a;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < TG / 32; ++w) a = fmaxf(a, red[w]);
-    return a;
+// Four codes of y0 .. y3, |y| <= qmax.
+template <int CODE> __device__ __forceinline__ uint32_t code4(float y0, float y1, float y2, float y3) {
+    if (CODE == kCodeE4m3) {
+        uint16_t lo, hi;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(lo) : "f"(y1), "f"(y0));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(hi) : "f"(y3), "f"(y2));
+        return (uint32_t)lo | ((uint32_t)hi << 16);
+    }
+    // adding 1.5 * 2^23 rounds to the nearest even integer and leaves it, in two's
+    // complement, in the low bits
+    const float k = 12582912.f;
+    const uint32_t a = __float_as_uint(y0 + k), b = __float_as_uint(y1 + k);
+    const uint32_t c = __float_as_uint(y2 + k), d = __float_as_uint(y3 + k);
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
-// |x| with NaN as infinity, so that the maximum carries it
-__device__ __forceinline__ float mag(float x) {
-    const float a = fabsf(x);
-    return a <= 3.402823466e38f ? a : INFINITY;
+// x / s within +-most, 0 where it is no number.
+__device__ __noinline__ float divided(float x, float s, float most) {
+    const float y = __fdiv_rn(x, s);
+    return fabsf(y) <= most ? y : y > 0.f ? most : y < 0.f ? -most : 0.f;
+}
+
+template <int TG> __device__ __forceinline__ uint32_t group_max(uint32_t a, uint32_t *red) {
+    a = __reduce_max_sync(0xffffffffu, a);
+    if (TG == 32) return a;
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = a;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < TG / 32; ++w) a = max(a, red[w]);
+    return a;
 }
 
 // One unit by TG threads.  VEC: rows and codes are moved eight elements at a
 // time (width a multiple of 8, aligned rows).
 template <typename T, int CODE, int TG, bool VEC>
-__global__ void __launch_bounds__(128) append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(128) append_kernel(const __grid_constant__ AppendArgs a) {
     using Op = CodeOps<CODE>;
-    __shared__ float red[4];
-    constexpr int UNITS = 128 / TG;
+    __shared__ uint32_t red[4];
     const int tid = threadIdx.x % TG;
-    long long u = (long long)blockIdx.x * UNITS + threadIdx.x / TG;
-    const long long nunits = 2LL * a.B * a.touch * a.Hkv;
-    if (u >= nunits) return;
-    const int which = (int)(u & 1);
-    u >>= 1;
-    const int h = (int)(u % a.Hkv);
-    u /= a.Hkv;
-    const int t = (int)(u % a.touch), b = (int)(u / a.touch);
+    const uint32_t u = blockIdx.x * (128 / TG) + threadIdx.x / TG;
+    if (u >= a.nunits) return;
+    // (in 32 bits) units: sequence, block, head, K or V
+    const int which = (int)(u & 1u);
+    const uint32_t u2 = u >> 1, u3 = u2 / (uint32_t)a.Hkv;
+    const int h = (int)(u2 - u3 * (uint32_t)a.Hkv);
+    const int b = (int)(u3 / (uint32_t)a.touch), t = (int)(u3 - (uint32_t)b * (uint32_t)a.touch);
 
     const long long cap = (long long)a.max_pages << a.page_shift;
     const int len = clamp_len(__ldg(a.seqlens_k + b), (int)cap);
@@ -102,94 +155,113 @@ __global__ void __launch_bounds__(128) append_kernel(const AppendArgs a) {
     const int page = __ldg(a.block_table + (long long)b * a.max_pages + span.entry);
     if (page < 0 || page >= a.num_pages) return;
     const int start = (int)span.start, first = (int)span.first;
-    const int rows = (int)(span.last - span.first), sub = span.sub;
+    const int rows = (int)(span.last - span.first);
     const int W = a.width[which];
-    float *sp = a.scales[which] + ((long long)page * a.nblk + sub) * a.Hkv + h;
+    float *sp = a.scales[which] + ((long long)page * a.nblk + span.sub) * a.Hkv + h;
     const T *src = static_cast<const T *>(a.x[which]) +
                    ((row0 + (first - len)) * a.Hkv + h) * (long long)W;
-    const long long pitch = (long long)a.Hkv * W;  // elements between rows, of both sides
-    // code row `r` of the page
+    const int pitch = a.Hkv * W;  // elements between rows, of both sides
     uint8_t *page_base = a.pages[which] +
                          (((long long)page << a.page_shift) * a.Hkv + h) * (long long)W;
-    uint8_t *dst = page_base + (first & ((1 << a.page_shift) - 1)) * pitch;
+    uint8_t *dst = page_base + (long long)(first & ((1 << a.page_shift) - 1)) * pitch;
+    const bool old_rows = start < len;
+    float s_old = old_rows ? __ldcg(sp) : 0.f;
 
-    const int per_row = VEC ? W / 8 : W;
+    // Vectors (or elements) tid, tid + TG, ...: row and column of each by
+    // stepping, without a division.
+    const int per_row = VEC ? W / 8 : W, unit = VEC ? 8 : 1;
     const int items = rows * per_row;
+    const int dr = TG / per_row, dc = TG - dr * per_row;
+    const int r_first = tid / per_row, c_first = tid - r_first * per_row;
+    struct Place {
+        int c;
+        long long at;
+    };
+    auto begin = [&]() -> Place { return {c_first, (long long)r_first * pitch + c_first * unit}; };
+    auto next = [&](Place &q) {
+        q.c += dc;
+        q.at += (long long)dr * pitch + dc * unit;
+        if (q.c >= per_row) {
+            q.c -= per_row;
+            q.at += pitch - per_row * unit;
+        }
+    };
+
     Vec8<T> keep[VEC ? kKeep : 1];
-    float amax = 0.f;
+    uint32_t mx = 0;
     if (VEC) {
+        Place q = begin();
 #pragma unroll
         for (int i = 0; i < kKeep; ++i) {
-            const int it = tid + i * TG;
-            if (it < items) keep[i].load(src + (it / per_row) * pitch + (it % per_row) * 8);
+            if (tid + i * TG < items) keep[i].load(src + q.at);
+            else keep[i].clear();
+            next(q);
         }
 #pragma unroll
-        for (int i = 0; i < kKeep; ++i)
-            if (tid + i * TG < items)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) amax = fmaxf(amax, mag(keep[i].at(j)));
-        for (int it = tid + kKeep * TG; it < items; it += TG) {
+        for (int i = 0; i < kKeep; ++i) mx = keep[i].max_into(mx);
+        for (int it = tid + kKeep * TG; it < items; it += TG, next(q)) {
             Vec8<T> v;
-            v.load(src + (it / per_row) * pitch + (it % per_row) * 8);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) amax = fmaxf(amax, mag(v.at(j)));
+            v.load(src + q.at);
+            mx = v.max_into(mx);
         }
+        if (sizeof(T) == 2) mx = max(mx & 0xffffu, mx >> 16);
     } else {
-        for (int it = tid; it < items; it += TG)
-            amax = fmaxf(amax, mag(to_f32<T>(src[(it / per_row) * pitch + it % per_row])));
+        Place q = begin();
+        for (int it = tid; it < items; it += TG, next(q)) {
+            const T x = src[q.at];
+            uint32_t w = sizeof(T) == 2 ? (uint32_t)*reinterpret_cast<const uint16_t *>(&x) & 0x7fffu
+                                        : *reinterpret_cast<const uint32_t *>(&x) & 0x7fffffffu;
+            mx = max(mx, w);
+        }
     }
-    amax = group_max<TG>(amax, red);
+    mx = group_max<TG>(mx, red);
 
-    float s = append_scale(amax, CODE);
-    const bool old_rows = start < len;
-    float s_old = 0.f;
-    if (old_rows) {
-        s_old = *sp;
-        s = (s_old != s_old || s != s) ? __int_as_float(0x7fc00000) : fmaxf(s_old, s);
-    }
-    if (TG == 32) __syncwarp(); else __syncthreads();  // every thread has read s_old
+    const float nan = __int_as_float(0x7fc00000);
+    float s = mx >= Bits<T>::kInf ? nan : append_scale(Bits<T>::value(mx), CODE);
+    if (old_rows) s = s_old != s_old || s != s ? nan : fmaxf(s_old, s);
     if (tid == 0 && !(old_rows && s == s_old)) *sp = s;
 
     // x / s: a multiplication where s is a power of two (always, unless the
-    // caller's own scales are not)
-    const bool pow2 = (__float_as_uint(s) & 0x007fffffu) == 0u && s > 0.f && s < 1e38f;
+    // caller's own scales are not); a NaN scale: codes 0
+    const bool pow2 = (__float_as_uint(s) & 0x807fffffu) == 0u && s > 0.f && s < 1e38f;
     const float inv = pow2 ? 1.f / s : 0.f;
-    auto code_of = [&](float x) -> uint8_t {
-        float y = pow2 ? x * inv : __fdiv_rn(x, s);
-        y = fabsf(y) <= 3.402823466e38f ? y : 0.f;
-        return Op::code(y);
-    };
-    if (VEC) {
-        auto put = [&](const Vec8<T> &v, int it) {
-            uint8_t c[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) c[j] = code_of(v.at(j));
-            uint2 w;
-            w.x = c[0] | (c[1] << 8) | (c[2] << 16) | ((uint32_t)c[3] << 24);
-            w.y = c[4] | (c[5] << 8) | (c[6] << 16) | ((uint32_t)c[7] << 24);
-            *reinterpret_cast<uint2 *>(dst + (it / per_row) * pitch + (it % per_row) * 8) = w;
+    auto emit = [&](auto is_pow2) {
+        auto scaled = [&](float x) -> float {
+            return decltype(is_pow2)::value ? x * inv : divided(x, s, Op::kMax);
         };
+        Place q = begin();
+        if (VEC) {
+            auto put = [&](const Vec8<T> &v) {
+                float y[8];
 #pragma unroll
-        for (int i = 0; i < kKeep; ++i)
-            if (tid + i * TG < items) put(keep[i], tid + i * TG);
-        for (int it = tid + kKeep * TG; it < items; it += TG) {
-            Vec8<T> v;
-            v.load(src + (it / per_row) * pitch + (it % per_row) * 8);
-            put(v, it);
+                for (int j = 0; j < 8; ++j) y[j] = scaled(v.at(j));
+                *reinterpret_cast<uint2 *>(dst + q.at) =
+                    make_uint2(code4<CODE>(y[0], y[1], y[2], y[3]), code4<CODE>(y[4], y[5], y[6], y[7]));
+            };
+#pragma unroll
+            for (int i = 0; i < kKeep; ++i) {
+                if (tid + i * TG < items) put(keep[i]);
+                next(q);
+            }
+            for (int it = tid + kKeep * TG; it < items; it += TG, next(q)) {
+                Vec8<T> v;
+                v.load(src + q.at);
+                put(v);
+            }
+        } else {
+            for (int it = tid; it < items; it += TG, next(q)) dst[q.at] = Op::code(scaled(to_f32<T>(src[q.at])));
         }
-    } else {
-        for (int it = tid; it < items; it += TG)
-            dst[(it / per_row) * pitch + it % per_row] =
-                code_of(to_f32<T>(src[(it / per_row) * pitch + it % per_row]));
-    }
+    };
+    if (pow2) emit(std::true_type{});
+    else emit(std::false_type{});
 
     // earlier rows of a block whose scale has grown
     if (old_rows && !(s == s_old)) {
-        uint8_t *ob = page_base + (start & ((1 << a.page_shift) - 1)) * pitch;
+        uint8_t *ob = page_base + (long long)(start & ((1 << a.page_shift) - 1)) * pitch;
         const int n_old = (len - start) * W;
         const float ratio = __fdiv_rn(s_old, s);
         for (int it = tid; it < n_old; it += TG) {
-            uint8_t *c = ob + (it / W) * pitch + it % W;
+            uint8_t *c = ob + (long long)(it / W) * pitch + it % W;
             float y = Op::one(*c) * ratio;
             y = fabsf(y) <= 3.402823466e38f ? y : 0.f;
             *c = Op::code(y);
@@ -199,13 +271,8 @@ __global__ void __launch_bounds__(128) append_kernel(const AppendArgs a) {
 
 template <typename T, int CODE, int TG, bool VEC>
 int launch_t(const AppendArgs &a, cudaStream_t stream) {
-    const long long nunits = 2LL * a.B * a.touch * a.Hkv;
-    const long long blocks = (nunits + 128 / TG - 1) / (128 / TG);
-    if (blocks >= (1LL << 31)) {
-        set_error("attn_cache_append: too many blocks of rows");
-        return 2;
-    }
-    append_kernel<T, CODE, TG, VEC><<<(unsigned)blocks, 128, 0, stream>>>(a);
+    const unsigned blocks = (a.nunits + 128 / TG - 1) / (128 / TG);
+    append_kernel<T, CODE, TG, VEC><<<blocks, 128, 0, stream>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) {
         set_error("append kernel launch: %s", cudaGetErrorString(e));
@@ -260,6 +327,12 @@ int launch_cache_append(const void *k, const void *v, void *k_pages, void *v_pag
     a.blk_shift = blk_shift;
     // N rows from any offset in a block
     a.touch = (int)(((long long)N - 1 + (1 << blk_shift) - 1) / (1 << blk_shift)) + 1;
+    const double units = 2.0 * B * a.touch * Hkv;
+    if (units >= 2147483648.0) {
+        set_error("attn_cache_append: 2^31 or more blocks of rows");
+        return 2;
+    }
+    a.nunits = (uint32_t)units;
     if (code == kCodeE4m3) {
         switch (dtype) {
             case 0: return launch_code<float, kCodeE4m3>(a, stream);
