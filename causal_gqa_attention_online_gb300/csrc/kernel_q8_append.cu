@@ -41,7 +41,8 @@ struct AppendArgs {
     const int32_t *seqlens_new, *seqlens_k, *block_table;
     int max_pages, page_shift, num_pages, nblk, blk_shift;
     int touch;             // blocks a sequence's new rows can touch
-    uint32_t nunits;       // (sequence, block, head, K | V)
+    int row_shift[2];      // log2 of the vectors of a row (-1: no power of two)
+    int row_step[2];       // rows that a unit's threads take at a time
 };
 
 // |x| as an unsigned integer of the type's bits: ordered as the magnitudes are,
@@ -127,17 +128,16 @@ template <int TG> __device__ __forceinline__ uint32_t group_max(uint32_t a, uint
 // One unit by TG threads.  VEC: rows and codes are moved eight elements at a
 // time (width a multiple of 8, aligned rows).
 template <typename T, int CODE, int TG, bool VEC>
-__global__ void __launch_bounds__(128) append_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(128, VEC && sizeof(T) == 2 ? 8 : 3) append_kernel(const __grid_constant__ AppendArgs a) {
     using Op = CodeOps<CODE>;
     __shared__ uint32_t red[4];
     const int tid = threadIdx.x % TG;
+    // units: block, head, K or V of sequence blockIdx.y (+ gridDim.y ...)
     const uint32_t u = blockIdx.x * (128 / TG) + threadIdx.x / TG;
-    if (u >= a.nunits) return;
-    // (in 32 bits) units: sequence, block, head, K or V
     const int which = (int)(u & 1u);
-    const uint32_t u2 = u >> 1, u3 = u2 / (uint32_t)a.Hkv;
-    const int h = (int)(u2 - u3 * (uint32_t)a.Hkv);
-    const int b = (int)(u3 / (uint32_t)a.touch), t = (int)(u3 - (uint32_t)b * (uint32_t)a.touch);
+    const int t = (int)((u >> 1) / (uint32_t)a.Hkv), h = (int)((u >> 1) - (uint32_t)t * (uint32_t)a.Hkv);
+    const int b = blockIdx.y + blockIdx.z * gridDim.y;
+    if (t >= a.touch || b >= a.B) return;
 
     const long long cap = (long long)a.max_pages << a.page_shift;
     const int len = clamp_len(__ldg(a.seqlens_k + b), (int)cap);
@@ -171,8 +171,9 @@ __global__ void __launch_bounds__(128) append_kernel(const __grid_constant__ App
     // stepping, without a division.
     const int per_row = VEC ? W / 8 : W, unit = VEC ? 8 : 1;
     const int items = rows * per_row;
-    const int dr = TG / per_row, dc = TG - dr * per_row;
-    const int r_first = tid / per_row, c_first = tid - r_first * per_row;
+    const int dr = a.row_step[which], dc = TG - dr * per_row;  // TG / per_row
+    const int sh = a.row_shift[which];  // log2(per_row), or -1
+    const int r_first = sh >= 0 ? tid >> sh : tid / per_row, c_first = tid - r_first * per_row;
     struct Place {
         int c;
         long long at;
@@ -189,13 +190,22 @@ __global__ void __launch_bounds__(128) append_kernel(const __grid_constant__ App
 
     Vec8<T> keep[VEC ? kKeep : 1];
     uint32_t mx = 0;
+    // a whole block of rows that divide the threads: no tests, one step
+    const bool even = VEC && items == kKeep * TG && dc == 0;
+    const long long step = (long long)dr * pitch;
     if (VEC) {
         Place q = begin();
+        if (even) {
+            const T *x = src + q.at;
 #pragma unroll
-        for (int i = 0; i < kKeep; ++i) {
-            if (tid + i * TG < items) keep[i].load(src + q.at);
-            else keep[i].clear();
-            next(q);
+            for (int i = 0; i < kKeep; ++i, x += step) keep[i].load(x);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kKeep; ++i) {
+                if (tid + i * TG < items) keep[i].load(src + q.at);
+                else keep[i].clear();
+                next(q);
+            }
         }
 #pragma unroll
         for (int i = 0; i < kKeep; ++i) mx = keep[i].max_into(mx);
@@ -231,22 +241,28 @@ __global__ void __launch_bounds__(128) append_kernel(const __grid_constant__ App
         };
         Place q = begin();
         if (VEC) {
-            auto put = [&](const Vec8<T> &v) {
+            auto put = [&](const Vec8<T> &v, uint8_t *to) {
                 float y[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) y[j] = scaled(v.at(j));
-                *reinterpret_cast<uint2 *>(dst + q.at) =
+                *reinterpret_cast<uint2 *>(to) =
                     make_uint2(code4<CODE>(y[0], y[1], y[2], y[3]), code4<CODE>(y[4], y[5], y[6], y[7]));
             };
+            if (even) {
+                uint8_t *to = dst + q.at;
+#pragma unroll
+                for (int i = 0; i < kKeep; ++i, to += step) put(keep[i], to);
+                return;
+            }
 #pragma unroll
             for (int i = 0; i < kKeep; ++i) {
-                if (tid + i * TG < items) put(keep[i]);
+                if (tid + i * TG < items) put(keep[i], dst + q.at);
                 next(q);
             }
             for (int it = tid + kKeep * TG; it < items; it += TG, next(q)) {
                 Vec8<T> v;
                 v.load(src + q.at);
-                put(v);
+                put(v, dst + q.at);
             }
         } else {
             for (int it = tid; it < items; it += TG, next(q)) dst[q.at] = Op::code(scaled(to_f32<T>(src[q.at])));
@@ -271,8 +287,21 @@ __global__ void __launch_bounds__(128) append_kernel(const __grid_constant__ App
 
 template <typename T, int CODE, int TG, bool VEC>
 int launch_t(const AppendArgs &a, cudaStream_t stream) {
-    const unsigned blocks = (a.nunits + 128 / TG - 1) / (128 / TG);
-    append_kernel<T, CODE, TG, VEC><<<blocks, 128, 0, stream>>>(a);
+    AppendArgs x = a;
+    for (int i = 0; i < 2; ++i) {
+        const int per_row = VEC ? a.width[i] / 8 : a.width[i];
+        x.row_shift[i] = -1;
+        for (int k = 0; k < 10; ++k)
+            if (1 << k == per_row) x.row_shift[i] = k;
+        x.row_step[i] = TG / per_row;
+    }
+    const long long units = 2LL * a.touch * a.Hkv, blocks = (units + 128 / TG - 1) / (128 / TG);
+    if (units >= (1LL << 31)) {
+        set_error("attn_cache_append: 2^31 or more blocks of rows in a sequence");
+        return 2;
+    }
+    const unsigned by = a.B < 65535 ? a.B : 65535;
+    append_kernel<T, CODE, TG, VEC><<<dim3((unsigned)blocks, by, (a.B + by - 1) / by), 128, 0, stream>>>(x);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) {
         set_error("append kernel launch: %s", cudaGetErrorString(e));
@@ -327,12 +356,6 @@ int launch_cache_append(const void *k, const void *v, void *k_pages, void *v_pag
     a.blk_shift = blk_shift;
     // N rows from any offset in a block
     a.touch = (int)(((long long)N - 1 + (1 << blk_shift) - 1) / (1 << blk_shift)) + 1;
-    const double units = 2.0 * B * a.touch * Hkv;
-    if (units >= 2147483648.0) {
-        set_error("attn_cache_append: 2^31 or more blocks of rows");
-        return 2;
-    }
-    a.nunits = (uint32_t)units;
     if (code == kCodeE4m3) {
         switch (dtype) {
             case 0: return launch_code<float, kCodeE4m3>(a, stream);

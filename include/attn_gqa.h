@@ -389,7 +389,7 @@ ATTN_API int attn_bwd_varlen(const void *q, const void *k, const void *v, const 
  * sequence b's rows [cu_seqlens_new[b], cu_seqlens_new[b + 1]), max_new an upper
  * bound of their number.
  * Widths in [1, 512].  Returns ATTN_OK, ATTN_ERR_INVALID, ATTN_ERR_UNSUPPORTED
- * (more than 2^31 blocks of rows) or ATTN_ERR_CUDA; asynchronous on `stream`.
+ * (2^31 or more blocks of rows in a sequence) or ATTN_ERR_CUDA; asynchronous on `stream`.
  */
 ATTN_API int attn_cache_append(const void *k, const void *v, void *k_pages, void *v_pages,
                                float *k_scale, float *v_scale, int B, int N, int Hkv, int D,
