@@ -67,7 +67,7 @@ __device__ void copy_pages(const PoolTable &t, const int32_t *src, const int32_t
     for (long long c = (long long)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); c < total;
          c += step) {
         const int i = (int)(c / per_page), r = (int)(c - (long long)i * per_page);
-        const int sp = __ldg(src + (src_back ? n - 1 - i : i)), dp = __ldg(dst + i);
+        const int sp = __ldcg(src + (src_back ? n - 1 - i : i)), dp = __ldcg(dst + i);
         if (sp < 0 || sp >= src_pages || dp < 0 || dp >= dst_pages) continue;
         int pool = 0;
         while (r >= t.first_chunk[pool + 1]) ++pool;
@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kCopyThreads)
 __global__ void __launch_bounds__(kCopyThreads)
     copy_counted_kernel(const __grid_constant__ PoolTable t, const int32_t *src, const int32_t *dst,
                         const int32_t *count, int pages, bool src_back) {
-    copy_pages(t, src, dst, __ldg(count), pages, pages, src_back);
+    copy_pages(t, src, dst, __ldcg(count), pages, pages, src_back);
 }
 
 // --------------------------------------------------------------- block scans
@@ -136,9 +136,10 @@ struct ForkArgs {
     // new one, the lowest claiming entry, and whether an entry holds it
     int32_t *was, *full, *held;
     unsigned long long *claim;
+    int32_t *need;       // pages each slot takes
+    int32_t *list;       // the free pages, in ascending order
     int32_t *src, *dst;  // pages to copy (N at most)
-    int32_t *list;       // the free pages in use, in ascending order
-    int32_t *count;      // [0] pages to copy, [1] free pages
+    int32_t *count;      // [0] pages to copy
 };
 
 struct Slot {
@@ -180,12 +181,24 @@ __device__ __forceinline__ bool keeps(const ForkArgs &a, int i, int j, int c) {
            __ldcg(a.claim + c) == (unsigned long long)i * a.M + j;
 }
 
+// Four phases, each spread over the whole cluster; the dependent loads of a slot
+// (parent, length, entry, the entry's page) are what they cost, so a warp takes a
+// slot and every warp has as few as can be.  Slots and pages are dealt out in
+// contiguous parts, so that a part's place in the order is the sum of the parts
+// before it, read through distributed shared memory.
 __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
-    fork_plan_kernel(const ForkArgs a) {
+    fork_plan_kernel(const __grid_constant__ ForkArgs a) {
     __shared__ int warps[32];
+    __shared__ int part_free;  // free pages of this block's part
+    __shared__ int part_wide;  // slots of its part that do not fit the table
+    __shared__ unsigned long long part_need;  // pages its slots take
     cg::cluster_group cluster = cg::this_cluster();
-    const int gt = blockIdx.x * kPlanThreads + threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int gt = blockIdx.x * kPlanThreads + tid;
     const int gn = kPlanCtas * kPlanThreads;
+    constexpr int NW = kPlanThreads / 32;
+    // the finish grid (a programmatic dependent launch) may be scheduled now
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     // 1. clear the per-page workspace
     for (int p = gt; p < a.P; p += gn) {
         a.was[p] = 0;
@@ -193,21 +206,26 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
         a.held[p] = 0;
         a.claim[p] = ~0ull;
     }
-    if (gt < 2) a.count[gt] = 0;
+    if (gt == 0) a.count[0] = 0;
+    if (tid == 0) {
+        part_free = 0;
+        part_wide = 0;
+        part_need = 0;
+    }
     __threadfence();
     cluster.sync();
-    // 2. references by the old table; full entries and claims of the new one
+    // 2. references by the old table; full entries and claims of the new one; free
+    // pages of each part
     for (long long e = gt; e < (long long)a.S * a.M; e += gn) {
         const int c = __ldg(a.table + e);
         if (c >= 0 && c < a.P) atomicAdd(a.was + c, 1);
     }
-    int nfree = 0;
-    for (int p = gt; p < a.P; p += gn) nfree += __ldg(a.refs + p) == 0;
-    if (nfree) atomicAdd(a.count + 1, nfree);
-    const int lane = threadIdx.x & 31;
-    for (int i = gt >> 5; i < a.N; i += gn >> 5) {
+    const int per_s = (int)(((long long)a.N + kPlanCtas - 1) / kPlanCtas);
+    const int s0 = (int)min((long long)blockIdx.x * per_s, (long long)a.N), s1 = min(s0 + per_s, a.N);
+    for (int i = s0 + warp; i < s1; i += NW) {
         const Slot s = slot_of(a, i);
         if (s.parent < 0) continue;
+        if (lane == 0 && s.want > a.M) atomicAdd(&part_wide, 1);
         const int last = (int)min(s.want, (long long)a.M);
         for (int j = lane; j < last; j += 32) {
             const int c = cand_of(a, s, j);
@@ -216,116 +234,117 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
             else atomicMin(a.claim + c, (unsigned long long)i * a.M + j);
         }
     }
+    const int per_p = (a.P + kPlanCtas - 1) / kPlanCtas;
+    const int p0 = (int)min((long long)blockIdx.x * per_p, (long long)a.P);
+    const int p1 = (int)min((long long)p0 + per_p, (long long)a.P);
+    int nfree = 0;
+    for (int p = p0 + tid; p < p1; p += kPlanThreads) nfree += __ldg(a.refs + p) == 0;
+    nfree = __reduce_add_sync(0xffffffffu, nfree);
+    if (lane == 0 && nfree) atomicAdd(&part_free, nfree);
     __threadfence();
     cluster.sync();
-    if (blockIdx.x != 0) return;
-    // 3. one block: entries that need a page, in slot order, take the free pages
-    // in ascending order
-    int wide = 0;
-    long long need = 0;
-    const int warp = threadIdx.x >> 5;
-    constexpr int NW = kPlanThreads / 32;
-    for (int i = warp; i < a.N; i += NW) {
+    // 3. how many pages each slot takes; the free pages in ascending order
+    for (int i = s0 + warp; i < s1; i += NW) {
         const Slot s = slot_of(a, i);
-        if (s.parent < 0) continue;
-        if (lane == 0 && s.want > a.M) ++wide;
-        const int last = (int)min(s.want, (long long)a.M);
-        for (int j = s.nfull + lane; j < last; j += 32) need += !keeps(a, i, j, cand_of(a, s, j));
-    }
-    __shared__ unsigned long long sum_need;
-    __shared__ int sum_wide;
-    if (threadIdx.x == 0) {
-        sum_need = 0;
-        sum_wide = 0;
-    }
-    __syncthreads();
-    if (need) atomicAdd(&sum_need, (unsigned long long)need);
-    if (wide) atomicAdd(&sum_wide, wide);
-    __syncthreads();
-    const long long total = (long long)sum_need, missing = total - __ldcg(a.count + 1);
-    const bool fine = missing <= 0 && sum_wide == 0;
-    if (threadIdx.x == 0) {
-        a.status[0] = missing > 0 ? (int)min(missing, (long long)INT_MAX) : 0;
-        a.status[1] = sum_wide;
-        a.status[2] = fine ? (int)total : 0;
-        if (!fine) a.status[3] = 0;
-    }
-    if (!fine) return;
-    // the first `total` free pages in ascending order, eight pages a thread
-    int base = 0;
-    for (long long p0 = 0; p0 < a.P && base < total; p0 += 8 * kPlanThreads) {
-        const long long p = p0 + 8 * threadIdx.x;
-        unsigned f = 0;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (p + k < a.P && __ldg(a.refs + p + k) == 0) f |= 1u << k;
-        int tot;
-        int at = base + block_scan(__popc(f), warps, &tot);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if ((f >> k) & 1u) a.list[at++] = (int)(p + k);
-        base += tot;
-    }
-    __syncthreads();
-    // slots in order, 32 at a time (one a warp): count, scan, assign
-    __shared__ int copies;
-    if (threadIdx.x == 0) copies = 0;
-    int taken = 0;
-    for (int i0 = 0; i0 < a.N; i0 += NW) {
-        const int i = i0 + warp;
-        Slot s;
-        s.parent = -1;
-        s.nfull = s.len = 0;
-        s.want = 0;
-        if (i < a.N) s = slot_of(a, i);
         const int last = s.parent < 0 ? 0 : (int)min(s.want, (long long)a.M);
         int cnt = 0;
         for (int j = s.nfull + lane; j < last; j += 32) cnt += !keeps(a, i, j, cand_of(a, s, j));
+        cnt = __reduce_add_sync(0xffffffffu, cnt);
+        if (lane == 0) {
+            a.need[i] = cnt;
+            if (cnt) atomicAdd(&part_need, (unsigned long long)cnt);
+        }
+    }
+    int free_before = 0, all_free = 0, wide = 0;
+    for (int r = 0; r < kPlanCtas; ++r) {
+        const int f = *cluster.map_shared_rank(&part_free, r);
+        if (r < (int)blockIdx.x) free_before += f;
+        all_free += f;
+        wide += *cluster.map_shared_rank(&part_wide, r);
+    }
+    for (long long q = p0; q < p1; q += 8 * kPlanThreads) {  // eight pages a thread
+        const long long p = q + 8 * tid;
+        unsigned f = 0;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) cnt += __shfl_xor_sync(0xffffffffu, cnt, o);
+        for (int k = 0; k < 8; ++k)
+            if (p + k < p1 && __ldg(a.refs + p + k) == 0) f |= 1u << k;
         int tot;
-        int at = block_scan(lane == 0 ? cnt : 0, warps, &tot);
-        at = taken + __shfl_sync(0xffffffffu, at, 0);
-        taken += tot;
-        for (int j0 = s.nfull; j0 < last; j0 += 32) {
-            const int j = j0 + lane;
-            int c = -1;
-            bool get = false;
-            if (j < last) {
-                c = cand_of(a, s, j);
-                get = !keeps(a, i, j, c);
-            }
-            const unsigned m = __ballot_sync(0xffffffffu, get);
-            int pg = c;
-            if (get) pg = a.list[at + __popc(m & ((1u << lane) - 1u))];
-            at += __popc(m);
-            if (j < last) {
-                a.table_out[(long long)i * a.M + j] = pg;
-                a.held[pg] = 1;
-                if (get && c >= 0 && c < a.P && j == s.nfull && (s.len & ((1 << a.page_shift) - 1))) {
-                    const int k = atomicAdd(&copies, 1);
-                    a.src[k] = c;
-                    a.dst[k] = pg;
+        int at = free_before + block_scan(__popc(f), warps, &tot);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if ((f >> k) & 1u) a.list[at++] = (int)(p + k);
+        free_before += tot;
+    }
+    __threadfence();
+    cluster.sync();
+    // 4. entries that need a page take the free ones in the order of slots and
+    // entries, when there are enough
+    unsigned long long before = 0, total = 0;
+    for (int r = 0; r < kPlanCtas; ++r) {
+        const unsigned long long x = *cluster.map_shared_rank(&part_need, r);
+        if (r < (int)blockIdx.x) before += x;
+        total += x;
+    }
+    const long long missing = (long long)total - all_free;
+    const bool fine = missing <= 0 && wide == 0;
+    if (gt == 0) {
+        a.status[0] = missing > 0 ? (int)min(missing, (long long)INT_MAX) : 0;
+        a.status[1] = wide;
+        a.status[2] = fine ? (int)total : 0;
+        if (!fine) a.status[3] = 0;
+    }
+    if (fine) {
+        int taken = (int)before;
+        for (int i0 = s0; i0 < s1; i0 += NW) {
+            const int i = i0 + warp;
+            Slot s;
+            s.parent = -1;
+            s.nfull = s.len = 0;
+            s.want = 0;
+            if (i < s1) s = slot_of(a, i);
+            const int last = s.parent < 0 ? 0 : (int)min(s.want, (long long)a.M);
+            int tot;
+            int at = block_scan(lane == 0 && i < s1 ? __ldcg(a.need + i) : 0, warps, &tot);
+            at = taken + __shfl_sync(0xffffffffu, at, 0);
+            taken += tot;
+            for (int j0 = s.nfull; j0 < last; j0 += 32) {
+                const int j = j0 + lane;
+                int c = -1;
+                bool get = false;
+                if (j < last) {
+                    c = cand_of(a, s, j);
+                    get = !keeps(a, i, j, c);
+                }
+                const unsigned m = __ballot_sync(0xffffffffu, get);
+                int pg = c;
+                if (get) pg = __ldcg(a.list + at + __popc(m & ((1u << lane) - 1u)));
+                at += __popc(m);
+                if (j < last) {
+                    a.table_out[(long long)i * a.M + j] = pg;
+                    a.held[pg] = 1;
+                    if (get && c >= 0 && c < a.P && j == s.nfull && (s.len & ((1 << a.page_shift) - 1))) {
+                        const int k = atomicAdd(a.count, 1);
+                        a.src[k] = c;
+                        a.dst[k] = pg;
+                    }
                 }
             }
         }
     }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        a.status[3] = copies;
-        a.count[0] = copies;
-    }
+    cluster.sync();  // (every part's sums are read, and every copy is counted)
+    if (gt == 0 && fine) a.status[3] = __ldcg(a.count);
 }
 
 // The new version's remaining entries, lengths and counts, and the page copies.
 __global__ void __launch_bounds__(kCopyThreads)
-    fork_finish_kernel(const ForkArgs a, const __grid_constant__ PoolTable t) {
-    const bool fine = __ldg(a.status) == 0 && __ldg(a.status + 1) == 0;
+    fork_finish_kernel(const __grid_constant__ ForkArgs a, const __grid_constant__ PoolTable t) {
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    const bool fine = __ldcg(a.status) == 0 && __ldcg(a.status + 1) == 0;
     const long long gt = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     const long long gn = (long long)gridDim.x * blockDim.x;
     for (long long p = gt; p < a.P; p += gn) {
         const int r = __ldg(a.refs + p);
-        a.refs_out[p] = fine ? r - __ldg(a.was + p) + __ldg(a.full + p) + __ldg(a.held + p) : r;
+        a.refs_out[p] = fine ? r - __ldcg(a.was + p) + __ldcg(a.full + p) + __ldcg(a.held + p) : r;
     }
     const int lane = threadIdx.x & 31;
     for (long long i = gt >> 5; i < a.N; i += gn >> 5) {
@@ -343,7 +362,7 @@ __global__ void __launch_bounds__(kCopyThreads)
             a.table_out[i * a.M + j] = v;
         }
     }
-    if (t.n > 0) copy_pages(t, a.src, a.dst, __ldg(a.count), a.P, a.P);
+    if (t.n > 0) copy_pages(t, a.src, a.dst, __ldcg(a.count), a.P, a.P);
 }
 
 // ------------------------------------------------------------------ compact
@@ -357,7 +376,9 @@ struct CompactArgs {
 };
 
 __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
-    compact_plan_kernel(const CompactArgs a) {
+    compact_plan_kernel(const __grid_constant__ CompactArgs a) {
+    // the finish grid (a programmatic dependent launch) may be scheduled now
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     __shared__ int warps[32];
     __shared__ int mine;  // live pages of this block's part
     cg::cluster_group cluster = cg::this_cluster();
@@ -411,14 +432,15 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
 }
 
 __global__ void __launch_bounds__(kCopyThreads)
-    compact_finish_kernel(const CompactArgs a, const __grid_constant__ PoolTable t) {
+    compact_finish_kernel(const __grid_constant__ CompactArgs a, const __grid_constant__ PoolTable t) {
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
     const long long gt = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     const long long gn = (long long)gridDim.x * blockDim.x;
     for (long long e = gt; e < (long long)a.S * a.M; e += gn) {
         const int c = __ldg(a.table + e);
-        a.table_out[e] = c >= 0 && c < a.P ? __ldg(a.remap + c) : -1;
+        a.table_out[e] = c >= 0 && c < a.P ? __ldcg(a.remap + c) : -1;
     }
-    if (t.n > 0) copy_pages(t, a.src, a.dst, __ldg(a.count), a.P, a.P, true);
+    if (t.n > 0) copy_pages(t, a.src, a.dst, __ldcg(a.count), a.P, a.P, true);
 }
 
 // --------------------------------------------------------------------- host
@@ -466,6 +488,27 @@ int launched(const char *what) {
     return 0;
 }
 
+// A finish kernel as the programmatic dependent of its plan.
+template <typename A>
+int launch_finish(void (*kern)(A, PoolTable), unsigned blocks, const A &a, const PoolTable &t, const char *what,
+                  cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kCopyThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, t);
+    if (e != cudaSuccess) {
+        set_error("%s launch: %s", what, cudaGetErrorString(e));
+        return 3;
+    }
+    return launched(what);
+}
+
 // The pools past the first kMaxPools, in launches of their own.
 template <typename F> int for_pool_groups(const void *const *src, void *const *dst, const long long *bytes, int n, F f) {
     int rc = 0;
@@ -495,7 +538,7 @@ int launch_pages_copy(const void *const *src_pools, void *const *dst_pools, cons
 }
 
 unsigned long long pages_fork_workspace(int N, int P) {
-    return 8ull * P + 4ull * (4ull * P + 2ull * N + 2ull);
+    return 8ull * P + 4ull * (4ull * P + 3ull * N + 1ull);
 }
 
 int launch_pages_fork(void *const *pools, const long long *bytes, int npools,
@@ -523,7 +566,8 @@ int launch_pages_fork(void *const *pools, const long long *bytes, int npools,
     a.full = a.was + P;
     a.held = a.full + P;
     a.list = a.held + P;
-    a.src = a.list + P;
+    a.need = a.list + P;
+    a.src = a.need + N;
     a.dst = a.src + N;
     a.count = a.dst + N;
     fork_plan_kernel<<<kPlanCtas, kPlanThreads, 0, stream>>>(a);
@@ -536,8 +580,7 @@ int launch_pages_fork(void *const *pools, const long long *bytes, int npools,
             return launched("page copy kernel");
         }
         const long long other = (long long)N * 32 > P ? (long long)N * 32 : P;
-        fork_finish_kernel<<<grid_for(chunks, other), kCopyThreads, 0, stream>>>(a, t);
-        return launched("page fork kernel");
+        return launch_finish(fork_finish_kernel, grid_for(chunks, other), a, t, "page fork kernel", stream);
     });
 }
 
@@ -570,8 +613,8 @@ int launch_pages_compact(void *const *pools, const long long *bytes, int npools,
             copy_counted_kernel<<<grid_for(chunks, 0), kCopyThreads, 0, stream>>>(t, a.src, a.dst, a.count, P, true);
             return launched("page copy kernel");
         }
-        compact_finish_kernel<<<grid_for(chunks, (long long)S * M), kCopyThreads, 0, stream>>>(a, t);
-        return launched("page compact kernel");
+        return launch_finish(compact_finish_kernel, grid_for(chunks, (long long)S * M), a, t,
+                             "page compact kernel", stream);
     });
 }
 
