@@ -22,7 +22,7 @@ return.
 """
 from __future__ import annotations
 
-import ctypes
+import array
 import math
 
 import torch
@@ -189,9 +189,9 @@ def attn_fwd_paged_q8(q, k_pages, v_pages, k_scale, v_scale, block_table, seqlen
 
 
 def _pool_arrays(pools, pages, dev, what):
-    """Pointers and page bytes of pools whose first axis counts ``pages`` pages."""
-    n = len(pools)
-    ptrs, sizes = [0] * n, [0] * n
+    """Pointers and page bytes of pools whose first axis counts ``pages`` pages,
+    as 64-bit arrays."""
+    ptrs, sizes = array.array("Q"), array.array("q")
     for i, t in enumerate(pools):
         if t.dim() < 1 or t.shape[0] != pages:
             raise ValueError(f"{what}[{i}]: shape {tuple(t.shape)}, expected {pages} pages first")
@@ -199,9 +199,14 @@ def _pool_arrays(pools, pages, dev, what):
             raise ValueError(f"{what}[{i}] must be contiguous")
         if t.device != dev:
             raise ValueError(f"{what}[{i}] is on {t.device}, expected {dev}")
-        ptrs[i] = t.data_ptr()
-        sizes[i] = t.nbytes // max(pages, 1)
-    return (ctypes.c_void_p * max(n, 1))(*ptrs), (ctypes.c_longlong * max(n, 1))(*sizes), n
+        ptrs.append(t.data_ptr())
+        sizes.append(t.nbytes // max(pages, 1))
+    return ptrs, sizes
+
+
+def _at(a):
+    """The address of an array's first element (it lives as long as the array)."""
+    return a.buffer_info()[0]
 
 
 def attn_pages_copy(src_pools, dst_pools, src, dst, *, stream=None):
@@ -218,18 +223,18 @@ def attn_pages_copy(src_pools, dst_pools, src, dst, *, stream=None):
     dx = _tensor("dst", dst, torch.int32, (n,), dev)
     sp = src_pools[0].shape[0] if len(src_pools) else 0
     dp = dst_pools[0].shape[0] if len(dst_pools) else 0
-    sptr, sbytes, npools = _pool_arrays(src_pools, sp, dev, "src_pools")
+    sptr, sbytes = _pool_arrays(src_pools, sp, dev, "src_pools")
     if dst_pools is src_pools:
         dptr = sptr
     else:
-        dptr, dbytes, _ = _pool_arrays(dst_pools, dp, dev, "dst_pools")
-        if list(sbytes) != list(dbytes):
+        dptr, dbytes = _pool_arrays(dst_pools, dp, dev, "dst_pools")
+        if sbytes != dbytes:
             raise ValueError("the pages of a source pool and of its destination differ in size")
     if not _here(dev, stream):
         with _elsewhere(dev, stream):
             return attn_pages_copy(src_pools, dst_pools, src, dst)
-    _check(load_library().attn_pages_copy(sptr, dptr, sbytes, npools, sp, dp, sx, dx, n,
-                                          _raw_stream(dev.index)))
+    _check(load_library().attn_pages_copy(_at(sptr), _at(dptr), _at(sbytes), len(sptr), sp, dp, sx,
+                                          dx, n, _raw_stream(dev.index)))
 
 
 def attn_pages_fork(pools, block_table, seqlens, refcount, parents, page_size, *, new_tokens=None,
@@ -253,19 +258,19 @@ def attn_pages_fork(pools, block_table, seqlens, refcount, parents, page_size, *
     rx = _tensor("refcount", refcount, torch.int32, (P,), dev)
     px = _tensor("parents", parents, torch.int32, (N,), dev)
     nx = None if new_tokens is None else _tensor("new_tokens", new_tokens, torch.int32, (N,), dev)
-    ptrs, sizes, npools = _pool_arrays(pools, P, dev, "pools")
+    ptrs, sizes = _pool_arrays(pools, P, dev, "pools")
     if not _here(dev, stream):
         with _elsewhere(dev, stream):
             return attn_pages_fork(pools, block_table, seqlens, refcount, parents, page_size,
                                    new_tokens=new_tokens)
     # one allocation: the new version's table, lengths, counts, and the status
     out = torch.empty((N * M + N + P + 4,), dtype=torch.int32, device=dev)
-    table_out, lens_out, refs_out, status = out.split((N * M, N, P, 4))
-    at = out.data_ptr()
+    at, l0, r0, s0 = out.data_ptr(), N * M, N * M + N, N * M + N + P
     _check(load_library().attn_pages_fork(
-        ptrs, sizes, npools, tx, lx, rx, S, M, P, int(page_size), px, nx, N, at, at + 4 * N * M,
-        at + 4 * (N * M + N), at + 4 * (N * M + N + P), _raw_stream(dev.index)))
-    return table_out.view(N, M), lens_out, refs_out, status
+        _at(ptrs), _at(sizes), len(ptrs), tx, lx, rx, S, M, P, int(page_size), px, nx, N, at,
+        at + 4 * l0, at + 4 * r0, at + 4 * s0, _raw_stream(dev.index)))
+    return (out.as_strided((N, M), (M, 1), 0), out.as_strided((N,), (1,), l0),
+            out.as_strided((P,), (1,), r0), out.as_strided((4,), (1,), s0))
 
 
 def attn_pages_compact(pools, block_table, refcount, *, stream=None):
@@ -278,14 +283,14 @@ def attn_pages_compact(pools, block_table, refcount, *, stream=None):
     P = refcount.numel()
     tx = _tensor("block_table", block_table, torch.int32, (S, M), dev)
     rx = _tensor("refcount", refcount, torch.int32, (P,), dev)
-    ptrs, sizes, npools = _pool_arrays(pools, P, dev, "pools")
+    ptrs, sizes = _pool_arrays(pools, P, dev, "pools")
     if not _here(dev, stream):
         with _elsewhere(dev, stream):
             return attn_pages_compact(pools, block_table, refcount)
     out = torch.empty((S * M + 2 * P + 1,), dtype=torch.int32, device=dev)
-    table_out, refs_out, remap, n_live = out.split((S * M, P, P, 1))
-    at = out.data_ptr()
+    at, r0, m0, n0 = out.data_ptr(), S * M, S * M + P, S * M + 2 * P
     _check(load_library().attn_pages_compact(
-        ptrs, sizes, npools, tx, rx, S, M, P, at, at + 4 * S * M, at + 4 * (S * M + P),
-        at + 4 * (S * M + 2 * P), _raw_stream(dev.index)))
-    return table_out.view(S, M), refs_out, remap, n_live.view(())
+        _at(ptrs), _at(sizes), len(ptrs), tx, rx, S, M, P, at, at + 4 * r0, at + 4 * m0,
+        at + 4 * n0, _raw_stream(dev.index)))
+    return (out.as_strided((S, M), (M, 1), 0), out.as_strided((P,), (1,), r0),
+            out.as_strided((P,), (1,), m0), out.as_strided((), (), n0))
