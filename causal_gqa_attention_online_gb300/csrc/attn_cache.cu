@@ -112,10 +112,11 @@ template <typename F> int with_workspace(unsigned long long bytes, cudaStream_t 
     return rc;
 }
 
-// Bytes of expanded keys and values that one group of sequences may take: the
-// rows stay in the L2 cache between the expansion and the kernel that reads
-// them (a longer sequence than this is a group of its own).
-constexpr long long kExpandBytes = 64LL << 20;
+// Bytes of expanded keys and values that one group of sequences may take (a
+// longer sequence than this is a group of its own).  Larger groups fill the
+// prefill's grid better: four sequences of up to 8192 keys (134 MB) take one
+// launch of 256 units instead of two of 128, half of them over a short tail.
+constexpr long long kExpandBytes = 512LL << 20;
 
 // Attention over contiguous 16- or 32-bit copies of the keys and values, for
 // problems the 8-bit kernels do not take: groups of sequences one after the
