@@ -374,7 +374,7 @@ int attn_pages_fork(void *const *pools, const long long *page_bytes, int npools,
         set_error("attn_pages_fork: the outputs are a new version and may not alias the inputs");
         return ATTN_ERR_INVALID;
     }
-    return with_workspace(pages_fork_workspace(N, num_pages),
+    return with_workspace(pages_fork_workspace(page_bytes, npools, N, max_pages, num_pages),
                           reinterpret_cast<cudaStream_t>(stream), [&](void *ws) {
         return launch_pages_fork(pools, page_bytes, npools, block_table, seqlens, refcount, S,
                                  max_pages, num_pages, log2_of(page_size), parents, new_tokens, N,
@@ -405,7 +405,7 @@ int attn_pages_compact(void *const *pools, const long long *page_bytes, int npoo
         set_error("attn_pages_compact: refcount_out may not alias refcount");
         return ATTN_ERR_INVALID;
     }
-    return with_workspace(pages_compact_workspace(num_pages),
+    return with_workspace(pages_compact_workspace(page_bytes, npools, S, max_pages, num_pages),
                           reinterpret_cast<cudaStream_t>(stream), [&](void *ws) {
         return launch_pages_compact(pools, page_bytes, npools, block_table, refcount, S, max_pages,
                                     num_pages, block_table_out, refcount_out, remap, n_live, ws,

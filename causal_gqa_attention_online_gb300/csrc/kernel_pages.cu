@@ -7,6 +7,8 @@
 // work is latency bound (a few thousand entries); it runs as one cluster of
 // kPlanCtas blocks that meet at cluster barriers, so a plan is one launch
 // whatever its phases, and the copies and the table follow in a second one.
+// Where few bytes can move (kSmallBytes), and the pages' counts fit the cluster's
+// shared memory, the cluster does all of it: one launch and no workspace.
 // Page numbers are handed out lowest first and the results do not depend on
 // the order of any atomic: counts and minima only.
 //
@@ -56,18 +58,18 @@ template <typename V> __device__ __forceinline__ void copy_units(uint8_t *dst, c
     }
 }
 
-// Pages src[i] -> dst[i] (src_back: src[n - 1 - i] -> dst[i]) of every pool, by
-// the warps of the grid.  Entries outside the pools are skipped.
-__device__ void copy_pages(const PoolTable &t, const int32_t *src, const int32_t *dst, int n,
-                           int src_pages, int dst_pages, bool src_back = false) {
+// Pages pair(i).x -> pair(i).y of every pool for i < n, by warp `first`, first +
+// step, ....  Pairs outside the pools are skipped.
+template <typename F>
+__device__ __forceinline__ void copy_pairs(const PoolTable &t, int n, int src_pages, int dst_pages,
+                                           long long first, long long step, F pair) {
     const int per_page = t.first_chunk[t.n];
     const long long total = (long long)n * per_page;
     const int lane = threadIdx.x & 31;
-    const long long step = (long long)gridDim.x * (blockDim.x / 32);
-    for (long long c = (long long)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); c < total;
-         c += step) {
+    for (long long c = first; c < total; c += step) {
         const int i = (int)(c / per_page), r = (int)(c - (long long)i * per_page);
-        const int sp = __ldcg(src + (src_back ? n - 1 - i : i)), dp = __ldcg(dst + i);
+        const int2 sd = pair(i);
+        const int sp = sd.x, dp = sd.y;
         if (sp < 0 || sp >= src_pages || dp < 0 || dp >= dst_pages) continue;
         int pool = 0;
         while (r >= t.first_chunk[pool + 1]) ++pool;
@@ -81,6 +83,17 @@ __device__ void copy_pages(const PoolTable &t, const int32_t *src, const int32_t
         else if ((low & 3) == 0) copy_units<uint32_t>(d, s, len / 4, lane);
         else copy_units<uint8_t>(d, s, len, lane);
     }
+}
+
+// Pages src[i] -> dst[i] (src_back: src[n - 1 - i] -> dst[i]), by the warps of the
+// grid.
+__device__ __forceinline__ void copy_pages(const PoolTable &t, const int32_t *src, const int32_t *dst, int n,
+                                           int src_pages, int dst_pages, bool src_back = false) {
+    const int warps = blockDim.x / 32;
+    copy_pairs(t, n, src_pages, dst_pages, (long long)blockIdx.x * warps + (threadIdx.x >> 5),
+               (long long)gridDim.x * warps, [&](int i) {
+        return make_int2(__ldcg(src + (src_back ? n - 1 - i : i)), __ldcg(dst + i));
+    });
 }
 
 __global__ void __launch_bounds__(kCopyThreads)
@@ -365,6 +378,174 @@ __global__ void __launch_bounds__(kCopyThreads)
     if (t.n > 0) copy_pages(t, a.src, a.dst, __ldcg(a.count), a.P, a.P);
 }
 
+// The whole of a small fork by one cluster.  The per-page counts live in the shared
+// memory of the block that has the page's part (parts of 2^part_shift pages), the
+// free pages of a part in a list of its own, and each block copies the pages of
+// its own slots.
+struct SmallFork {
+    ForkArgs a;
+    int part_shift;
+};
+
+__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
+    fork_small_kernel(const __grid_constant__ SmallFork sf, const __grid_constant__ PoolTable t) {
+    extern __shared__ __align__(16) unsigned char dyn[];
+    __shared__ int warps[32];
+    __shared__ int part_free, part_wide, part_copies;
+    __shared__ unsigned long long part_need;
+    const ForkArgs &a = sf.a;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int gt = blockIdx.x * kPlanThreads + tid;
+    const int gn = kPlanCtas * kPlanThreads;
+    constexpr int NW = kPlanThreads / 32;
+    const int per_p = 1 << sf.part_shift, pmask = per_p - 1;
+    const int per_s = (a.N + kPlanCtas - 1) / kPlanCtas;
+    // (entries are numbered in 32 bits here: the 64-bit minimum on another block's
+    // shared memory was seen to lose updates)
+    int2 *moves = reinterpret_cast<int2 *>(dyn);                   // [per_s] pages to copy
+    unsigned *claim = reinterpret_cast<unsigned *>(moves + per_s);  // [per_p]
+    int *was = reinterpret_cast<int *>(claim + per_p), *full = was + per_p, *held = full + per_p;
+    int *list = held + per_p;                   // [per_p] free pages of the part
+    int *need = list + per_p;                   // [per_s]
+    // page c's entry of an array
+    auto of = [&](auto *arr, int c) { return cluster.map_shared_rank(arr, c >> sf.part_shift) + (c & pmask); };
+    auto keep = [&](int i, int j, int c) -> bool {
+        if (c < 0 || c >= a.P) return false;
+        const int refs = __ldg(a.refs + c);
+        return refs > 0 && *of(full, c) == 0 && refs <= *of(was, c) &&
+               *of(claim, c) == (unsigned)(i * a.M + j);
+    };
+    const int p0 = min(blockIdx.x << sf.part_shift, (unsigned)a.P), p1 = min(p0 + per_p, a.P);
+    const int s0 = min((int)blockIdx.x * per_s, a.N), s1 = min(s0 + per_s, a.N);
+    // 1. clear; the free pages of the part, in ascending order
+    for (int p = tid; p < per_p; p += kPlanThreads) {
+        was[p] = 0;
+        full[p] = 0;
+        held[p] = 0;
+        claim[p] = ~0u;
+    }
+    if (tid == 0) {
+        part_wide = 0;
+        part_copies = 0;
+        part_need = 0;
+    }
+    int nf = 0;
+    for (int q = p0; q < p1; q += kPlanThreads) {
+        const int p = q + tid;
+        const int f = p < p1 && __ldg(a.refs + p) == 0;
+        int tot;
+        const int at = nf + block_scan(f, warps, &tot);
+        if (f) list[at] = p;
+        nf += tot;
+    }
+    if (tid == 0) part_free = nf;
+    cluster.sync();
+    // 2. references by the old table; full entries and claims of the new one
+    for (long long e = gt; e < (long long)a.S * a.M; e += gn) {
+        const int c = __ldg(a.table + e);
+        if (c >= 0 && c < a.P) atomicAdd(of(was, c), 1);
+    }
+    for (int i = s0 + warp; i < s1; i += NW) {
+        const Slot s = slot_of(a, i);
+        if (lane == 0) a.lens_out[i] = s.len;
+        if (s.parent < 0) continue;
+        if (lane == 0 && s.want > a.M) atomicAdd(&part_wide, 1);
+        const int last = (int)min(s.want, (long long)a.M);
+        for (int j = lane; j < last; j += 32) {
+            const int c = cand_of(a, s, j);
+            if (c < 0 || c >= a.P) continue;
+            if (j < s.nfull) atomicAdd(of(full, c), 1);
+            else atomicMin(of(claim, c), (unsigned)(i * a.M + j));
+        }
+    }
+    cluster.sync();
+    // 3. how many pages each slot takes
+    for (int i = s0 + warp; i < s1; i += NW) {
+        const Slot s = slot_of(a, i);
+        const int last = s.parent < 0 ? 0 : (int)min(s.want, (long long)a.M);
+        int cnt = 0;
+        for (int j = s.nfull + lane; j < last; j += 32) cnt += !keep(i, j, cand_of(a, s, j));
+        cnt = __reduce_add_sync(0xffffffffu, cnt);
+        if (lane == 0) {
+            need[i - s0] = cnt;
+            if (cnt) atomicAdd(&part_need, (unsigned long long)cnt);
+        }
+    }
+    cluster.sync();
+    // 4. entries that need a page take the free ones in the order of slots and entries
+    unsigned long long before = 0, total = 0;
+    int wide = 0, free_end[kPlanCtas], all_free = 0;
+#pragma unroll
+    for (int r = 0; r < kPlanCtas; ++r) {
+        const unsigned long long x = *cluster.map_shared_rank(&part_need, r);
+        if (r < (int)blockIdx.x) before += x;
+        total += x;
+        wide += *cluster.map_shared_rank(&part_wide, r);
+        all_free += *cluster.map_shared_rank(&part_free, r);
+        free_end[r] = all_free;
+    }
+    auto free_page = [&](int k) -> int {  // the k-th free page
+        int r = 0, first = 0;
+#pragma unroll
+        for (int x = 0; x < kPlanCtas - 1; ++x)
+            if (k >= free_end[x]) {
+                r = x + 1;
+                first = free_end[x];
+            }
+        return cluster.map_shared_rank(list, r)[k - first];
+    };
+    const long long missing = (long long)total - all_free;
+    const bool fine = missing <= 0 && wide == 0;
+    if (gt == 0) {
+        a.status[0] = missing > 0 ? (int)min(missing, (long long)INT_MAX) : 0;
+        a.status[1] = wide;
+        a.status[2] = fine ? (int)total : 0;
+    }
+    int taken = (int)before;
+    for (int i0 = s0; i0 < s1; i0 += NW) {
+        const int i = i0 + warp;
+        Slot s;
+        s.parent = -1;
+        s.nfull = s.len = 0;
+        s.want = 0;
+        if (i < s1 && fine) s = slot_of(a, i);
+        const int last = s.parent < 0 ? 0 : (int)min(s.want, (long long)a.M);
+        int tot;
+        int at = block_scan(lane == 0 && i < s1 ? need[i - s0] : 0, warps, &tot);
+        at = taken + __shfl_sync(0xffffffffu, at, 0);
+        taken += tot;
+        if (i >= s1) continue;
+        if (!fine && lane == 0) a.lens_out[i] = 0;
+        for (int j0 = 0; j0 < a.M; j0 += 32) {
+            const int j = j0 + lane;
+            const int c = j < last ? cand_of(a, s, j) : -1;
+            const bool get = j < last && j >= s.nfull && !keep(i, j, c);
+            const unsigned m = __ballot_sync(0xffffffffu, get);
+            int pg = c >= 0 && c < a.P ? c : -1;
+            if (get) pg = free_page(at + __popc(m & ((1u << lane) - 1u)));
+            at += __popc(m);
+            if (j < a.M) a.table_out[(long long)i * a.M + j] = pg;
+            if (j < last && j >= s.nfull) *of(held, pg) = 1;
+            if (get && c >= 0 && c < a.P && j == s.nfull && (s.len & ((1 << a.page_shift) - 1)))
+                moves[atomicAdd(&part_copies, 1)] = make_int2(c, pg);
+        }
+    }
+    cluster.sync();
+    // 5. the counts of the part's pages, and the block's copies
+    for (int p = p0 + tid; p < p1; p += kPlanThreads) {
+        const int r = __ldg(a.refs + p), k = p - p0;
+        a.refs_out[p] = fine ? r - was[k] + full[k] + held[k] : r;
+    }
+    if (gt == 0) {
+        int copies = 0;
+        for (int r = 0; r < kPlanCtas; ++r) copies += *cluster.map_shared_rank(&part_copies, r);
+        a.status[3] = copies;
+    }
+    if (t.n > 0) copy_pairs(t, part_copies, a.P, a.P, warp, NW, [&](int i) { return moves[i]; });
+    cluster.sync();  // every block's sums are read before it exits
+}
+
 // ------------------------------------------------------------------ compact
 
 struct CompactArgs {
@@ -429,6 +610,89 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
         a.remap[s] = d;
         a.refs_out[d] = __ldg(a.refs + s);
     }
+}
+
+// The whole of a small compaction by one cluster: a block has a part of the pages,
+// lists the live ones at or behind the live count (movers) and fills the holes
+// before it from the parts' lists, in ascending order both.
+__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
+    compact_small_kernel(const __grid_constant__ CompactArgs a, const __grid_constant__ PoolTable t) {
+    extern __shared__ __align__(16) unsigned char dyn[];
+    __shared__ int warps[32];
+    __shared__ int part_live, part_movers, part_holes;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int tid = threadIdx.x, warp = tid >> 5;
+    const int per = (a.P + kPlanCtas - 1) / kPlanCtas;
+    const int p0 = min((int)blockIdx.x * per, a.P), p1 = min(p0 + per, a.P);
+    int2 *moves = reinterpret_cast<int2 *>(dyn);       // [per] {page, hole}: the holes of this part
+    int *movers = reinterpret_cast<int *>(moves + per);  // [per]
+    int cnt = 0;
+    for (int p = p0 + tid; p < p1; p += kPlanThreads) cnt += __ldg(a.refs + p) > 0;
+    int tot;
+    block_scan(cnt, warps, &tot);
+    if (tid == 0) part_live = tot;
+    cluster.sync();
+    int n = 0;
+    for (int r = 0; r < kPlanCtas; ++r) n += *cluster.map_shared_rank(&part_live, r);
+    int nm = 0, nh = 0;
+    for (int q = p0; q < p1; q += kPlanThreads) {
+        const int p = q + tid;
+        const int r = p < p1 ? __ldg(a.refs + p) : 0;
+        const int mover = p < p1 && r > 0 && p >= n, hole = p < p1 && r <= 0 && p < n;
+        const int at_m = nm + block_scan(mover, warps, &tot);
+        nm += tot;
+        const int at_h = nh + block_scan(hole, warps, &tot);
+        nh += tot;
+        if (mover) movers[at_m] = p;
+        if (hole) moves[at_h].y = p;
+        if (p < p1) {
+            // (a mover's number and a hole's count follow below)
+            if (!mover) a.remap[p] = r > 0 ? p : -1;
+            if (!hole) a.refs_out[p] = p < n ? r : 0;
+        }
+    }
+    if (tid == 0) {
+        part_movers = nm;
+        part_holes = nh;
+        if (blockIdx.x == 0) *a.n_live = n;
+    }
+    cluster.sync();
+    int before = 0, end[kPlanCtas], sum = 0;
+#pragma unroll
+    for (int r = 0; r < kPlanCtas; ++r) {
+        if (r < (int)blockIdx.x) before += *cluster.map_shared_rank(&part_holes, r);
+        sum += *cluster.map_shared_rank(&part_movers, r);
+        end[r] = sum;
+    }
+    for (int k = tid; k < nh; k += kPlanThreads) {
+        int r = 0, first = 0;
+#pragma unroll
+        for (int x = 0; x < kPlanCtas - 1; ++x)
+            if (before + k >= end[x]) {
+                r = x + 1;
+                first = end[x];
+            }
+        const int p = cluster.map_shared_rank(movers, r)[before + k - first], d = moves[k].y;
+        moves[k].x = p;
+        a.remap[p] = d;
+        a.refs_out[d] = __ldg(a.refs + p);
+    }
+    __threadfence();
+    cluster.sync();
+    for (long long e = blockIdx.x * kPlanThreads + tid; e < (long long)a.S * a.M; e += kPlanCtas * kPlanThreads) {
+        const int c = __ldg(a.table + e);
+        a.table_out[e] = c >= 0 && c < a.P ? __ldcg(a.remap + c) : -1;
+    }
+    // (the holes lie in the first parts: their copies are spread over all blocks)
+    if (t.n > 0) {
+        for (int r = 0; r < kPlanCtas; ++r) {
+            const int m = *cluster.map_shared_rank(&part_holes, r);
+            const int2 *list = cluster.map_shared_rank(moves, r);
+            copy_pairs(t, m, a.P, a.P, blockIdx.x * (kPlanThreads / 32) + warp, kPlanCtas * (kPlanThreads / 32),
+                       [&](int i) { return list[i]; });
+        }
+    }
+    cluster.sync();  // every block's lists are read before it exits
 }
 
 __global__ void __launch_bounds__(kCopyThreads)
@@ -523,6 +787,56 @@ template <typename F> int for_pool_groups(const void *const *src, void *const *d
     return rc;
 }
 
+
+// What a cluster moves by itself: 8 SMs copy about 1 TB/s, so up to here the second
+// launch costs more than it saves.
+constexpr long long kSmallBytes = 4LL << 20;
+constexpr int kSmallShared = 200 * 1024;  // dynamic shared memory a block
+
+template <typename A>
+int launch_small(void (*kern)(A, PoolTable), const A &a, const PoolTable &t, size_t smem, const char *what,
+                 cudaStream_t stream) {
+    cudaError_t e = cudaSuccess;
+    if (smem > 40 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) {
+        set_error("%s: cudaFuncSetAttribute: %s", what, cudaGetErrorString(e));
+        return 3;
+    }
+    kern<<<kPlanCtas, kPlanThreads, smem, stream>>>(a, t);
+    return launched(what);
+}
+
+long long page_total(const long long *bytes, int n) {
+    long long x = 0;
+    for (int i = 0; i < n; ++i) x += bytes[i];
+    return x;
+}
+
+// log2 of the pages of a block's part, and the shared memory that a small fork
+// takes.
+int fork_part_shift(int P) {
+    int k = 0;
+    while ((8LL << k) < P) ++k;
+    return k;
+}
+size_t fork_small_shared(int N, int P) {
+    const size_t per_s = (N + kPlanCtas - 1) / kPlanCtas;
+    return ((size_t)20 << fork_part_shift(P)) + per_s * 12;
+}
+size_t compact_small_shared(int P) { return (size_t)((P + kPlanCtas - 1) / kPlanCtas) * 12; }
+
+constexpr long long kSmallEntries = 1 << 17;  // of a table
+
+bool fork_is_small(const long long *bytes, int npools, int N, int M, int P) {
+    return (long long)N * M <= kSmallEntries && npools <= kMaxPools && N <= (1 << 20) && P <= (1 << 20) &&
+           fork_small_shared(N, P) <= kSmallShared && (double)N * page_total(bytes, npools) <= kSmallBytes;
+}
+// (at most half of the pages move)
+bool compact_is_small(const long long *bytes, int npools, int S, int M, int P) {
+    return (long long)S * M <= kSmallEntries && npools <= kMaxPools && P <= (1 << 20) && compact_small_shared(P) <= kSmallShared &&
+           0.5 * P * page_total(bytes, npools) <= kSmallBytes;
+}
+
 }  // namespace
 
 int launch_pages_copy(const void *const *src_pools, void *const *dst_pools, const long long *bytes,
@@ -537,7 +851,8 @@ int launch_pages_copy(const void *const *src_pools, void *const *dst_pools, cons
     });
 }
 
-unsigned long long pages_fork_workspace(int N, int P) {
+unsigned long long pages_fork_workspace(const long long *bytes, int npools, int N, int M, int P) {
+    if (fork_is_small(bytes, npools, N, M, P)) return 0;
     return 8ull * P + 4ull * (4ull * P + 3ull * N + 1ull);
 }
 
@@ -561,6 +876,13 @@ int launch_pages_fork(void *const *pools, const long long *bytes, int npools,
     a.lens_out = seqlens_out;
     a.refs_out = refcount_out;
     a.status = status;
+    if (fork_is_small(bytes, npools, N, M, P)) {
+        PoolTable t;
+        const int rc = fill_pools(t, pools, pools, bytes, npools);
+        if (rc) return rc;
+        return launch_small(fork_small_kernel, SmallFork{a, fork_part_shift(P)}, t, fork_small_shared(N, P),
+                            "page fork kernel", stream);
+    }
     a.claim = static_cast<unsigned long long *>(ws);
     a.was = reinterpret_cast<int32_t *>(a.claim + P);
     a.full = a.was + P;
@@ -584,7 +906,9 @@ int launch_pages_fork(void *const *pools, const long long *bytes, int npools,
     });
 }
 
-unsigned long long pages_compact_workspace(int P) { return 4ull * (2ull * P + 2ull); }
+unsigned long long pages_compact_workspace(const long long *bytes, int npools, int S, int M, int P) {
+    return compact_is_small(bytes, npools, S, M, P) ? 0 : 4ull * (2ull * P + 1ull);
+}
 
 int launch_pages_compact(void *const *pools, const long long *bytes, int npools,
                          const int32_t *block_table, const int32_t *refcount, int S, int M, int P,
@@ -600,6 +924,12 @@ int launch_pages_compact(void *const *pools, const long long *bytes, int npools,
     a.refs_out = refcount_out;
     a.remap = remap;
     a.n_live = n_live;
+    if (compact_is_small(bytes, npools, S, M, P)) {
+        PoolTable t;
+        const int rc = fill_pools(t, pools, pools, bytes, npools);
+        if (rc) return rc;
+        return launch_small(compact_small_kernel, a, t, compact_small_shared(P), "page compact kernel", stream);
+    }
     a.src = static_cast<int32_t *>(ws);
     a.dst = a.src + P;
     a.count = a.dst + P;

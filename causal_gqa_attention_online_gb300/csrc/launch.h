@@ -135,14 +135,15 @@ constexpr int kMaxPools = 64;  // pools one launch copies
 int launch_pages_copy(const void *const *src_pools, void *const *dst_pools, const long long *bytes,
                       int npools, int src_pages, int dst_pages, const int32_t *src,
                       const int32_t *dst, int n, cudaStream_t stream);
-// ws: the given number of bytes at an 8-byte aligned address.
-unsigned long long pages_fork_workspace(int N, int P);
+// ws: the given number of bytes (0: null) at an 8-byte aligned address.
+unsigned long long pages_fork_workspace(const long long *bytes, int npools, int N, int M, int P);
 int launch_pages_fork(void *const *pools, const long long *bytes, int npools,
                       const int32_t *block_table, const int32_t *seqlens, const int32_t *refcount,
                       int S, int M, int P, int page_shift, const int32_t *parents,
                       const int32_t *new_tokens, int N, int32_t *table_out, int32_t *seqlens_out,
                       int32_t *refcount_out, int32_t *status, void *ws, cudaStream_t stream);
-unsigned long long pages_compact_workspace(int P);
+unsigned long long pages_compact_workspace(const long long *bytes, int npools, int S, int M,
+                                           int P);
 int launch_pages_compact(void *const *pools, const long long *bytes, int npools,
                          const int32_t *block_table, const int32_t *refcount, int S, int M, int P,
                          int32_t *table_out, int32_t *refcount_out, int32_t *remap,

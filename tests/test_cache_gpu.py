@@ -499,15 +499,23 @@ def check_fork(g, table, lens, refs, parents, new, page, shapes=(160, 5000)):
     return ref
 
 
+# pages of a few bytes (one cluster does everything), and of so many that the copies
+# take a launch of their own
+BIG = (1 << 18, 5000)
+
+
+@pytest.mark.parametrize("shapes", [(160, 5000), BIG, ()])
 @pytest.mark.parametrize("seed", range(12))
-def test_fork(seed):
+def test_fork(seed, shapes):
     g = np.random.default_rng(300 + seed)
     S, M, page = int(g.integers(1, 40)), int(g.integers(1, 50)), int(2 ** g.integers(0, 7))
     table, lens, refs = random_table(g, S, M, page, S * M + 5)
     N = int(g.integers(1, 50))
     parents = g.integers(-1, S + 1, N)
     new = np.minimum(g.integers(-2, 3 * page, N), M * page // 2)
-    check_fork(g, table, lens, refs, parents, None if seed % 4 == 0 else new, page)
+    if shapes == BIG and len(refs) * sum(shapes) > 1 << 28:
+        shapes = (1 << 28) // len(refs) // 16 * 16, 48
+    check_fork(g, table, lens, refs, parents, None if seed % 4 == 0 else new, page, shapes)
 
 
 def test_fork_of_many_slots_and_wide_growth():
@@ -518,37 +526,40 @@ def test_fork_of_many_slots_and_wide_growth():
     assert ref[3][0] == 0 and ref[3][3] > 300
 
 
-def test_fork_makes_a_rolled_back_page_private():
+@pytest.mark.parametrize("shapes", [(160, 5000), BIG])
+def test_fork_makes_a_rolled_back_page_private(shapes):
     # slot 0 rolled back into page 3, which slot 1 still holds as a full page
     table = np.array([[3, -1], [3, 1]], np.int32)
     refs = np.array([0, 1, 0, 2], np.int32)
-    ref = check_fork(np.random.default_rng(0), table, np.array([2, 5]), refs, [0, 1], [1, 1], 4)
+    ref = check_fork(np.random.default_rng(0), table, np.array([2, 5]), refs, [0, 1], [1, 1], 4, shapes)
     assert ref[0].tolist() == [[0, -1], [3, 1]] and ref[4] == [(3, 0)]
     # the same page held by nobody else but a pin: copied, too
     ref = check_fork(np.random.default_rng(0), table[:1], np.array([2]), np.array([0, 0, 0, 2]), [0],
-                     [1], 4)
+                     [1], 4, shapes)
     assert ref[4] == [(3, 0)]
 
 
-def test_fork_without_room_changes_nothing():
+@pytest.mark.parametrize("shapes", [(160, 5000), BIG])
+def test_fork_without_room_changes_nothing(shapes):
     g = np.random.default_rng(33)
     table, lens, refs = random_table(g, 6, 8, 4, 14, pins=0)
-    ref = check_fork(g, table, lens, refs, [0, 1, 2, 3, 4, 5] * 3, [9] * 18, 4)
+    ref = check_fork(g, table, lens, refs, [0, 1, 2, 3, 4, 5] * 3, [9] * 18, 4, shapes)
     assert ref[3][0] > 0
-    ref = check_fork(g, table, lens, refs, [0, -1], [100, 0], 4)
+    ref = check_fork(g, table, lens, refs, [0, -1], [100, 0], 4, shapes)
     assert ref[3][1] == 1
-    ref = check_fork(g, table, lens, refs, [0, -1], [2 ** 31 - 1, 0], 4)
+    ref = check_fork(g, table, lens, refs, [0, -1], [2 ** 31 - 1, 0], 4, shapes)
     assert ref[3][1] == 1
 
 
-def test_fork_of_an_inconsistent_table_stays_in_bounds():
+@pytest.mark.parametrize("small", [True, False])
+def test_fork_of_an_inconsistent_table_stays_in_bounds(small):
     # entries out of range, lengths past the table, counts that do not fit: wrong pages
     # at worst; the guard bytes behind every buffer stay
     g = np.random.default_rng(34)
     S, M, P, N = 7, 6, 20, 30
     table = g.integers(-5, P + 5, (S, M)).astype(np.int32)
     lens = g.integers(-10, 10 * M, S).astype(np.int32)
-    pools = random_pools(g, P, (100,))
+    pools = random_pools(g, P, (100,) if small else (1 << 19,))
     for refs in (np.zeros(P), np.full(P, 3), g.integers(-1, 3, P)):
         out = attn.attn_pages_fork(pools, i32(table), i32(lens), i32(refs), i32(g.integers(-3, S + 3, N)), 4,
                                    new_tokens=i32(g.integers(-5, 9, N)))
@@ -565,11 +576,14 @@ def test_fork_without_slots_frees_everything():
 
 @pytest.mark.parametrize("P", [1, 2, 31, 1024, 5000, 40001])
 @pytest.mark.parametrize("share", [0.0, 0.1, 0.5, 0.95, 1.0])
-def test_compact(P, share):
+@pytest.mark.parametrize("big", [False, True])
+def test_compact(P, share, big):
     g = np.random.default_rng(P + int(100 * share))
+    if big and P < 1024:
+        pytest.skip("the same path as without")
     refs = np.where(g.random(P) < share, g.integers(1, 4, P), 0).astype(np.int32)
     table = g.integers(-3, P + 3, (9, 33)).astype(np.int32)
-    pools = random_pools(g, P, (48, 33))
+    pools = random_pools(g, P, ((1 << 25) // P // 16 * 16, 33) if big else (48, 33))
     want = [p.cpu().numpy().copy() for p in pools]
     out = attn.attn_pages_compact(pools, i32(table), i32(refs))
     ref = cache_ref.compact(table, refs)
