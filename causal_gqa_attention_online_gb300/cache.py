@@ -33,22 +33,23 @@ ATTN_CACHE_E4M3, ATTN_CACHE_INT8 = 0, 1
 _CACHE_CODE = {torch.float8_e4m3fn: ATTN_CACHE_E4M3, torch.int8: ATTN_CACHE_INT8}
 
 
-def _raw_stream(i):
-    """The handle of device ``i``'s current stream (what
-    torch.cuda.current_stream(i).cuda_stream is, without the object: 0.1 us
-    against 2.9)."""
-    return torch._C._cuda_getCurrentRawStream(i)
+# The handle of device i's current stream and the current device: what
+# torch.cuda.current_stream(i).cuda_stream and torch.cuda.current_device() give,
+# without their objects and checks (0.2 us against 4 a call).
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
-def _here(dev, stream):
-    """Whether a call on ``dev`` can go to the current stream as it is.
+def _here(i, stream):
+    """Whether a call on device ``i`` can go to the current stream as it is.
     (Otherwise the entry points call themselves with ``_elsewhere`` in force.)"""
-    return stream is None and dev.type == "cuda" and dev.index == torch.cuda.current_device()
+    return stream is None and i >= 0 and i == _current_device()
 
 
-def _elsewhere(dev, stream):
-    """Makes ``dev`` and ``stream`` current: the library works on the current
+def _elsewhere(t, stream):
+    """Makes t's device and ``stream`` current: the library works on the current
     device, and outputs that a call allocates belong to its stream."""
+    dev = t.device
     if dev.type != "cuda":
         raise ValueError(f"the tensors are on {dev}: the library runs on CUDA devices only")
     if stream is None:
@@ -58,20 +59,20 @@ def _elsewhere(dev, stream):
     return torch.cuda.stream(stream)
 
 
-def _tensor(name, t, dtype, shape, dev):
-    """Checks one tensor; returns its address."""
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == dev:
+def _tensor(name, t, dtype, shape, i):
+    """Checks one tensor (of device ``i``, -1: the CPU); returns its address."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == i:
         return t.data_ptr()
     n = 1
     for x in shape:
         n *= x
-    _check_tensor(name, t, dtype, n, dev)
+    _check_tensor(name, t, dtype, n, torch.device("cuda", i) if i >= 0 else torch.device("cpu"))
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     return t.data_ptr()
 
 
-def _cache(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, dev):
+def _cache(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, i):
     """Checks a cache; returns its addresses (k_pages, v_pages, k_scale,
     v_scale, block_table, seqlens_k), sizes (P, page, block, Hkv, D, Dv, B,
     max_pages) and code."""
@@ -88,12 +89,12 @@ def _cache(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, dev):
     if nblk < 1 or page % nblk:
         raise ValueError(f"k_scale: {nblk} blocks do not divide a page of {page} tokens")
     scales = (P, nblk, Hkv)
-    ptrs = (_tensor("k_pages", k_pages, k_pages.dtype, (P, page, Hkv, D), dev),
-            _tensor("v_pages", v_pages, k_pages.dtype, (P, page, Hkv, Dv), dev),
-            _tensor("k_scale", k_scale, torch.float32, scales, dev),
-            _tensor("v_scale", v_scale, torch.float32, scales, dev),
-            _tensor("block_table", block_table, torch.int32, (B, M), dev),
-            _tensor("seqlens_k", seqlens_k, torch.int32, (B,), dev))
+    ptrs = (_tensor("k_pages", k_pages, k_pages.dtype, (P, page, Hkv, D), i),
+            _tensor("v_pages", v_pages, k_pages.dtype, (P, page, Hkv, Dv), i),
+            _tensor("k_scale", k_scale, torch.float32, scales, i),
+            _tensor("v_scale", v_scale, torch.float32, scales, i),
+            _tensor("block_table", block_table, torch.int32, (B, M), i),
+            _tensor("seqlens_k", seqlens_k, torch.int32, (B,), i))
     return ptrs, (P, page, page // nblk, Hkv, D, Dv, B, M), code
 
 
@@ -103,27 +104,27 @@ def attn_cache_append(k, v, k_pages, v_pages, k_scale, v_scale, block_table, seq
     the cache behind the ``seqlens_k`` rows each sequence has; ``seqlens_new``
     int32 [B]: how many of the N are there (default: all).  The pages they go to
     are in ``block_table`` already.  ``seqlens_k`` is not changed."""
-    dev = k.device
+    i = k.get_device()
     (kp, vp, ks, vs, table, lens), (P, page, block, Hkv, D, Dv, B, M), code = _cache(
-        k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, dev)
+        k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, i)
     if k.dim() != 4 or k.shape[0] != B or k.shape[2:] != (Hkv, D):
         raise ValueError(f"k: shape {tuple(k.shape)}, expected [{B}, N, {Hkv}, {D}]")
     dtype = _DTYPE_CODE.get(k.dtype)
     if dtype is None:
         raise TypeError(f"k: dtype {k.dtype}, expected float32, float16 or bfloat16")
     N = k.shape[1]
-    kx = _tensor("k", k, k.dtype, (B, N, Hkv, D), dev)
-    vx = _tensor("v", v, k.dtype, (B, N, Hkv, Dv), dev)
+    kx = _tensor("k", k, k.dtype, (B, N, Hkv, D), i)
+    vx = _tensor("v", v, k.dtype, (B, N, Hkv, Dv), i)
     new = None
     if seqlens_new is not None:
-        new = _tensor("seqlens_new", seqlens_new, torch.int32, (B,), dev)
-    if not _here(dev, stream):
-        with _elsewhere(dev, stream):
+        new = _tensor("seqlens_new", seqlens_new, torch.int32, (B,), i)
+    if not _here(i, stream):
+        with _elsewhere(k, stream):
             return attn_cache_append(k, v, k_pages, v_pages, k_scale, v_scale, block_table,
                                      seqlens_k, seqlens_new=seqlens_new)
     _check(load_library().attn_cache_append(kx, vx, kp, vp, ks, vs, B, N, Hkv, D, Dv, new, lens,
                                             table, M, page, P, block, code, dtype,
-                                            _raw_stream(dev.index)))
+                                            _raw_stream(i)))
 
 
 def attn_cache_append_varlen(k, v, cu_seqlens_new, max_new, k_pages, v_pages, k_scale, v_scale,
@@ -131,25 +132,25 @@ def attn_cache_append_varlen(k, v, cu_seqlens_new, max_new, k_pages, v_pages, k_
     """attn_cache_append with the new rows packed: k [T,Hkv,D], v [T,Hkv,Dv],
     sequence b's rows [cu_seqlens_new[b], cu_seqlens_new[b + 1]), at most
     ``max_new`` of them."""
-    dev = k.device
+    i = k.get_device()
     (kp, vp, ks, vs, table, lens), (P, page, block, Hkv, D, Dv, B, M), code = _cache(
-        k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, dev)
+        k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, i)
     if k.dim() != 3 or k.shape[1:] != (Hkv, D):
         raise ValueError(f"k: shape {tuple(k.shape)}, expected [T, {Hkv}, {D}]")
     dtype = _DTYPE_CODE.get(k.dtype)
     if dtype is None:
         raise TypeError(f"k: dtype {k.dtype}, expected float32, float16 or bfloat16")
     T = k.shape[0]
-    kx = _tensor("k", k, k.dtype, (T, Hkv, D), dev)
-    vx = _tensor("v", v, k.dtype, (T, Hkv, Dv), dev)
-    cu = _tensor("cu_seqlens_new", cu_seqlens_new, torch.int32, (B + 1,), dev)
-    if not _here(dev, stream):
-        with _elsewhere(dev, stream):
+    kx = _tensor("k", k, k.dtype, (T, Hkv, D), i)
+    vx = _tensor("v", v, k.dtype, (T, Hkv, Dv), i)
+    cu = _tensor("cu_seqlens_new", cu_seqlens_new, torch.int32, (B + 1,), i)
+    if not _here(i, stream):
+        with _elsewhere(k, stream):
             return attn_cache_append_varlen(k, v, cu_seqlens_new, max_new, k_pages, v_pages,
                                             k_scale, v_scale, block_table, seqlens_k)
     _check(load_library().attn_cache_append_varlen(kx, vx, kp, vp, ks, vs, B, T, int(max_new), Hkv,
                                                    D, Dv, cu, lens, table, M, page, P, block, code,
-                                                   dtype, _raw_stream(dev.index)))
+                                                   dtype, _raw_stream(i)))
 
 
 def attn_fwd_paged_q8(q, k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, o=None,
@@ -158,49 +159,49 @@ def attn_fwd_paged_q8(q, k_pages, v_pages, k_scale, v_scale, block_table, seqlen
     """attn_fwd_paged over an 8-bit cache: q [B,Q,Hq,D]; ``seqlens_k`` counts the
     keys to attend to (append first).  Returns (o [B,Q,Hq,Dv], lse [B,Q,Hq] or
     None)."""
-    dev = q.device
+    i = q.get_device()
     (kp, vp, ks, vs, table, lens), (P, page, block, Hkv, D, Dv, B, M), code = _cache(
-        k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, dev)
+        k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, i)
     if q.dim() != 4 or q.shape[0] != B or q.shape[3] != D:
         raise ValueError(f"q: shape {tuple(q.shape)}, expected [{B}, Q, Hq, {D}]")
     dtype = _DTYPE_CODE.get(q.dtype)
     if dtype is None:
         raise TypeError(f"q: dtype {q.dtype}, expected float32, float16 or bfloat16")
     Q, Hq = q.shape[1], q.shape[2]
-    if not _here(dev, stream):
-        with _elsewhere(dev, stream):
+    if not _here(i, stream):
+        with _elsewhere(q, stream):
             return attn_fwd_paged_q8(q, k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k,
                                      o, lse, seqlens_q=seqlens_q, window=window, scale=scale,
                                      algo=algo, mask=mask, want_lse=want_lse)
-    qx = _tensor("q", q, q.dtype, (B, Q, Hq, D), dev)
+    qx = _tensor("q", q, q.dtype, (B, Q, Hq, D), i)
     if o is None:
         o = (torch.empty_like(q) if D == Dv else
-             torch.empty((B, Q, Hq, Dv), dtype=q.dtype, device=dev))
+             torch.empty((B, Q, Hq, Dv), dtype=q.dtype, device=q.device))
     if lse is None and want_lse:
-        lse = torch.empty((B, Q, Hq), dtype=torch.float32, device=dev)
-    ox = _tensor("o", o, q.dtype, (B, Q, Hq, Dv), dev)
-    lx = None if lse is None else _tensor("lse", lse, torch.float32, (B, Q, Hq), dev)
-    sq = None if seqlens_q is None else _tensor("seqlens_q", seqlens_q, torch.int32, (B,), dev)
+        lse = torch.empty((B, Q, Hq), dtype=torch.float32, device=q.device)
+    ox = _tensor("o", o, q.dtype, (B, Q, Hq, Dv), i)
+    lx = None if lse is None else _tensor("lse", lse, torch.float32, (B, Q, Hq), i)
+    sq = None if seqlens_q is None else _tensor("seqlens_q", seqlens_q, torch.int32, (B,), i)
     _check(load_library().attn_fwd_paged_q8(
         qx, kp, vp, ks, vs, ox, lx, B, Hq, Hkv, Q, D, Dv, table, M, page, P, block, code, sq, lens,
         int(window), 1.0 / math.sqrt(D) if scale is None else float(scale), MASKS[mask], dtype,
-        ALGOS[algo], _raw_stream(dev.index)))
+        ALGOS[algo], _raw_stream(i)))
     return o, lse
 
 
-def _pool_arrays(pools, pages, dev, what):
-    """Pointers and page bytes of pools whose first axis counts ``pages`` pages,
-    as 64-bit arrays."""
+def _pool_arrays(pools, pages, i, what):
+    """Pointers and page bytes of pools (of device ``i``) whose first axis counts
+    ``pages`` pages, as 64-bit arrays."""
     ptrs, sizes = array.array("Q"), array.array("q")
-    for i, t in enumerate(pools):
-        if t.dim() < 1 or t.shape[0] != pages:
-            raise ValueError(f"{what}[{i}]: shape {tuple(t.shape)}, expected {pages} pages first")
+    for k, t in enumerate(pools):
+        if t.dim() < 1 or t.size(0) != pages:
+            raise ValueError(f"{what}[{k}]: shape {tuple(t.shape)}, expected {pages} pages first")
         if not t.is_contiguous():
-            raise ValueError(f"{what}[{i}] must be contiguous")
-        if t.device != dev:
-            raise ValueError(f"{what}[{i}] is on {t.device}, expected {dev}")
+            raise ValueError(f"{what}[{k}] must be contiguous")
+        if t.get_device() != i:
+            raise ValueError(f"{what}[{k}] is on {t.device}, unlike the tables")
         ptrs.append(t.data_ptr())
-        sizes.append(t.nbytes // max(pages, 1))
+        sizes.append(t.nbytes // pages if pages else 0)
     return ptrs, sizes
 
 
@@ -215,26 +216,26 @@ def attn_pages_copy(src_pools, dst_pools, src, dst, *, stream=None):
     ``src``, ``dst``: int32 [n]; the dst pages are distinct, and none of them is
     a src page of the same pool.  Pairs with a page that does not exist are
     skipped."""
-    dev = src.device
+    i = src.get_device()
     if len(src_pools) != len(dst_pools):
         raise ValueError(f"{len(src_pools)} source pools and {len(dst_pools)} destinations")
     n = src.numel()
-    sx = _tensor("src", src, torch.int32, (n,), dev)
-    dx = _tensor("dst", dst, torch.int32, (n,), dev)
+    sx = _tensor("src", src, torch.int32, (n,), i)
+    dx = _tensor("dst", dst, torch.int32, (n,), i)
     sp = src_pools[0].shape[0] if len(src_pools) else 0
     dp = dst_pools[0].shape[0] if len(dst_pools) else 0
-    sptr, sbytes = _pool_arrays(src_pools, sp, dev, "src_pools")
+    sptr, sbytes = _pool_arrays(src_pools, sp, i, "src_pools")
     if dst_pools is src_pools:
         dptr = sptr
     else:
-        dptr, dbytes = _pool_arrays(dst_pools, dp, dev, "dst_pools")
+        dptr, dbytes = _pool_arrays(dst_pools, dp, i, "dst_pools")
         if sbytes != dbytes:
             raise ValueError("the pages of a source pool and of its destination differ in size")
-    if not _here(dev, stream):
-        with _elsewhere(dev, stream):
+    if not _here(i, stream):
+        with _elsewhere(src, stream):
             return attn_pages_copy(src_pools, dst_pools, src, dst)
     _check(load_library().attn_pages_copy(_at(sptr), _at(dptr), _at(sbytes), len(sptr), sp, dp, sx,
-                                          dx, n, _raw_stream(dev.index)))
+                                          dx, n, _raw_stream(i)))
 
 
 def attn_pages_fork(pools, block_table, seqlens, refcount, parents, page_size, *, new_tokens=None,
@@ -250,27 +251,27 @@ def attn_pages_fork(pools, block_table, seqlens, refcount, parents, page_size, *
     new tensors; status: pages that were missing, slots that do not fit
     max_pages, pages taken, pages copied.  Where one of the first two is not 0,
     nothing was copied, the new table is empty and the old version still stands."""
-    dev = block_table.device
+    i = block_table.get_device()
     S, M = block_table.shape
     P, N = refcount.numel(), parents.numel()
-    tx = _tensor("block_table", block_table, torch.int32, (S, M), dev)
-    lx = _tensor("seqlens", seqlens, torch.int32, (S,), dev)
-    rx = _tensor("refcount", refcount, torch.int32, (P,), dev)
-    px = _tensor("parents", parents, torch.int32, (N,), dev)
-    nx = None if new_tokens is None else _tensor("new_tokens", new_tokens, torch.int32, (N,), dev)
-    ptrs, sizes = _pool_arrays(pools, P, dev, "pools")
-    if not _here(dev, stream):
-        with _elsewhere(dev, stream):
+    tx = _tensor("block_table", block_table, torch.int32, (S, M), i)
+    lx = _tensor("seqlens", seqlens, torch.int32, (S,), i)
+    rx = _tensor("refcount", refcount, torch.int32, (P,), i)
+    px = _tensor("parents", parents, torch.int32, (N,), i)
+    nx = None if new_tokens is None else _tensor("new_tokens", new_tokens, torch.int32, (N,), i)
+    ptrs, sizes = _pool_arrays(pools, P, i, "pools")
+    if not _here(i, stream):
+        with _elsewhere(block_table, stream):
             return attn_pages_fork(pools, block_table, seqlens, refcount, parents, page_size,
                                    new_tokens=new_tokens)
     # one allocation: the new version's table, lengths, counts, and the status
-    out = torch.empty((N * M + N + P + 4,), dtype=torch.int32, device=dev)
+    out = torch.empty((N * M + N + P + 4,), dtype=torch.int32, device=block_table.device)
     at, l0, r0, s0 = out.data_ptr(), N * M, N * M + N, N * M + N + P
     _check(load_library().attn_pages_fork(
         _at(ptrs), _at(sizes), len(ptrs), tx, lx, rx, S, M, P, int(page_size), px, nx, N, at,
-        at + 4 * l0, at + 4 * r0, at + 4 * s0, _raw_stream(dev.index)))
-    return (out.as_strided((N, M), (M, 1), 0), out.as_strided((N,), (1,), l0),
-            out.as_strided((P,), (1,), r0), out.as_strided((4,), (1,), s0))
+        at + 4 * l0, at + 4 * r0, at + 4 * s0, _raw_stream(i)))
+    table_out, lens_out, refs_out, status = out.split_with_sizes((l0, N, P, 4))
+    return table_out.view(N, M), lens_out, refs_out, status
 
 
 def attn_pages_compact(pools, block_table, refcount, *, stream=None):
@@ -278,19 +279,19 @@ def attn_pages_compact(pools, block_table, refcount, *, stream=None):
     pool, in place, and renumbers them: returns (block_table, refcount, remap
     [P], n_live []), new tensors; remap: a live page's new number, -1 for a free
     one."""
-    dev = block_table.device
+    i = block_table.get_device()
     S, M = block_table.shape
     P = refcount.numel()
-    tx = _tensor("block_table", block_table, torch.int32, (S, M), dev)
-    rx = _tensor("refcount", refcount, torch.int32, (P,), dev)
-    ptrs, sizes = _pool_arrays(pools, P, dev, "pools")
-    if not _here(dev, stream):
-        with _elsewhere(dev, stream):
+    tx = _tensor("block_table", block_table, torch.int32, (S, M), i)
+    rx = _tensor("refcount", refcount, torch.int32, (P,), i)
+    ptrs, sizes = _pool_arrays(pools, P, i, "pools")
+    if not _here(i, stream):
+        with _elsewhere(block_table, stream):
             return attn_pages_compact(pools, block_table, refcount)
-    out = torch.empty((S * M + 2 * P + 1,), dtype=torch.int32, device=dev)
+    out = torch.empty((S * M + 2 * P + 1,), dtype=torch.int32, device=block_table.device)
     at, r0, m0, n0 = out.data_ptr(), S * M, S * M + P, S * M + 2 * P
     _check(load_library().attn_pages_compact(
         _at(ptrs), _at(sizes), len(ptrs), tx, rx, S, M, P, at, at + 4 * r0, at + 4 * m0,
-        at + 4 * n0, _raw_stream(dev.index)))
-    return (out.as_strided((S, M), (M, 1), 0), out.as_strided((P,), (1,), r0),
-            out.as_strided((P,), (1,), m0), out.as_strided((), (), n0))
+        at + 4 * n0, _raw_stream(i)))
+    table_out, refs_out, remap, n_live = out.split_with_sizes((r0, P, P, 1))
+    return table_out.view(S, M), refs_out, remap, n_live.view(())

@@ -657,11 +657,13 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
         if (blockIdx.x == 0) *a.n_live = n;
     }
     cluster.sync();
-    int before = 0, end[kPlanCtas], sum = 0;
+    int before = 0, end[kPlanCtas], holes_end[kPlanCtas], sum = 0, holes = 0;
 #pragma unroll
     for (int r = 0; r < kPlanCtas; ++r) {
-        if (r < (int)blockIdx.x) before += *cluster.map_shared_rank(&part_holes, r);
+        if (r == (int)blockIdx.x) before = holes;
+        holes += *cluster.map_shared_rank(&part_holes, r);
         sum += *cluster.map_shared_rank(&part_movers, r);
+        holes_end[r] = holes;
         end[r] = sum;
     }
     for (int k = tid; k < nh; k += kPlanThreads) {
@@ -683,15 +685,19 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
         const int c = __ldg(a.table + e);
         a.table_out[e] = c >= 0 && c < a.P ? __ldcg(a.remap + c) : -1;
     }
-    // (the holes lie in the first parts: their copies are spread over all blocks)
-    if (t.n > 0) {
-        for (int r = 0; r < kPlanCtas; ++r) {
-            const int m = *cluster.map_shared_rank(&part_holes, r);
-            const int2 *list = cluster.map_shared_rank(moves, r);
-            copy_pairs(t, m, a.P, a.P, blockIdx.x * (kPlanThreads / 32) + warp, kPlanCtas * (kPlanThreads / 32),
-                       [&](int i) { return list[i]; });
-        }
-    }
+    // (the holes lie in the first parts: the copies are spread over all blocks)
+    if (t.n > 0)
+        copy_pairs(t, holes_end[kPlanCtas - 1], a.P, a.P, blockIdx.x * (kPlanThreads / 32) + warp,
+                   kPlanCtas * (kPlanThreads / 32), [&](int i) {
+            int r = 0, first = 0;
+#pragma unroll
+            for (int x = 0; x < kPlanCtas - 1; ++x)
+                if (i >= holes_end[x]) {
+                    r = x + 1;
+                    first = holes_end[x];
+                }
+            return cluster.map_shared_rank(moves, r)[i - first];
+        });
     cluster.sync();  // every block's lists are read before it exits
 }
 
