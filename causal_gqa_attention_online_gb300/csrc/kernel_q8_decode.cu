@@ -27,7 +27,8 @@
 // Bound: HBM, one byte an element -- at 8 flops a byte, twice the 16-bit
 // decode's arithmetic per byte, the conversions (4 to 5 instructions for four
 // codes) have to stay out of the way.  A CTA is four consumer warps of 32 keys
-// each and a producer warp: it looks pages up one tile ahead, issues one TMA
+// each and a producer warp: it looks pages up 32 boxes at a time and a group ahead
+// (one tile ahead it had a tile each table latency, 0.7 us), issues one TMA
 // box per page piece (up to 64 rows) and the block scales as 4-byte cp.async,
 // all completing on the stage's mbarrier; consumers free a stage with one
 // arrival a warp, so no warp waits for another within a tile.  Tiles that every
@@ -129,14 +130,18 @@ __device__ __forceinline__ UnitKeys unit_of(const Q8Args &a, int b) {
     return u;
 }
 
-// The first tile of share i of n <= T (so that no share is empty), and the share
-// of tile t.
-__device__ __forceinline__ long long share_begin(long long i, long long T, long long n) {
-    return i * T / n;
-}
-__device__ __forceinline__ long long share_at(long long t, long long T, long long n) {
-    return ((t + 1) * n - 1) / T;
-}
+// T tiles in n shares, 1 <= n <= T: the first T % n of them have a tile more.  (In
+// 32 bits, with one division: 64-bit ones in the prologue cost a CTA 0.3 us each.)
+struct Shares {
+    uint32_t q, r;
+    __host__ __device__ __forceinline__ Shares(uint32_t T, uint32_t n) : q(T / n), r(T - T / n * n) {}
+    // the first tile of share i, and the share of tile t
+    __host__ __device__ __forceinline__ uint32_t begin(uint32_t i) const { return i * q + (i < r ? i : r); }
+    __host__ __device__ __forceinline__ uint32_t of(uint32_t t) const {
+        const uint32_t head = r * (q + 1);
+        return t < head ? t / (q + 1) : r + (t - head) / q;
+    }
+};
 
 // Four columns of a joined row: acc / sum, and its LSE from the log2 sums' maximum
 // (a row without keys: +0 and -inf; one with a NaN key: NaN).
@@ -247,31 +252,35 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
         }
     }
     if (C == 0 && warp == 4) {
-        // this CTA's share of the tiles of all sequences, and where it begins
-        long long T = 0;
-        int n0 = 0;  // of the first 32 sequences
-        for (int b0 = 0; b0 < p.B; b0 += 32) {
-            const int n = b0 + lane < p.B ? unit_of(a, b0 + lane).ntiles : 0;
-            if (b0 == 0) n0 = n;
-            T += __reduce_add_sync(0xffffffffu, (unsigned)n);
+        // this CTA's share of the tiles of all sequences, and where it begins; the
+        // first 128 sequences' tiles stay in registers between the two passes
+        constexpr int CH = 4;
+        int n0[CH];
+        uint32_t T = 0;
+#pragma unroll
+        for (int k = 0; k < CH; ++k) n0[k] = 32 * k + lane < p.B ? unit_of(a, 32 * k + lane).ntiles : 0;
+#pragma unroll
+        for (int k = 0; k < CH; ++k) T += n0[k];
+        for (int b0 = 32 * CH; b0 < p.B; b0 += 32)
+            if (b0 + lane < p.B) T += unit_of(a, b0 + lane).ntiles;
+        T = __reduce_add_sync(0xffffffffu, T);
+        const uint32_t shares = min((uint32_t)a.shares, T);
+        const Shares sh(T, shares > 0 ? shares : 1);
+        uint32_t t0 = 0, left = 0;
+        if (share_i < (int)shares) {
+            t0 = sh.begin(share_i);
+            left = sh.begin(share_i + 1) - t0;
         }
-        const long long shares = min((long long)a.shares, T);
-        long long t0 = 0, left = 0;
-        if (share_i < shares) {
-            t0 = share_begin(share_i, T, shares);
-            left = share_begin(share_i + 1, T, shares) - t0;
-        }
-        long long before = 0;
+        uint32_t before = 0;
         bool found = left == 0;
-        for (int b0 = 0; !found && b0 < p.B; b0 += 32) {
-            const int n = b0 == 0 ? n0 : b0 + lane < p.B ? unit_of(a, b0 + lane).ntiles : 0;
+        auto look = [&](int b0, int n) {
             int incl = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, incl, o);
                 if (lane >= o) incl += y;
             }
-            const long long first = before + incl - n;
+            const uint32_t first = before + incl - n;
             const bool here = t0 >= first && t0 < first + n;
             if (here) {
                 share[1] = b0 + lane;
@@ -279,16 +288,20 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
                 if (kvh == 0) {
                     // where the sequence's first seam is this share's beginning
                     int4 v = make_int4(-1, 0, 0, 0);
-                    const int c0 = (int)share_at(first, T, shares);
+                    const int c0 = (int)sh.of(first);
                     if (t0 > first && c0 == share_i - 1)
-                        v = make_int4(b0 + lane, c0, (int)share_at(first + n - 1, T, shares),
-                                      share_begin(c0, T, shares) < first ? 1 : 0);
+                        v = make_int4(b0 + lane, c0, (int)sh.of(first + n - 1), sh.begin(c0) < first ? 1 : 0);
                     a.seam[share_i] = v;
                 }
             }
             found = __any_sync(0xffffffffu, here);
             before += __shfl_sync(0xffffffffu, incl, 31);
-        }
+        };
+#pragma unroll
+        for (int k = 0; k < CH; ++k)
+            if (!found && 32 * k < p.B) look(32 * k, n0[k]);
+        for (int b0 = 32 * CH; !found && b0 < p.B; b0 += 32)
+            look(b0, b0 + lane < p.B ? unit_of(a, b0 + lane).ntiles : 0);
         if (lane == 0) {
             share[0] = left;
             if (left == 0 && kvh == 0) a.seam[share_i] = make_int4(-1, 0, 0, 0);
@@ -317,8 +330,8 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
             if (rank == 0 && warp == 0) empty_rows(a, b, kvh, lane);
             return;
         }
-        tile = (int)share_begin(rank, un.ntiles, C);
-        left = (int)share_begin(rank + 1, un.ntiles, C) - tile;
+        tile = rank * un.ntiles / C;  // (some ranks have none where there are few)
+        left = (rank + 1) * un.ntiles / C - tile;
     } else {
         left = share[0];
         if (left == 0) return;
@@ -344,19 +357,27 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
         while (left > 0 && ok) {
             const int n = (int)min((long long)(un.ntiles - tile), left);
             const int32_t *table = p.block_table + (long long)b * p.max_pages;
-            auto page_of = [&](int t) -> int {  // lane i: the page of box i of tile t
-                const unsigned key = (unsigned)(un.kbeg + t * kTile) + ((unsigned)lane << a.box_shift);
+            // pages a warp's width of boxes at a time, one group ahead: lane i of
+            // group x has box 32 x + i, counted from the segment's first tile
+            const int tiles_a_group = 32 / nbox;
+            auto pages_of = [&](int x) -> int {
+                const long long key =
+                    (long long)un.kbeg + (long long)tile * kTile + ((long long)(32 * x + lane) << a.box_shift);
                 int pg = 0;
-                if (t < un.ntiles && lane < nbox && key < (unsigned)un.kend)
-                    pg = __ldg(table + (key >> p.page_shift));
+                if (key < un.kend) pg = __ldg(table + (key >> p.page_shift));
                 return min(max(pg, 0), p.num_pages - 1);
             };
-            int pg_next = page_of(tile);
+            int pg_group = pages_of(0), pg_next = pages_of(1);
             for (int t = tile; t < tile + n; ++t, ++it) {
                 const uint32_t s = it % NS;
                 const uint32_t fb = full + 8 * s, st = sbase + s * L::STAGE;
-                const int pg = pg_next;
-                pg_next = page_of(t + 1);
+                const int in_group = (t - tile) % tiles_a_group;
+                if (in_group == 0 && t > tile) {
+                    pg_group = pg_next;
+                    pg_next = pages_of((t - tile) / tiles_a_group + 1);
+                }
+                // lane i: the page of box i
+                const int pg = __shfl_sync(0xffffffffu, pg_group, (in_group * nbox + lane) & 31);
                 if (it >= (uint32_t)NS) {
                     const bool got = sm100::mbar_wait(empty + 8 * s, (it / NS - 1) & 1u, abort_flag, p.wait_ns);
                     if (!__all_sync(0xffffffffu, got)) {
@@ -502,13 +523,14 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
             const float *sc = reinterpret_cast<const float *>(smem + s * L::STAGE + 2 * L::TILE) + kw0;
 
             // S^T = K Q^T
-            float sacc[2][NT][4];
+            // (a row of products on one accumulator waits for each; two rows halve that)
+            float sacc[2][NT][4], sodd[2][NT][4];
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) sacc[mt][nt][j] = 0.f;
+                    for (int j = 0; j < 4; ++j) sacc[mt][nt][j] = sodd[mt][nt][j] = 0.f;
 #pragma unroll
             for (int kk = 0; kk < DP / 16; kk += 2) {
 #pragma unroll
@@ -522,10 +544,18 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
                         Op::k_pairs(r[2 * h + 1], f[1], f[3]);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
-                            MmaOp<__half>::run(sacc[mt][nt], f, qf[kk + h][nt][0], qf[kk + h][nt][1]);
+                            MmaOp<__half>::run(h ? sodd[mt][nt] : sacc[mt][nt], f, qf[kk + h][nt][0],
+                                               qf[kk + h][nt][1]);
                     }
                 }
             }
+
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) sacc[mt][nt][j] += sodd[mt][nt][j];
 
             // the largest finite value scale so far, of keys some row attends to
             const int uk = key0 + lane;
@@ -988,7 +1018,8 @@ bool q8_decode_supported(const AttnParams &p, int dtype) {
     // TMA copies rows of D bytes from 16-byte boundaries, and whole 8-row swizzle atoms
     if (p.D % 16 || p.Dv % 16 || p.D > 256 || p.Dv > 256 || p.page_size < 8) return false;
     if ((long long)p.Q * p.G > 16 || p.Q < 1) return false;
-    return p.Hkv <= 65535;  // CTAs and merge blocks are counted in 32 bits
+    // CTAs, merge blocks and tiles are counted in 32 bits
+    return p.Hkv <= 65535 && (long long)p.B * (((long long)p.K + kTile - 1) / kTile) < (1LL << 31);
 }
 
 unsigned long long q8_decode_workspace(const AttnParams &p, int nsm) {
