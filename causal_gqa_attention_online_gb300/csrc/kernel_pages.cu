@@ -194,6 +194,20 @@ __device__ __forceinline__ bool keeps(const ForkArgs &a, int i, int j, int c) {
            __ldcg(a.claim + c) == (unsigned long long)i * a.M + j;
 }
 
+// f(0), f(1), ... for the entries first, first + step, ... below end of an array,
+// four loads at a time.
+template <typename F>
+__device__ __forceinline__ void for_entries(const int32_t *v, long long first, long long end, long long step, F f) {
+    for (; first < end; first += 4 * step) {
+        int c[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) c[k] = first + k * step < end ? __ldg(v + first + k * step) : -1;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (first + k * step < end) f(first + k * step, c[k]);
+    }
+}
+
 // Four phases, each spread over the whole cluster; the dependent loads of a slot
 // (parent, length, entry, the entry's page) are what they cost, so a warp takes a
 // slot and every warp has as few as can be.  Slots and pages are dealt out in
@@ -225,27 +239,30 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
         part_wide = 0;
         part_need = 0;
     }
-    __threadfence();
+    const int per_s = (int)(((long long)a.N + kPlanCtas - 1) / kPlanCtas);
+    const int s0 = (int)min((long long)blockIdx.x * per_s, (long long)a.N), s1 = min(s0 + per_s, a.N);
+    Slot mine;  // the warp's first slot, kept over the phases
+    mine.parent = -1;
+    mine.len = mine.nfull = 0;
+    mine.want = 0;
+    if (s0 + warp < s1) mine = slot_of(a, s0 + warp);
+    auto slot = [&](int i) -> Slot { return i == s0 + warp ? mine : slot_of(a, i); };
+    // (a cluster barrier orders what the blocks write, in global memory too)
     cluster.sync();
     // 2. references by the old table; full entries and claims of the new one; free
     // pages of each part
-    for (long long e = gt; e < (long long)a.S * a.M; e += gn) {
-        const int c = __ldg(a.table + e);
+    for_entries(a.table, gt, (long long)a.S * a.M, gn, [&](long long, int c) {
         if (c >= 0 && c < a.P) atomicAdd(a.was + c, 1);
-    }
-    const int per_s = (int)(((long long)a.N + kPlanCtas - 1) / kPlanCtas);
-    const int s0 = (int)min((long long)blockIdx.x * per_s, (long long)a.N), s1 = min(s0 + per_s, a.N);
+    });
     for (int i = s0 + warp; i < s1; i += NW) {
-        const Slot s = slot_of(a, i);
+        const Slot s = slot(i);
         if (s.parent < 0) continue;
         if (lane == 0 && s.want > a.M) atomicAdd(&part_wide, 1);
-        const int last = (int)min(s.want, (long long)a.M);
-        for (int j = lane; j < last; j += 32) {
-            const int c = cand_of(a, s, j);
-            if (c < 0 || c >= a.P) continue;
+        for_entries(a.table + (long long)s.parent * a.M, lane, min(s.want, (long long)a.M), 32, [&](long long j, int c) {
+            if (c < 0 || c >= a.P) return;
             if (j < s.nfull) atomicAdd(a.full + c, 1);
             else atomicMin(a.claim + c, (unsigned long long)i * a.M + j);
-        }
+        });
     }
     const int per_p = (a.P + kPlanCtas - 1) / kPlanCtas;
     const int p0 = (int)min((long long)blockIdx.x * per_p, (long long)a.P);
@@ -254,11 +271,10 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     for (int p = p0 + tid; p < p1; p += kPlanThreads) nfree += __ldg(a.refs + p) == 0;
     nfree = __reduce_add_sync(0xffffffffu, nfree);
     if (lane == 0 && nfree) atomicAdd(&part_free, nfree);
-    __threadfence();
     cluster.sync();
     // 3. how many pages each slot takes; the free pages in ascending order
     for (int i = s0 + warp; i < s1; i += NW) {
-        const Slot s = slot_of(a, i);
+        const Slot s = slot(i);
         const int last = s.parent < 0 ? 0 : (int)min(s.want, (long long)a.M);
         int cnt = 0;
         for (int j = s.nfull + lane; j < last; j += 32) cnt += !keeps(a, i, j, cand_of(a, s, j));
@@ -269,6 +285,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
         }
     }
     int free_before = 0, all_free = 0, wide = 0;
+#pragma unroll
     for (int r = 0; r < kPlanCtas; ++r) {
         const int f = *cluster.map_shared_rank(&part_free, r);
         if (r < (int)blockIdx.x) free_before += f;
@@ -288,11 +305,11 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
             if ((f >> k) & 1u) a.list[at++] = (int)(p + k);
         free_before += tot;
     }
-    __threadfence();
     cluster.sync();
     // 4. entries that need a page take the free ones in the order of slots and
     // entries, when there are enough
     unsigned long long before = 0, total = 0;
+#pragma unroll
     for (int r = 0; r < kPlanCtas; ++r) {
         const unsigned long long x = *cluster.map_shared_rank(&part_need, r);
         if (r < (int)blockIdx.x) before += x;
@@ -314,7 +331,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
             s.parent = -1;
             s.nfull = s.len = 0;
             s.want = 0;
-            if (i < s1) s = slot_of(a, i);
+            if (i < s1) s = slot(i);
             const int last = s.parent < 0 ? 0 : (int)min(s.want, (long long)a.M);
             int tot;
             int at = block_scan(lane == 0 && i < s1 ? __ldcg(a.need + i) : 0, warps, &tot);
@@ -440,29 +457,32 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
         nf += tot;
     }
     if (tid == 0) part_free = nf;
+    Slot mine;  // the warp's first slot, kept over the phases
+    mine.parent = -1;
+    mine.len = mine.nfull = 0;
+    mine.want = 0;
+    if (s0 + warp < s1) mine = slot_of(a, s0 + warp);
+    auto slot = [&](int i) -> Slot { return i == s0 + warp ? mine : slot_of(a, i); };
     cluster.sync();
     // 2. references by the old table; full entries and claims of the new one
-    for (long long e = gt; e < (long long)a.S * a.M; e += gn) {
-        const int c = __ldg(a.table + e);
+    for_entries(a.table, gt, (long long)a.S * a.M, gn, [&](long long, int c) {
         if (c >= 0 && c < a.P) atomicAdd(of(was, c), 1);
-    }
+    });
     for (int i = s0 + warp; i < s1; i += NW) {
-        const Slot s = slot_of(a, i);
+        const Slot s = slot(i);
         if (lane == 0) a.lens_out[i] = s.len;
         if (s.parent < 0) continue;
         if (lane == 0 && s.want > a.M) atomicAdd(&part_wide, 1);
-        const int last = (int)min(s.want, (long long)a.M);
-        for (int j = lane; j < last; j += 32) {
-            const int c = cand_of(a, s, j);
-            if (c < 0 || c >= a.P) continue;
+        for_entries(a.table + (long long)s.parent * a.M, lane, min(s.want, (long long)a.M), 32, [&](long long j, int c) {
+            if (c < 0 || c >= a.P) return;
             if (j < s.nfull) atomicAdd(of(full, c), 1);
-            else atomicMin(of(claim, c), (unsigned)(i * a.M + j));
-        }
+            else atomicMin(of(claim, c), (unsigned)(i * a.M + (int)j));
+        });
     }
     cluster.sync();
     // 3. how many pages each slot takes
     for (int i = s0 + warp; i < s1; i += NW) {
-        const Slot s = slot_of(a, i);
+        const Slot s = slot(i);
         const int last = s.parent < 0 ? 0 : (int)min(s.want, (long long)a.M);
         int cnt = 0;
         for (int j = s.nfull + lane; j < last; j += 32) cnt += !keep(i, j, cand_of(a, s, j));
@@ -509,7 +529,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
         s.parent = -1;
         s.nfull = s.len = 0;
         s.want = 0;
-        if (i < s1 && fine) s = slot_of(a, i);
+        if (i < s1 && fine) s = slot(i);
         const int last = s.parent < 0 ? 0 : (int)min(s.want, (long long)a.M);
         int tot;
         int at = block_scan(lane == 0 && i < s1 ? need[i - s0] : 0, warps, &tot);
@@ -539,6 +559,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     }
     if (gt == 0) {
         int copies = 0;
+#pragma unroll
         for (int r = 0; r < kPlanCtas; ++r) copies += *cluster.map_shared_rank(&part_copies, r);
         a.status[3] = copies;
     }
@@ -572,6 +593,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     if (threadIdx.x == 0) mine = tot;
     cluster.sync();
     int before = 0, n = 0;
+#pragma unroll
     for (int r = 0; r < kPlanCtas; ++r) {
         const int c = *cluster.map_shared_rank(&mine, r);
         if (r < (int)blockIdx.x) before += c;
@@ -602,7 +624,6 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
         *a.n_live = n;
         if (n == a.P) a.count[0] = 0;  // no hole
     }
-    __threadfence();
     cluster.sync();  // (also: every block has read `mine` before any leaves)
     const int moves = __ldcg(a.count);
     for (int k = blockIdx.x * kPlanThreads + threadIdx.x; k < moves; k += kPlanCtas * kPlanThreads) {
@@ -633,6 +654,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     if (tid == 0) part_live = tot;
     cluster.sync();
     int n = 0;
+#pragma unroll
     for (int r = 0; r < kPlanCtas; ++r) n += *cluster.map_shared_rank(&part_live, r);
     int nm = 0, nh = 0;
     for (int q = p0; q < p1; q += kPlanThreads) {
@@ -679,7 +701,6 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
         a.remap[p] = d;
         a.refs_out[d] = __ldg(a.refs + p);
     }
-    __threadfence();
     cluster.sync();
     for (long long e = blockIdx.x * kPlanThreads + tid; e < (long long)a.S * a.M; e += kPlanCtas * kPlanThreads) {
         const int c = __ldg(a.table + e);
