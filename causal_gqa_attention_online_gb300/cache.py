@@ -24,6 +24,7 @@ from __future__ import annotations
 
 import array
 import math
+import operator
 
 import torch
 
@@ -38,6 +39,11 @@ _CACHE_CODE = {torch.float8_e4m3fn: ATTN_CACHE_E4M3, torch.int8: ATTN_CACHE_INT8
 # without their objects and checks (0.2 us against 4 a call).
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
+
+
+# Checks of many tensors go through these (half the time of a loop's method calls).
+_is_contiguous, _get_device = torch.Tensor.is_contiguous, torch.Tensor.get_device
+_data_ptr, _nbytes = torch.Tensor.data_ptr, operator.attrgetter("nbytes")
 
 
 def _here(i, stream):
@@ -83,19 +89,28 @@ def _cache(k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, i):
     if k_pages.dim() != 4 or v_pages.dim() != 4 or k_scale.dim() != 3 or block_table.dim() != 2:
         raise ValueError("pages are [P, page, Hkv, D], scales [P, page / block, Hkv] and the "
                          "block table [B, max_pages]")
-    P, page, Hkv, D = k_pages.shape
-    Dv, nblk = v_pages.shape[3], k_scale.shape[1]
+    pages, scales = k_pages.shape, k_scale.shape
+    P, page, Hkv, D = pages
+    Dv, nblk = v_pages.size(3), scales[1]
     B, M = block_table.shape
     if nblk < 1 or page % nblk:
         raise ValueError(f"k_scale: {nblk} blocks do not divide a page of {page} tokens")
-    scales = (P, nblk, Hkv)
-    ptrs = (_tensor("k_pages", k_pages, k_pages.dtype, (P, page, Hkv, D), i),
-            _tensor("v_pages", v_pages, k_pages.dtype, (P, page, Hkv, Dv), i),
-            _tensor("k_scale", k_scale, torch.float32, scales, i),
-            _tensor("v_scale", v_scale, torch.float32, scales, i),
-            _tensor("block_table", block_table, torch.int32, (B, M), i),
-            _tensor("seqlens_k", seqlens_k, torch.int32, (B,), i))
-    return ptrs, (P, page, page // nblk, Hkv, D, Dv, B, M), code
+    tensors = (k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k)
+    if not (all(map(_is_contiguous, tensors)) and all(map(i.__eq__, map(_get_device, tensors))) and
+            v_pages.dtype is k_pages.dtype and k_scale.dtype is torch.float32 and
+            v_scale.dtype is torch.float32 and block_table.dtype is torch.int32 and
+            seqlens_k.dtype is torch.int32 and (Dv == D or v_pages.shape[:3] == pages[:3]) and
+            (Dv != D or v_pages.shape == pages) and scales == (P, nblk, Hkv) and
+            v_scale.shape == scales and seqlens_k.shape == (B,)):
+        for name, t, dtype, shape in (
+                ("k_pages", k_pages, k_pages.dtype, (P, page, Hkv, D)),
+                ("v_pages", v_pages, k_pages.dtype, (P, page, Hkv, Dv)),
+                ("k_scale", k_scale, torch.float32, (P, nblk, Hkv)),
+                ("v_scale", v_scale, torch.float32, (P, nblk, Hkv)),
+                ("block_table", block_table, torch.int32, (B, M)),
+                ("seqlens_k", seqlens_k, torch.int32, (B,))):
+            _tensor(name, t, dtype, shape, i)
+    return map(_data_ptr, tensors), (P, page, page // nblk, Hkv, D, Dv, B, M), code
 
 
 def attn_cache_append(k, v, k_pages, v_pages, k_scale, v_scale, block_table, seqlens_k, *,
@@ -192,17 +207,20 @@ def attn_fwd_paged_q8(q, k_pages, v_pages, k_scale, v_scale, block_table, seqlen
 def _pool_arrays(pools, pages, i, what):
     """Pointers and page bytes of pools (of device ``i``) whose first axis counts
     ``pages`` pages, as 64-bit arrays."""
-    ptrs, sizes = array.array("Q"), array.array("q")
-    for k, t in enumerate(pools):
-        if t.dim() < 1 or t.size(0) != pages:
-            raise ValueError(f"{what}[{k}]: shape {tuple(t.shape)}, expected {pages} pages first")
-        if not t.is_contiguous():
-            raise ValueError(f"{what}[{k}] must be contiguous")
-        if t.get_device() != i:
-            raise ValueError(f"{what}[{k}] is on {t.device}, unlike the tables")
-        ptrs.append(t.data_ptr())
-        sizes.append(t.nbytes // pages if pages else 0)
-    return ptrs, sizes
+    if not (all(map(_is_contiguous, pools)) and all(map(i.__eq__, map(_get_device, pools))) and
+            all(map((pages,).__eq__, [t.shape[:1] for t in pools]))):
+        for k, t in enumerate(pools):
+            if t.dim() < 1 or t.shape[0] != pages:
+                raise ValueError(f"{what}[{k}]: shape {tuple(t.shape)}, expected {pages} pages "
+                                 "first")
+            if not t.is_contiguous():
+                raise ValueError(f"{what}[{k}] must be contiguous")
+            if t.get_device() != i:
+                raise ValueError(f"{what}[{k}] is on {t.device}, unlike the tables")
+    sizes = array.array("q", map(_nbytes, pools))
+    if pages > 1:
+        sizes = array.array("q", [x // pages for x in sizes])
+    return array.array("Q", map(_data_ptr, pools)), sizes
 
 
 def _at(a):
