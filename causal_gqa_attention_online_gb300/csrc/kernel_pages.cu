@@ -6,9 +6,11 @@
 // version as it was, and every call can be captured into a graph.  The integer
 // work is latency bound (a few thousand entries); it runs as one cluster of
 // kPlanCtas blocks that meet at cluster barriers, so a plan is one launch
-// whatever its phases, and the copies and the table follow in a second one.
-// Where few bytes can move (kSmallBytes), and the pages' counts fit the cluster's
-// shared memory, the cluster does all of it: one launch and no workspace.
+// whatever its phases.  Per-page counts live in the cluster's shared memory where
+// they fit (80 thousand pages), and there is no workspace then; where few bytes
+// can move (kSmallBytes) the cluster copies them itself, otherwise a second launch
+// does, which finds the pairs in the new version.  Larger pools keep the counts in
+// a workspace, and the table follows in the second launch, too.
 // Page numbers are handed out lowest first and the results do not depend on
 // the order of any atomic: counts and minima only.
 //
@@ -58,6 +60,21 @@ template <typename V> __device__ __forceinline__ void copy_units(uint8_t *dst, c
     }
 }
 
+// Chunk r of a page's (over all pools): page sp -> dp, by a warp.
+__device__ __forceinline__ void copy_chunk(const PoolTable &t, int sp, int dp, int r) {
+    int pool = 0;
+    while (r >= t.first_chunk[pool + 1]) ++pool;
+    const long long off = (long long)(r - t.first_chunk[pool]) * kChunk;
+    const long long bytes = t.bytes[pool];
+    const int len = (int)min((long long)kChunk, bytes - off), lane = threadIdx.x & 31;
+    const uint8_t *s = t.src[pool] + sp * bytes + off;
+    uint8_t *d = t.dst[pool] + dp * bytes + off;
+    const uintptr_t low = reinterpret_cast<uintptr_t>(s) | reinterpret_cast<uintptr_t>(d) | (uintptr_t)len;
+    if ((low & 15) == 0) copy_units<uint4>(d, s, len / 16, lane);
+    else if ((low & 3) == 0) copy_units<uint32_t>(d, s, len / 4, lane);
+    else copy_units<uint8_t>(d, s, len, lane);
+}
+
 // Pages pair(i).x -> pair(i).y of every pool for i < n, by warp `first`, first +
 // step, ....  Pairs outside the pools are skipped.
 template <typename F>
@@ -65,23 +82,13 @@ __device__ __forceinline__ void copy_pairs(const PoolTable &t, int n, int src_pa
                                            long long first, long long step, F pair) {
     const int per_page = t.first_chunk[t.n];
     const long long total = (long long)n * per_page;
-    const int lane = threadIdx.x & 31;
+    int2 next = first < total ? pair((int)(first / per_page)) : make_int2(-1, -1);
     for (long long c = first; c < total; c += step) {
         const int i = (int)(c / per_page), r = (int)(c - (long long)i * per_page);
-        const int2 sd = pair(i);
-        const int sp = sd.x, dp = sd.y;
+        const int sp = next.x, dp = next.y;
+        if (c + step < total) next = pair((int)((c + step) / per_page));  // under way during the copy
         if (sp < 0 || sp >= src_pages || dp < 0 || dp >= dst_pages) continue;
-        int pool = 0;
-        while (r >= t.first_chunk[pool + 1]) ++pool;
-        const long long off = (long long)(r - t.first_chunk[pool]) * kChunk;
-        const long long bytes = t.bytes[pool];
-        const int len = (int)min((long long)kChunk, bytes - off);
-        const uint8_t *s = t.src[pool] + sp * bytes + off;
-        uint8_t *d = t.dst[pool] + dp * bytes + off;
-        const uintptr_t low = reinterpret_cast<uintptr_t>(s) | reinterpret_cast<uintptr_t>(d) | (uintptr_t)len;
-        if ((low & 15) == 0) copy_units<uint4>(d, s, len / 16, lane);
-        else if ((low & 3) == 0) copy_units<uint32_t>(d, s, len / 4, lane);
-        else copy_units<uint8_t>(d, s, len, lane);
+        copy_chunk(t, sp, dp, r);
     }
 }
 
@@ -112,9 +119,9 @@ __global__ void __launch_bounds__(kCopyThreads)
 
 // --------------------------------------------------------------- block scans
 
-// Exclusive sum of v over the block's threads; *total gets the block's sum.
+// Exclusive sum of v over the block's NW warps; *total gets the block's sum.
 // `warps`: 32 ints of shared memory.
-__device__ __forceinline__ int block_scan(int v, int *warps, int *total) {
+template <int NW = 32> __device__ __forceinline__ int block_scan(int v, int *warps, int *total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int incl = v;
 #pragma unroll
@@ -126,7 +133,7 @@ __device__ __forceinline__ int block_scan(int v, int *warps, int *total) {
     if (lane == 31) warps[warp] = incl;
     __syncthreads();
     if (warp == 0) {
-        int w = warps[lane];
+        int w = lane < NW ? warps[lane] : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, w, o);
@@ -433,6 +440,8 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
         return refs > 0 && *of(full, c) == 0 && refs <= *of(was, c) &&
                *of(claim, c) == (unsigned)(i * a.M + j);
     };
+    // the copy grid (a programmatic dependent launch) may be scheduled now
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     const int p0 = min(blockIdx.x << sf.part_shift, (unsigned)a.P), p1 = min(p0 + per_p, a.P);
     const int s0 = min((int)blockIdx.x * per_s, a.N), s1 = min(s0 + per_s, a.N);
     // 1. clear; the free pages of the part, in ascending order
@@ -567,6 +576,39 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     cluster.sync();  // every block's sums are read before it exits
 }
 
+// The copies of a fork whose plan kept no list: slot i's partly filled page, where
+// its entry is not its parent's.  Every block lists the pairs (kSlotsMax at most),
+// in slot order, in shared memory first.
+constexpr int kSlotsMax = 2048;
+
+__global__ void __launch_bounds__(kCopyThreads)
+    fork_copy_kernel(const __grid_constant__ ForkArgs a, const __grid_constant__ PoolTable t) {
+    __shared__ int2 moves[kSlotsMax];
+    __shared__ int warps[32];
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    if (__ldcg(a.status + 3) == 0) return;  // (0 as well where the call did not fit)
+    int count = 0;
+    for (int i0 = 0; i0 < a.N; i0 += kCopyThreads) {
+        const int i = i0 + threadIdx.x;
+        int2 m = make_int2(-1, -1);
+        if (i < a.N) {
+            const Slot s = slot_of(a, i);
+            if (s.parent >= 0 && s.nfull < a.M && (s.len & ((1 << a.page_shift) - 1)) != 0) {
+                const int c = cand_of(a, s, s.nfull), d = __ldcg(a.table_out + (long long)i * a.M + s.nfull);
+                if (c >= 0 && c < a.P && c != d) m = make_int2(c, d);
+            }
+        }
+        int tot;
+        const int at = count + block_scan<kCopyThreads / 32>(m.x >= 0, warps, &tot);
+        if (m.x >= 0) moves[at] = m;
+        count += tot;
+    }
+    __syncthreads();
+    constexpr int W = kCopyThreads / 32;
+    copy_pairs(t, count, a.P, a.P, (long long)blockIdx.x * W + (threadIdx.x >> 5), (long long)gridDim.x * W,
+               [&](int i) { return moves[i]; });
+}
+
 // ------------------------------------------------------------------ compact
 
 struct CompactArgs {
@@ -645,6 +687,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     const int tid = threadIdx.x, warp = tid >> 5;
     const int per = (a.P + kPlanCtas - 1) / kPlanCtas;
     const int p0 = min((int)blockIdx.x * per, a.P), p1 = min(p0 + per, a.P);
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     int2 *moves = reinterpret_cast<int2 *>(dyn);       // [per] {page, hole}: the holes of this part
     int *movers = reinterpret_cast<int *>(moves + per);  // [per]
     int cnt = 0;
@@ -720,6 +763,16 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
             return cluster.map_shared_rank(moves, r)[i - first];
         });
     cluster.sync();  // every block's lists are read before it exits
+}
+
+// The copies of a compaction whose plan kept no list: page p at or behind the live
+// count goes to remap[p].
+__global__ void __launch_bounds__(kCopyThreads)
+    compact_copy_kernel(const __grid_constant__ CompactArgs a, const __grid_constant__ PoolTable t) {
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    const int n = __ldcg(a.n_live), warps = kCopyThreads / 32;
+    copy_pairs(t, a.P - n, a.P, a.P, (long long)blockIdx.x * warps + (threadIdx.x >> 5), (long long)gridDim.x * warps,
+               [&](int i) { return make_int2(n + i, __ldcg(a.remap + n + i)); });
 }
 
 __global__ void __launch_bounds__(kCopyThreads)
@@ -854,14 +907,26 @@ size_t compact_small_shared(int P) { return (size_t)((P + kPlanCtas - 1) / kPlan
 
 constexpr long long kSmallEntries = 1 << 17;  // of a table
 
-bool fork_is_small(const long long *bytes, int npools, int N, int M, int P) {
-    return (long long)N * M <= kSmallEntries && npools <= kMaxPools && N <= (1 << 20) && P <= (1 << 20) &&
-           fork_small_shared(N, P) <= kSmallShared && (double)N * page_total(bytes, npools) <= kSmallBytes;
+// Bytes from which on a plan with lists in a workspace is worth its allocation (4 us
+// of host time): a copy launch that looks the pairs up is some 5% slower.
+constexpr double kListBytes = 64.0 * (1 << 20);
+
+// Whether a plan goes without a workspace: its counts fit the cluster's shared
+// memory, its table is not so large that a whole grid has to write it, and not
+// much can move; and whether the cluster copies as well.
+bool fork_fits(const long long *bytes, int npools, int N, int M, int P) {
+    return (long long)N * M <= kSmallEntries && N <= kSlotsMax && P <= (1 << 20) &&
+           fork_small_shared(N, P) <= kSmallShared && (double)N * page_total(bytes, npools) <= kListBytes;
 }
-// (at most half of the pages move)
-bool compact_is_small(const long long *bytes, int npools, int S, int M, int P) {
-    return (long long)S * M <= kSmallEntries && npools <= kMaxPools && P <= (1 << 20) && compact_small_shared(P) <= kSmallShared &&
-           0.5 * P * page_total(bytes, npools) <= kSmallBytes;
+bool fork_copies(const long long *bytes, int npools, int N) {
+    return npools <= kMaxPools && (double)N * page_total(bytes, npools) <= kSmallBytes;
+}
+bool compact_fits(const long long *bytes, int npools, int S, int M, int P) {
+    return (long long)S * M <= kSmallEntries && P <= (1 << 20) && compact_small_shared(P) <= kSmallShared &&
+           0.5 * P * page_total(bytes, npools) <= kListBytes;
+}
+bool compact_copies(const long long *bytes, int npools, int P) {  // (at most half of the pages move)
+    return npools <= kMaxPools && 0.5 * P * page_total(bytes, npools) <= kSmallBytes;
 }
 
 }  // namespace
@@ -879,8 +944,7 @@ int launch_pages_copy(const void *const *src_pools, void *const *dst_pools, cons
 }
 
 unsigned long long pages_fork_workspace(const long long *bytes, int npools, int N, int M, int P) {
-    if (fork_is_small(bytes, npools, N, M, P)) return 0;
-    return 8ull * P + 4ull * (4ull * P + 3ull * N + 1ull);
+    return fork_fits(bytes, npools, N, M, P) ? 0 : 8ull * P + 4ull * (4ull * P + 3ull * N + 1ull);
 }
 
 int launch_pages_fork(void *const *pools, const long long *bytes, int npools,
@@ -903,12 +967,23 @@ int launch_pages_fork(void *const *pools, const long long *bytes, int npools,
     a.lens_out = seqlens_out;
     a.refs_out = refcount_out;
     a.status = status;
-    if (fork_is_small(bytes, npools, N, M, P)) {
-        PoolTable t;
-        const int rc = fill_pools(t, pools, pools, bytes, npools);
-        if (rc) return rc;
-        return launch_small(fork_small_kernel, SmallFork{a, fork_part_shift(P)}, t, fork_small_shared(N, P),
-                            "page fork kernel", stream);
+    if (fork_fits(bytes, npools, N, M, P)) {
+        PoolTable none;
+        none.n = 0;
+        none.first_chunk[0] = 0;
+        const bool all = fork_copies(bytes, npools, N);
+        int rc = 0;
+        if (all) rc = fill_pools(none, pools, pools, bytes, npools);
+        if (rc == 0)
+            rc = launch_small(fork_small_kernel, SmallFork{a, fork_part_shift(P)}, none, fork_small_shared(N, P),
+                              "page fork kernel", stream);
+        if (rc || all) return rc;
+        return for_pool_groups(pools, pools, bytes, npools, [&](const PoolTable &t, bool first) {
+            const unsigned blocks = grid_for((long long)N * t.first_chunk[t.n], 0);
+            if (first) return launch_finish(fork_copy_kernel, blocks, a, t, "page copy kernel", stream);
+            fork_copy_kernel<<<blocks, kCopyThreads, 0, stream>>>(a, t);
+            return launched("page copy kernel");
+        });
     }
     a.claim = static_cast<unsigned long long *>(ws);
     a.was = reinterpret_cast<int32_t *>(a.claim + P);
@@ -934,7 +1009,7 @@ int launch_pages_fork(void *const *pools, const long long *bytes, int npools,
 }
 
 unsigned long long pages_compact_workspace(const long long *bytes, int npools, int S, int M, int P) {
-    return compact_is_small(bytes, npools, S, M, P) ? 0 : 4ull * (2ull * P + 1ull);
+    return compact_fits(bytes, npools, S, M, P) ? 0 : 4ull * (2ull * P + 1ull);
 }
 
 int launch_pages_compact(void *const *pools, const long long *bytes, int npools,
@@ -951,11 +1026,22 @@ int launch_pages_compact(void *const *pools, const long long *bytes, int npools,
     a.refs_out = refcount_out;
     a.remap = remap;
     a.n_live = n_live;
-    if (compact_is_small(bytes, npools, S, M, P)) {
-        PoolTable t;
-        const int rc = fill_pools(t, pools, pools, bytes, npools);
-        if (rc) return rc;
-        return launch_small(compact_small_kernel, a, t, compact_small_shared(P), "page compact kernel", stream);
+    if (compact_fits(bytes, npools, S, M, P)) {
+        PoolTable none;
+        none.n = 0;
+        none.first_chunk[0] = 0;
+        const bool all = compact_copies(bytes, npools, P);
+        int rc = 0;
+        if (all) rc = fill_pools(none, pools, pools, bytes, npools);
+        if (rc == 0)
+            rc = launch_small(compact_small_kernel, a, none, compact_small_shared(P), "page compact kernel", stream);
+        if (rc || all) return rc;
+        return for_pool_groups(pools, pools, bytes, npools, [&](const PoolTable &t, bool first) {
+            const unsigned blocks = grid_for((long long)(P / 2) * t.first_chunk[t.n], 0);
+            if (first) return launch_finish(compact_copy_kernel, blocks, a, t, "page copy kernel", stream);
+            compact_copy_kernel<<<blocks, kCopyThreads, 0, stream>>>(a, t);
+            return launched("page copy kernel");
+        });
     }
     a.src = static_cast<int32_t *>(ws);
     a.dst = a.src + P;

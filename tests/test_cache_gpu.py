@@ -499,12 +499,12 @@ def check_fork(g, table, lens, refs, parents, new, page, shapes=(160, 5000)):
     return ref
 
 
-# pages of a few bytes (one cluster does everything), and of so many that the copies
-# take a launch of their own
-BIG = (1 << 18, 5000)
+# pages of a few bytes (one cluster does everything), of so many that the copies take
+# a launch of their own, and of so many more that the plan keeps lists
+BIG, HUGE = (1 << 18, 5000), (1 << 20, 1 << 20, 5000)
 
 
-@pytest.mark.parametrize("shapes", [(160, 5000), BIG, ()])
+@pytest.mark.parametrize("shapes", [(160, 5000), BIG, HUGE, ()])
 @pytest.mark.parametrize("seed", range(12))
 def test_fork(seed, shapes):
     g = np.random.default_rng(300 + seed)
@@ -513,8 +513,8 @@ def test_fork(seed, shapes):
     N = int(g.integers(1, 50))
     parents = g.integers(-1, S + 1, N)
     new = np.minimum(g.integers(-2, 3 * page, N), M * page // 2)
-    if shapes == BIG and len(refs) * sum(shapes) > 1 << 28:
-        shapes = (1 << 28) // len(refs) // 16 * 16, 48
+    if len(refs) * sum(shapes) > 1 << 30:
+        shapes = (1 << 30) // len(refs) // 16 * 16, 48
     check_fork(g, table, lens, refs, parents, None if seed % 4 == 0 else new, page, shapes)
 
 
@@ -524,6 +524,27 @@ def test_fork_of_many_slots_and_wide_growth():
     ref = check_fork(g, table, lens, refs, g.integers(0, 300, 1100), g.integers(0, 64, 1100), 16,
                      shapes=(64,))
     assert ref[3][0] == 0 and ref[3][3] > 300
+
+
+@pytest.mark.parametrize("room", [True, False])
+def test_fork_in_a_pool_of_very_many_pages(room):
+    """200 thousand pages: the counts are kept in a workspace."""
+    g = np.random.default_rng(37)
+    table, lens, refs = random_table(g, 40, 60, 8, 200003, pins=5)
+    if not room:
+        refs[refs == 0] = 1
+    parents = g.integers(-1, 40, 70)
+    check_fork(g, table, lens, refs, parents, g.integers(0, 30, 70), 8, shapes=(48, 1000))
+
+
+def test_fork_of_a_wide_table():
+    """More entries than one cluster writes, and more slots than a block lists."""
+    g = np.random.default_rng(38)
+    table, lens, refs = random_table(g, 20, 30, 8, 9000, pins=5)
+    wide = np.full((20, 700), -1, np.int32)
+    wide[:, :30] = table
+    check_fork(g, wide, lens, refs, g.integers(0, 20, 300), np.ones(300, int), 8, shapes=(64,))
+    check_fork(g, table, lens, refs, g.integers(-1, 20, 4200), np.ones(4200, int), 8, shapes=(64,))
 
 
 @pytest.mark.parametrize("shapes", [(160, 5000), BIG])
@@ -574,16 +595,18 @@ def test_fork_without_slots_frees_everything():
     assert (ref[2] == 0).all()
 
 
-@pytest.mark.parametrize("P", [1, 2, 31, 1024, 5000, 40001])
+@pytest.mark.parametrize("P", [1, 2, 31, 1024, 5000, 40001, 200003])
 @pytest.mark.parametrize("share", [0.0, 0.1, 0.5, 0.95, 1.0])
-@pytest.mark.parametrize("big", [False, True])
-def test_compact(P, share, big):
+@pytest.mark.parametrize("total", [81, 1 << 25, 1 << 28])
+def test_compact(P, share, total):
+    """Pools of 81 bytes a page (one cluster does everything), of 32 MB (a copy
+    launch) and of 256 MB (lists in a workspace)."""
     g = np.random.default_rng(P + int(100 * share))
-    if big and P < 1024:
-        pytest.skip("the same path as without")
+    if total > 81 and not 1024 <= P <= 40001:
+        pytest.skip("the same path as with small pages")
     refs = np.where(g.random(P) < share, g.integers(1, 4, P), 0).astype(np.int32)
     table = g.integers(-3, P + 3, (9, 33)).astype(np.int32)
-    pools = random_pools(g, P, ((1 << 25) // P // 16 * 16, 33) if big else (48, 33))
+    pools = random_pools(g, P, (total // P // 16 * 16, 33) if total > 81 else (48, 33))
     want = [p.cpu().numpy().copy() for p in pools]
     out = attn.attn_pages_compact(pools, i32(table), i32(refs))
     ref = cache_ref.compact(table, refs)
