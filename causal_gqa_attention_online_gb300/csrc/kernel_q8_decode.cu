@@ -309,13 +309,14 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
     } else if (C == 0) {
         // meanwhile: the rows of sequences without keys, +0 and -inf (each lane
         // looks at one of the CTA's sequences and heads, the warp writes)
-        const long long units = (long long)p.B * p.Hkv;
-        for (long long x0 = blockIdx.x + (long long)warp * 32 * gridDim.x; x0 < units; x0 += 128LL * gridDim.x) {
-            const long long x = x0 + (long long)lane * gridDim.x;
-            unsigned todo = __ballot_sync(0xffffffffu, x < units && unit_of(a, (int)(x / p.Hkv)).ntiles == 0);
+        const uint32_t units = (uint32_t)p.B * p.Hkv, step = gridDim.x;
+        for (uint64_t x0 = blockIdx.x + (uint64_t)warp * 32 * step; x0 < units; x0 += 128ull * step) {
+            const uint64_t x = x0 + (uint64_t)lane * step;
+            const uint32_t b = x < units ? (uint32_t)x / (uint32_t)p.Hkv : 0u;
+            unsigned todo = __ballot_sync(0xffffffffu, x < units && unit_of(a, b).ntiles == 0);
             for (; todo; todo &= todo - 1) {
-                const long long y = x0 + (long long)(__ffs(todo) - 1) * gridDim.x;
-                empty_rows(a, (int)(y / p.Hkv), (int)(y % p.Hkv), lane);
+                const uint32_t y = (uint32_t)x0 + (__ffs(todo) - 1) * step;
+                empty_rows(a, y / (uint32_t)p.Hkv, y % (uint32_t)p.Hkv, lane);
             }
         }
     }
@@ -1019,7 +1020,7 @@ bool q8_decode_supported(const AttnParams &p, int dtype) {
     if (p.D % 16 || p.Dv % 16 || p.D > 256 || p.Dv > 256 || p.page_size < 8) return false;
     if ((long long)p.Q * p.G > 16 || p.Q < 1) return false;
     // CTAs, merge blocks and tiles are counted in 32 bits
-    return p.Hkv <= 65535 && (long long)p.B * (((long long)p.K + kTile - 1) / kTile) < (1LL << 31);
+    return p.Hkv <= 65535 && (long long)p.B * p.Hkv < (1LL << 31) && (long long)p.B * (((long long)p.K + kTile - 1) / kTile) < (1LL << 31);
 }
 
 unsigned long long q8_decode_workspace(const AttnParams &p, int nsm) {
