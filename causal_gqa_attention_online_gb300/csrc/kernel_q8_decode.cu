@@ -524,14 +524,13 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
             const float *sc = reinterpret_cast<const float *>(smem + s * L::STAGE + 2 * L::TILE) + kw0;
 
             // S^T = K Q^T
-            // (a row of products on one accumulator waits for each; two rows halve that)
-            float sacc[2][NT][4], sodd[2][NT][4];
+            float sacc[2][NT][4];
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) sacc[mt][nt][j] = sodd[mt][nt][j] = 0.f;
+                    for (int j = 0; j < 4; ++j) sacc[mt][nt][j] = 0.f;
 #pragma unroll
             for (int kk = 0; kk < DP / 16; kk += 2) {
 #pragma unroll
@@ -545,18 +544,10 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
                         Op::k_pairs(r[2 * h + 1], f[1], f[3]);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
-                            MmaOp<__half>::run(h ? sodd[mt][nt] : sacc[mt][nt], f, qf[kk + h][nt][0],
-                                               qf[kk + h][nt][1]);
+                            MmaOp<__half>::run(sacc[mt][nt], f, qf[kk + h][nt][0], qf[kk + h][nt][1]);
                     }
                 }
             }
-
-#pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) sacc[mt][nt][j] += sodd[mt][nt][j];
 
             // the largest finite value scale so far, of keys some row attends to
             const int uk = key0 + lane;
@@ -825,11 +816,25 @@ __global__ void __launch_bounds__(kMergeThreads) q8_merge_kernel(const __grid_co
     const AttnParams &p = a.p;
     const int nrows = p.Q * p.G, per_share = p.Hkv * nrows;
     const int x = blockIdx.x / per_share, y = blockIdx.x - x * per_share;
+    const int seams = gridDim.x / per_share;
     const int kvh = y / nrows, row = y - kvh * nrows;
     const int tid = threadIdx.x;
     // launched as a programmatic dependent of the decode kernel
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    const int4 seam = __ldcg(a.seam + x + 1);
+    // the x-th seam: of share x + 1 where there can be one at each, else (fewer
+    // sequences than shares) by a search
+    int at_share = x + 1;
+    if (seams < a.shares - 1) {
+        at_share = 0;
+        for (int s0 = 1, seen = 0; s0 < a.shares && at_share == 0; s0 += 32) {
+            const int i = s0 + (tid & 31);
+            const unsigned m = __ballot_sync(0xffffffffu, i < a.shares && __ldcg(&a.seam[i].x) >= 0);
+            if (x < seen + __popc(m)) at_share = s0 + __fns(m, 0, x - seen + 1);
+            seen += __popc(m);
+        }
+        if (at_share == 0) return;
+    }
+    const int4 seam = __ldcg(a.seam + at_share);
     if (seam.x < 0) return;
     const int np = seam.z - seam.y + 1;
     const int C4 = p.Dv / 4, ngrp = kMergeThreads / C4, grp = tid / C4, c = tid - grp * C4;
@@ -959,7 +964,9 @@ int launch_t(const Q8Args &a, cudaStream_t stream) {
     }
     count_launch();
     if (a.cluster || a.shares == 1) return 0;
-    cfg.gridDim = dim3((unsigned)((a.shares - 1) * a.p.Hkv * a.p.Q * a.p.G));
+    // a sequence has one seam at most, and so has a share
+    const int seams = a.p.B < a.shares - 1 ? a.p.B : a.shares - 1;
+    cfg.gridDim = dim3((unsigned)(seams * a.p.Hkv * a.p.Q * a.p.G));
     cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = 0;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
