@@ -1024,11 +1024,24 @@ __global__ void __launch_bounds__(kSummaryWarps * 32) mask_summary_kernel(const 
 
 // ------------------------------------------------------------------ host
 
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    if (fn == nullptr) {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
+                                             cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    }
+    return fn;
+}
+
 // 4-D map over [d3][d2][d1][d0] (d0 innermost) with a {64, b1, b2, 1} box and
 // 128-byte swizzle.
 int make_map(CUtensorMap *map, const void *ptr, CUtensorMapDataType dt, uint64_t d0, uint64_t d1,
              uint64_t d2, uint64_t d3, uint32_t b1, uint32_t b2) {
-    auto fn = tma_encode_fn();
+    auto fn = encode_fn();
     if (fn == nullptr) {
         set_error("cuTensorMapEncodeTiled is not available from the driver");
         return 3;
@@ -1184,19 +1197,6 @@ long long unit_count(const AttnParams &p) {
 }
 
 }  // namespace
-
-PFN_cuTensorMapEncodeTiled_v12000 tma_encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    if (fn == nullptr) {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
-                                             cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    }
-    return fn;
-}
 
 bool prefill_tc_supported(const AttnParams &p, int dtype) {
     if (dtype != 1 && dtype != 2) return false;

@@ -905,6 +905,20 @@ __global__ void __launch_bounds__(kMergeThreads) q8_merge_kernel(const __grid_co
     }
 }
 
+// The driver's cuTensorMapEncodeTiled, or null.
+PFN_cuTensorMapEncodeTiled_v12000 tma_encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            ptr = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    }();
+    return fn;
+}
+
 // 3-D pool [rows][Hkv][D] of bytes as a 4-D map: boxes of box_rows rows of one
 // head, `inner` bytes wide (columns past D read as zeros).
 int pool_map(CUtensorMap *map, const void *ptr, int D, int Hkv, uint64_t rows, int inner, int box_rows) {

@@ -4,7 +4,6 @@
 #pragma once
 
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -80,8 +79,6 @@ int launch_prefill_wide512_tc(const AttnParams &p, int dtype, cudaStream_t strea
 bool fwd_mma_supported(const AttnParams &p, int dtype);
 int launch_fwd_mma(const AttnParams &p, int dtype, cudaStream_t stream);
 
-// The driver's cuTensorMapEncodeTiled, or null.
-PFN_cuTensorMapEncodeTiled_v12000 tma_encode_fn();
 // 4-D TMA map over 16-bit elements [d3][d2][d1][d0] (d0 innermost), box
 // {64, b1, b2, 1}, 128-byte swizzle; returns 0 or an attn_status code.
 int make_tma_map_4d(CUtensorMap *map, const void *ptr, bool bf16, uint64_t d0, uint64_t d1,

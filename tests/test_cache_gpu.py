@@ -769,6 +769,53 @@ def test_two_captured_graphs_replay_as_the_eager_calls():
                 assert torch.equal(a.view(torch.uint8) if a.dim() else a, b.view(torch.uint8) if b.dim() else b)
 
 
+def test_offsets_past_32_bits():
+    """Pools of more than 4 GB: pages at their end are read and written as those of a
+    small pool are (attention by both paths, appending, copying, forking)."""
+    g = np.random.default_rng(41)
+    page, Hkv, D, P = 64, 8, 256, 33000          # 131072 bytes a page
+    c = Cache(g, [500, 64, 130], page, 16, Hkv, D, D, "int8", max_pages=9)
+    small = list(c.gpu())
+    n = small[0].shape[0]
+    big = [torch.empty((P,) + tuple(t.shape[1:]), dtype=t.dtype, device=DEV) for t in small]
+    off = P - n
+    for t, b in zip(small, big):
+        b[off:] = t
+    table = i32(c.table)
+    far = torch.where(table >= 0, table + off, table)
+    lens, new = i32(c.lens), i32([5, 64, 3])
+    refs = torch.bincount(table[table >= 0].long(), minlength=n).to(torch.int32)
+    far_refs = torch.cat([torch.ones(off, dtype=torch.int32, device=DEV), refs])
+    # a fork that copies pages (and finds its free ones at the end), rows behind them
+    par = i32([0, 0, 1, 2])
+    t1, l1, r1, s1 = attn.attn_pages_fork(small, table, lens, refs, par, page)
+    t2, l2, r2, s2 = attn.attn_pages_fork(big, far, lens, far_refs, par, page)
+    assert torch.equal(torch.where(t1 >= 0, t1 + off, t1), t2) and s1[3] > 0 and torch.equal(s1, s2)
+    x = [torch.randn((4, 7, Hkv, D), device=DEV).bfloat16() for _ in range(2)]
+    room = i32([7, 3, 0, 5])
+    attn.attn_cache_append(*x, *small, t1, l1, seqlens_new=room)
+    attn.attn_cache_append(*x, *big, t2, l2, seqlens_new=room)
+    for Q in (1, 40):
+        q = torch.randn((4, Q, 2 * Hkv, D), device=DEV).bfloat16()
+        a = attn.attn_fwd_paged_q8(q, *small, t1, l1 + room)
+        b = attn.attn_fwd_paged_q8(q, *big, t2, l2 + room)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    src, dst = i32([0, 2]), i32([n - 1, n - 2])
+    attn.attn_pages_copy(small, small, src, dst)
+    attn.attn_pages_copy(big, big, src + off, dst + off)
+    for t, b in zip(small, big):
+        assert torch.equal(t.view(torch.uint8), b[off:].contiguous().view(torch.uint8))
+
+
+def test_attention_without_lse():
+    g = np.random.default_rng(42)
+    c = Cache(g, [300, 7], 64, 16, 2, 128, 128, "e4m3")
+    args = (torch.randn((2, 1, 8, 128), device=DEV).half(), *c.gpu(), i32(c.table), i32(c.lens))
+    o, lse = attn.attn_fwd_paged_q8(*args)
+    o2, none = attn.attn_fwd_paged_q8(*args, want_lse=False)
+    assert none is None and torch.equal(o, o2)
+
+
 def test_launch_count_moves():
     n = attn.kernel_launches()
     for _ in serve(1):
