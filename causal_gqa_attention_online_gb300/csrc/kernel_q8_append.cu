@@ -20,6 +20,11 @@
 // rows' vectors of eight elements in registers between the two passes, and
 // reads again (from L2) only what a block of more than kKeep vectors a thread
 // leaves over.  Units of few vectors take one warp, others four.
+// Magnitudes are compared as integers, two 16-bit ones an instruction (infinities
+// and NaN come out above every finite value); a whole block whose rows divide the
+// threads takes a path without tests and steps by one pointer.  Measured: prompts
+// of 16 ragged sequences up to 4096 rows (8 heads, D 128, bf16 to e4m3, 212 MB) 40
+// us, 5.4 TB/s, 0.79 of a plain copy; 64 sequences of one row 6 us.
 #include <type_traits>
 
 #include "q8.cuh"

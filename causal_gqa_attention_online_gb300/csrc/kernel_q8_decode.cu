@@ -27,8 +27,7 @@
 // Bound: HBM, one byte an element -- at 8 flops a byte, twice the 16-bit
 // decode's arithmetic per byte, the conversions (4 to 5 instructions for four
 // codes) have to stay out of the way.  A CTA is four consumer warps of 32 keys
-// each and a producer warp: it looks pages up 32 boxes at a time and a group ahead
-// (one tile ahead it had a tile each table latency, 0.7 us), issues one TMA
+// each and a producer warp: it looks pages up 32 boxes at a time and a group ahead, issues one TMA
 // box per page piece (up to 64 rows) and the block scales as 4-byte cp.async,
 // all completing on the stage's mbarrier; consumers free a stage with one
 // arrival a warp, so no warp waits for another within a tile.  Tiles that every
@@ -49,6 +48,13 @@
 // tiles a CTA with every CTA resident) give each (sequence, head) a cluster of up
 // to eight CTAs, which split its tiles and join their states through distributed
 // shared memory: one launch and no workspace.
+//
+// Measured: 64 ragged sequences up to 8192 keys (Hq 32, Hkv 8, D 128) in 100 us
+// with int8 codes (5.44 TB/s, 0.80 of a plain copy) and 93 with e4m3; the copies
+// without any arithmetic take 90, ten of them launch and first tile.  Two sequences
+// of 100003 keys, four rows each of 16 heads over 4, D 64, e4m3: 35 us (2.6 TB/s),
+// bound by the softmax's chain of 16 rows and by the prologue.  One sequence of 700
+// keys: 10 us on the GPU.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -807,8 +813,9 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
 }
 
 // Joins the partials of a sequence that spans several shares, one row a block:
-// groups of Dv / 4 threads take every ngrp-th partial, four loads in flight each,
-// then the groups are added up.
+// groups of Dv / 4 threads take every ngrp-th partial, four loads in flight each
+// under a running maximum, then the groups are added up.  4 to 5 us: the seam, the
+// partials, the output, each a memory latency.
 constexpr int kMergeThreads = 128;
 
 __global__ void __launch_bounds__(kMergeThreads) q8_merge_kernel(const __grid_constant__ Q8Args a, int R) {

@@ -411,11 +411,18 @@ ATTN_API int attn_cache_append_varlen(const void *k, const void *v, void *k_page
  * attn_fwd_paged; seqlens_k counts the rows to attend to, the new ones among
  * them (append first, then attend).  Codes and scales past a sequence's length
  * are never used as values.
- * Kernels (`algo`): the copy of the keys and values in q's type that the others
- * read is made in a workspace from the library's pool, one group of sequences
- * after the other; with the powers of two that attn_cache_append writes it is
- * exact (fp16: within +-65504), other scales round once.  algo then chooses as in
- * attn_fwd_ex.
+ * Kernels (`algo`): ATTN_ALGO_AUTO reads the codes themselves (ATTN_ALGO_DECODE)
+ * where few rows share them: bf16/fp16, Q * Hq / Hkv <= 16, D and Dv multiples of
+ * 16 up to 256, pages of 8 rows or more.  Scales then multiply scores and
+ * probabilities in fp32 and no key or value is rounded; small problems take one
+ * launch without a workspace, others a second one that merges the partials of
+ * sequences cut between blocks.  Other problems, and the other values of algo
+ * (as in attn_fwd_ex), run on a copy of the keys and values in q's type, made
+ * group by group of sequences in a workspace from the library's pool (512 MB, or
+ * one sequence): exact with the powers of two that attn_cache_append writes (fp16:
+ * within +-65504), rounded once with other scales.  A sequence's key that a row
+ * attends to and whose scale or code is NaN makes that row what attn_fwd gives for
+ * a NaN key or value (ATTN_ALGO_DECODE: NaN).
  * Return codes as attn_fwd.
  */
 ATTN_API int attn_fwd_paged_q8(const void *q, const void *k_pages, const void *v_pages,
