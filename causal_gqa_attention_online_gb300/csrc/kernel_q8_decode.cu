@@ -1048,7 +1048,8 @@ bool q8_decode_supported(const AttnParams &p, int dtype) {
     if (p.D % 16 || p.Dv % 16 || p.D > 256 || p.Dv > 256 || p.page_size < 8) return false;
     if ((long long)p.Q * p.G > 16 || p.Q < 1) return false;
     // CTAs, merge blocks and tiles are counted in 32 bits
-    return p.Hkv <= 65535 && (long long)p.B * p.Hkv < (1LL << 31) && (long long)p.B * (((long long)p.K + kTile - 1) / kTile) < (1LL << 31);
+    return p.Hkv <= 65535 && (long long)p.B * p.Hkv < (1LL << 31) &&
+           (long long)p.B * (((long long)p.K + kTile - 1) / kTile) < (1LL << 31);
 }
 
 unsigned long long q8_decode_workspace(const AttnParams &p, int nsm) {
