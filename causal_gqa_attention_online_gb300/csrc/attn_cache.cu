@@ -1,6 +1,7 @@
 // attn_cache.cu -- the C ABI of the 8-bit paged K/V cache: appending rows,
 // attention over it, and copying, forking and compacting its pages.
 // Declarations and contracts: include/attn_gqa.h.
+#include <cmath>
 #include <cstring>
 
 #include "attn_gqa.h"
@@ -10,6 +11,8 @@
 
 namespace attn {
 namespace {
+
+constexpr int kMaxCount = 1 << 30;  // pages of a pool and slots of a table, in the plans
 
 int log2_of(long long n) {  // n a power of two
     int s = 0;
@@ -43,6 +46,10 @@ int validate_cache(const void *k_pages, const void *v_pages, const float *k_scal
     if (Hkv < 1 || D < 1 || D > 512 || Dv < 1 || Dv > 512) {
         set_error("head widths must be in [1, 512] and Hkv positive (Hkv=%d D=%d Dv=%d)", Hkv, D,
                   Dv);
+        return ATTN_ERR_INVALID;
+    }
+    if ((long long)Hkv * (D > Dv ? D : Dv) >= (1LL << 31)) {
+        set_error("a token's heads have 2^31 or more elements (Hkv=%d D=%d Dv=%d)", Hkv, D, Dv);
         return ATTN_ERR_INVALID;
     }
     if (k_pages == nullptr || v_pages == nullptr || k_scale == nullptr || v_scale == nullptr) {
@@ -133,11 +140,12 @@ int run_expanded(const AttnParams &p, const Q8Cache &c, int dtype, int algo, cud
     long long group = kExpandBytes / (kb + vb > 0 ? kb + vb : 1);
     if (group < 1) group = 1;
     // every group's rows of q and o start on a 16-byte boundary
-    if ((p.Q * (long long)p.Hq * p.D * es) % 16 || (p.Q * (long long)p.Hq * p.Dv * es) % 16)
-        group = (group + 7) / 8 * 8;
+    const bool odd = (p.Q * (long long)p.Hq * p.D * es) % 16 || (p.Q * (long long)p.Hq * p.Dv * es) % 16;
+    const long long unit = odd ? 8 : 1;
+    group = (group + unit - 1) / unit * unit;
     // (the grids of the expansion and of the CUDA-core kernel)
-    const long long most = 65535 / (p.Hkv > 0 ? p.Hkv : 1) / 8 * 8;
-    if (most > 0 && group > most) group = most;
+    const long long most = 65535 / p.Hkv / unit * unit;
+    if (group > most) group = most > 0 ? most : unit;
     if (group > p.B) group = p.B;
     // the values start on a 256-byte boundary
     const long long v_at = (group * kb + 255) / 256 * 256;
@@ -256,6 +264,10 @@ int attn_fwd_paged_q8(const void *q, const void *k_pages, const void *v_pages,
         set_error("a window needs a causal mask (window=%d with ATTN_MASK_NONE)", window);
         return ATTN_ERR_INVALID;
     }
+    if (!std::isfinite(scale)) {
+        set_error("the scale must be finite (got %g)", (double)scale);
+        return ATTN_ERR_INVALID;
+    }
     if ((long long)B * Q * Hq == 0) return ATTN_OK;
     if ((max_pages > 0 && block_table == nullptr) || seqlens_k == nullptr) {
         set_error("paged K/V needs block_table and seqlens_k");
@@ -356,7 +368,8 @@ int attn_pages_fork(void *const *pools, const long long *page_bytes, int npools,
         set_error("page_size must be a power of two in [1, 2^20] (got %d)", page_size);
         return ATTN_ERR_INVALID;
     }
-    if (S < 0 || N < 0 || max_pages < 0 || num_pages < 1 ||
+    // (slots and pages are stepped through in 32 bits)
+    if (S < 0 || N < 0 || max_pages < 0 || num_pages < 1 || N > kMaxCount || num_pages > kMaxCount ||
         (long long)max_pages * page_size >= (1LL << 31)) {
         set_error("attn_pages_fork: bad sizes (S=%d N=%d max_pages=%d num_pages=%d page_size=%d)",
                   S, N, max_pages, num_pages, page_size);
@@ -391,7 +404,7 @@ int attn_pages_compact(void *const *pools, const long long *page_bytes, int npoo
     int rc = validate_pools(const_cast<const void *const *>(pools), pools, page_bytes, npools,
                             "attn_pages_compact");
     if (rc) return rc;
-    if (S < 0 || max_pages < 0 || num_pages < 1) {
+    if (S < 0 || max_pages < 0 || num_pages < 1 || num_pages > kMaxCount) {
         set_error("attn_pages_compact: bad sizes (S=%d max_pages=%d num_pages=%d)", S, max_pages,
                   num_pages);
         return ATTN_ERR_INVALID;

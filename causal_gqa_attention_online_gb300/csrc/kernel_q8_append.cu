@@ -141,8 +141,9 @@ __global__ void __launch_bounds__(128, VEC && sizeof(T) == 2 ? 8 : 3) append_ker
     const uint32_t u = blockIdx.x * (128 / TG) + threadIdx.x / TG;
     const int which = (int)(u & 1u);
     const int t = (int)((u >> 1) / (uint32_t)a.Hkv), h = (int)((u >> 1) - (uint32_t)t * (uint32_t)a.Hkv);
-    const int b = blockIdx.y + blockIdx.z * gridDim.y;
-    if (t >= a.touch || b >= a.B) return;
+    const uint32_t ub = blockIdx.y + blockIdx.z * gridDim.y;
+    if (t >= a.touch || ub >= (uint32_t)a.B) return;
+    const int b = (int)ub;
 
     const long long cap = (long long)a.max_pages << a.page_shift;
     const int len = clamp_len(__ldg(a.seqlens_k + b), (int)cap);

@@ -677,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
                 break;
             }
             const int key0 = un.kbeg + t * kTile + kw0;
-            if (key0 >= lo_all && key0 + 32 <= hi_all) step(std::false_type{}, key0, s);
+            if (key0 >= lo_all && hi_all - key0 >= 32) step(std::false_type{}, key0, s);
             else if (key0 < un.kend) step(std::true_type{}, key0, s);
             __syncwarp();
             if (lane == 0) sm100::mbar_arrive(empty + 8 * s);
@@ -1048,7 +1048,7 @@ bool q8_decode_supported(const AttnParams &p, int dtype) {
     if (p.D % 16 || p.Dv % 16 || p.D > 256 || p.Dv > 256 || p.page_size < 8) return false;
     if ((long long)p.Q * p.G > 16 || p.Q < 1) return false;
     // CTAs, merge blocks and tiles are counted in 32 bits
-    return p.Hkv <= 65535 && (long long)p.B * p.Hkv < (1LL << 31) &&
+    return p.Hkv <= 65535 && (long long)p.B * p.Hkv <= (1LL << 30) &&
            (long long)p.B * (((long long)p.K + kTile - 1) / kTile) < (1LL << 31);
 }
 

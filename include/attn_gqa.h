@@ -409,7 +409,7 @@ ATTN_API int attn_cache_append_varlen(const void *k, const void *v, void *k_page
  * attn_fwd_paged_q8 -- attn_fwd_paged over an 8-bit paged cache: the attention of
  * the values code * scale.  q [B, Q, Hq, D], o [B, Q, Hq, Dv], lse as in
  * attn_fwd_paged; seqlens_k counts the rows to attend to, the new ones among
- * them (append first, then attend).  Codes and scales past a sequence's length
+ * them (append first, then attend); `scale` is finite.  Codes and scales past a sequence's length
  * are never used as values.
  * Kernels (`algo`): ATTN_ALGO_AUTO reads the codes themselves (ATTN_ALGO_DECODE)
  * where few rows share them: bf16/fp16, Q * Hq / Hkv <= 16, D and Dv multiples of
@@ -437,7 +437,8 @@ ATTN_API int attn_fwd_paged_q8(const void *q, const void *k_pages, const void *v
  * Pages of a cache.  A pool is any array whose first axis counts pages: the K or
  * V pages of a layer, or their scales.  `pools` is a HOST array of npools device
  * pointers, page_bytes the bytes of one page of each (any number, also more than
- * one launch takes).  All pools share the block tables.
+ * one launch takes).  All pools share the block tables.  Tables have at most 2^30
+ * slots, pools 2^30 pages.
  *
  * attn_pages_copy -- copies page src[i] of src_pools[p] to page dst[i] of
  * dst_pools[p] for i < n and every p.  src and dst are device int32; pairs with a

@@ -807,6 +807,31 @@ def test_offsets_past_32_bits():
         assert torch.equal(t.view(torch.uint8), b[off:].contiguous().view(torch.uint8))
 
 
+def test_attention_at_the_last_key_that_32_bits_count():
+    """A sequence of 2^31 - 64 keys (a table that names one page again and again):
+    the last tile ends behind the keys and, counted in 32 bits, behind 2^31.  Every
+    score is -30 and every value 3, so the output is 3.  A thread adds up the terms
+    of 2^24 tiles over at least 256 shares in fp32, 2^16 additions: its sum of
+    probabilities is off by 2^16 * 2^-24 = 2^-8 of itself at most (the sums of values
+    are of equal powers of two, and exact), the merge of a few hundred terms by
+    2^-14, and fp16 rounds by 2^-11.  Keys that do not exist would score 0, e^30
+    above the others."""
+    page, D, K = 64, 16, (1 << 31) - 64
+    kp = torch.full((1, page, 1, D), 2, dtype=torch.int8, device=DEV)
+    vp = torch.full((1, page, 1, D), 3, dtype=torch.int8, device=DEV)
+    one = torch.ones((1, 1, 1), device=DEV)
+    table = torch.zeros((1, K // page), dtype=torch.int32, device=DEV)
+    q = torch.full((1, 1, 1, D), -1., dtype=torch.float16, device=DEV)   # score -32, x scale
+    scale = 30. / 32.
+    for lens, window in ((K, 0), (K, 1000), (K - 37, 0)):
+        o, lse = attn.attn_fwd_paged_q8(q, kp, vp, one, one, table, i32([lens]), window=window,
+                                        scale=scale)
+        n = min(lens, window or lens)
+        off = 2. ** -8 + 2. ** -14
+        assert abs(o.double().mean().item() - 3.) <= 3 * (off + 2. ** -11) and o.std() == 0
+        assert abs(lse.item() - (math.log(n) - 30.)) <= 1.01 * off + 1e-4   # (fp32 near 30: 2e-6)
+
+
 def test_attention_without_lse():
     g = np.random.default_rng(42)
     c = Cache(g, [300, 7], 64, 16, 2, 128, 128, "e4m3")

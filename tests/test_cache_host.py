@@ -117,6 +117,22 @@ def test_decode_kernel_refuses_what_it_does_not_take(lib, kw):
     assert "8-bit decode kernel" in lib.attn_last_error().decode()
 
 
+@pytest.mark.parametrize("scale", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("algo", [0, 1, 3])
+def test_attention_refuses_a_scale_that_is_no_number(lib, scale, algo):
+    p = [vp(x) for x in (1 << 20, 1 << 22, 1 << 23, 1 << 24, 1 << 25, 1 << 28)]
+    assert lib.attn_fwd_paged_q8(*p, None, 2, 4, 2, 1, 64, 64, vp(1 << 27), 4, 64, 16, 16, 1, None,
+                                 vp(1 << 26), 0, scale, 0, 2, algo, None) == 1
+    assert "finite" in lib.attn_last_error().decode()
+
+
+def test_cache_refuses_rows_of_too_many_elements(lib):
+    """A row's elements are counted in 32 bits."""
+    heads = (1 << 31) // 64
+    assert _append(lib, Hkv=heads) == 1 and "2^31" in lib.attn_last_error().decode()
+    assert _fwd(lib, Hq=heads, Hkv=heads) == 1 and "2^31" in lib.attn_last_error().decode()
+
+
 def test_attention_of_nothing_is_a_noop(lib):
     assert _fwd(lib, B=0, q=0, o=0, table=0, lens=0) == 0
     assert _fwd(lib, Q=0, q=0, o=0, table=0, lens=0) == 0
@@ -163,6 +179,8 @@ def _fork(lib, table=1 << 20, lens=1 << 21, refs=1 << 22, S=2, M=4, P=16, page=6
     (dict(page=10), "page_size"),
     (dict(S=-1), "bad sizes"),
     (dict(N=-1), "bad sizes"),
+    (dict(N=(1 << 30) + 1), "bad sizes"),
+    (dict(P=(1 << 30) + 1), "bad sizes"),
     (dict(P=0), "bad sizes"),
     (dict(M=1 << 26), "bad sizes"),
     (dict(refs=0), "null pointer"),
@@ -182,6 +200,7 @@ def test_fork_refuses(lib, kw, needle):
 @pytest.mark.parametrize("kw,needle", [
     (dict(S=-1), "bad sizes"),
     (dict(P=0), "bad sizes"),
+    (dict(P=(1 << 30) + 1), "bad sizes"),
     (dict(refs=0), "null pointer"),
     (dict(table=0), "null pointer"),
     (dict(remap=0), "null pointer"),
