@@ -93,11 +93,17 @@ struct Q8Args {
     float *part_o, *part_lse;
 };
 
+// Resident CTAs an SM: two, one where a row is wider than 128; three for 64-wide
+// heads with up to eight rows (125 registers), whose tiles are half as large: 32
+// sequences of up to 8192 keys and eight heads 43.3 us for 45.3, 64 of 4096 41.3 for
+// 43.8 (16 rows would spill and are slower: 24.7 for 22.7).
+constexpr int resident(int DP, int NT) { return DP > 128 ? 1 : DP == 64 && NT == 1 ? 3 : 2; }
+
 template <int DP, int NT> struct Ring {
     static constexpr int HALF = DP > 128 ? 128 : DP;  // bytes of a box row
     static constexpr int TILE = kTile * DP;
     static constexpr int STAGE = 2 * TILE + 2 * kTile * 4;
-    static constexpr int NS = DP == 64 ? 5 : 3;
+    static constexpr int NS = DP > 64 ? 3 : NT == 1 ? 4 : 5;
     // the warps' O are merged MC columns at a time through two warps' buffers
     static constexpr int R = NT * 8;
     static constexpr int MC = DP == 64 ? 64 : DP / NT;
@@ -107,7 +113,8 @@ template <int DP, int NT> struct Ring {
     static constexpr int BARS = STATS + (2 * 4 * R + 4) * 4;
     static constexpr int SHARE = BARS + 16 * NS;  // {left, sequence, tile}, abort flag
     static constexpr int SMEM = SHARE + 32;
-    static_assert(SMEM <= (DP > 128 ? 227 : 113) * 1024, "one or two CTAs an SM");
+    // (an SM has 228 KB, a CTA takes 1 KB more than its own)
+    static_assert(SMEM <= (228 / resident(DP, NT) - 1) * 1024, "resident() CTAs an SM");
 };
 
 // Byte offset of 16-byte chunk c of row r: rows of 64 bytes in the 64-byte
@@ -222,7 +229,7 @@ __device__ __noinline__ void join_cluster(const Q8Args &a, int b, int kvh, int r
 }
 
 template <int CODE, int DP, int NT>
-__global__ void __launch_bounds__(kThreads, DP > 128 ? 1 : 2)
+__global__ void __launch_bounds__(kThreads, resident(DP, NT))
     q8_decode_kernel(const __grid_constant__ Q8Args a, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV) {
     using Op = CodeOps<CODE>;
@@ -1016,7 +1023,8 @@ template <int CODE> int launch_code(const Q8Args &a, cudaStream_t stream) {
 }
 
 int resident_ctas(const AttnParams &p, int nsm) {
-    return (nsm < 1 ? 1 : nsm) * (p.D > 128 || p.Dv > 128 ? 1 : 2);
+    const int w = p.D > p.Dv ? p.D : p.Dv;
+    return (nsm < 1 ? 1 : nsm) * resident(w <= 64 ? 64 : w <= 128 ? 128 : 256, p.Q * p.G <= 8 ? 1 : 2);
 }
 
 // CTAs of a (sequence, head) in cluster mode, 0 for shares: as many as are all
@@ -1028,10 +1036,9 @@ int cluster_of(const AttnParams &p, int nsm) {
     return tiles <= 4 * c && units < (1LL << 31) ? c : 0;
 }
 
-// Shares: as many as give each resident CTA (two an SM up to widths of 128, one
-// above) one of a head; where that is few of them and leaves CTAs over (more
-// than a 40th), four times as many.  No more than the tables' capacity has
-// tiles.
+// Shares: as many as give each resident CTA one of a head; where that is few of
+// them and leaves CTAs over (more than a 40th), four times as many.  No more than
+// the tables' capacity has tiles.
 int shares_of(const AttnParams &p, int nsm) {
     const long long ctas = resident_ctas(p, nsm);
     long long n = ctas / p.Hkv;
