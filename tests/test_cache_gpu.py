@@ -1,6 +1,7 @@
 """The 8-bit paged cache on the GPU against its plain restatement in 64 bits
 (tests/cache_ref.py) and the oracle: appended codes and scales exactly,
 attention within a bound derived from the roundings, pages exactly."""
+import concurrent.futures
 import math
 
 import numpy as np
@@ -830,6 +831,39 @@ def test_attention_at_the_last_key_that_32_bits_count():
         off = 2. ** -8 + 2. ** -14
         assert abs(o.double().mean().item() - 3.) <= 3 * (off + 2. ** -11) and o.std() == 0
         assert abs(lse.item() - (math.log(n) - 30.)) <= 1.01 * off + 1e-4   # (fp32 near 30: 2e-6)
+
+
+def test_calls_from_two_threads():
+    """Two threads, a stream each, append, attend and fork at the same time, each on
+    a cache of its own: what the calls give one after the other."""
+    def work(seed, stream):
+        g = np.random.default_rng(seed)
+        c = Cache(g, [300, 64, 0, 1000 + seed], 64, 16, 4, 128, 128, "int8", max_pages=20)
+        x = [torch.from_numpy(g.standard_normal((4, 9, 4, 128), np.float32)).to(DEV).bfloat16()
+             for _ in range(2)]
+        q = torch.from_numpy(g.standard_normal((4, 9, 8, 128), np.float32)).to(DEV).bfloat16()
+        pools, table, lens = list(c.gpu()), i32(c.table), i32(c.lens)
+        refs = torch.zeros(pools[0].shape[0], dtype=torch.int32, device=DEV)
+        refs[table[table >= 0].long()] = 1
+        parents, new = i32([0, 1, 2, 3]), i32([1, 0, 3, 2])
+        torch.cuda.current_stream().synchronize()
+        out = []
+        with torch.cuda.stream(stream):
+            for _ in range(20):
+                t, n, r, s = attn.attn_pages_fork(pools, table, lens, refs, parents, 64, new_tokens=new)
+                attn.attn_cache_append(*x, *pools, t, n, seqlens_new=new)
+                for Q in (1, 9):
+                    out += attn.attn_fwd_paged_q8(q[:, :Q].contiguous(), *pools, t, n + new)
+                out += [t, n, r, s]
+        stream.synchronize()
+        return out
+
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    alone = [work(seed, streams[0]) for seed in (50, 51)]
+    with concurrent.futures.ThreadPoolExecutor(2) as pool:
+        both = list(pool.map(work, (50, 51), streams))
+    for a, b in zip(alone, both):
+        assert len(a) == len(b) and all(np.array_equal(bits(x), bits(y)) for x, y in zip(a, b))
 
 
 def test_attention_without_lse():
