@@ -316,7 +316,7 @@ int attn_fwd_paged_q8(const void *q, const void *k_pages, const void *v_pages,
     // choose among the kernels that read the expanded rows
     const bool decode = q8_decode_supported(p, dtype);
     if (algo == ATTN_ALGO_DECODE && !decode) {
-        set_error("the 8-bit decode kernel takes bf16/fp16, Q * Hq / Hkv <= 16, D and Dv multiples of "
+        set_error("the 8-bit decode kernel takes bf16/fp16, Q * Hq / Hkv <= 1024, D and Dv multiples of "
                   "16 up to 256 and pages of 8 rows or more");
         return ATTN_ERR_UNSUPPORTED;
     }
@@ -324,8 +324,8 @@ int attn_fwd_paged_q8(const void *q, const void *k_pages, const void *v_pages,
     rc = current_device(&dev);
     if (rc == 0) rc = status_ptr(dev, &p.status);
     if (rc) return rc;
-    if (decode && (algo == ATTN_ALGO_AUTO || algo == ATTN_ALGO_DECODE)) {
-        const int nsm = sm_count(dev);
+    const int nsm = sm_count(dev);
+    if (algo == ATTN_ALGO_DECODE || (algo == ATTN_ALGO_AUTO && decode && q8_decode_wins(p, nsm))) {
         return with_workspace(q8_decode_workspace(p, nsm), reinterpret_cast<cudaStream_t>(stream),
                               [&](void *ws) {
             return launch_q8_decode(p, c, dtype, nsm, ws, reinterpret_cast<cudaStream_t>(stream));

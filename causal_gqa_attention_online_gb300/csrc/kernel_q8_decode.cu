@@ -1,6 +1,6 @@
 // kernel_q8_decode.cu -- split-KV tensor-core decode over the 8-bit paged cache
-// (bf16 / fp16 queries, at most 16 rows of a KV group, widths multiples of 16
-// up to 256, pages of at least 8 rows).
+// (bf16 / fp16 queries, widths multiples of 16 up to 256, pages of at least 8 rows,
+// the rows of a KV group in row groups of 16 or fewer).
 //
 // The products are those of the 16-bit decode, keys (or value columns) on M and
 // the rows of the KV group on N,
@@ -36,7 +36,7 @@
 // be e4m3's NaN).
 //
 // Work: the 128-key tiles of all sequences, in order, are cut into equal shares
-// whatever the lengths, and a CTA takes one share for one KV head -- as many
+// whatever the lengths, and a CTA takes one share for one KV head (and row group) -- as many
 // shares as give every resident CTA one, so that the heads of a page are read at
 // the same time (with the heads one after the other, the 256-byte reads of
 // 128-byte head rows brought in 719 MB for 547).  The producer runs from one
@@ -77,6 +77,7 @@ namespace {
 constexpr int kTile = 128;  // keys a tile: 4 warps x 32
 constexpr int kThreads = 160;
 constexpr float kPOff = 14.f;  // p is scaled by 2^14
+constexpr int kMaxRows = 1024;  // rows of a KV group at most
 
 struct Q8Args {
     AttnParams p;
@@ -86,9 +87,10 @@ struct Q8Args {
     bool bf16;
     int cluster;   // CTAs of a (sequence, head), or 0: shares
     int shares;    // shares at most (no more than there are tiles are used)
+    int groups;    // row groups of a KV head, of R rows each (the last may have fewer)
     // workspace: for each share {sequence, its first share, its last} where the
     // merge of a sequence is found (its second share; {-1} elsewhere), partials
-    // [CTA][2][R] of normalised rows and log2 sums
+    // [CTA][2][R] of normalised rows and log2 sums (CTA: share, head, row group)
     int4 *seam;
     float *part_o, *part_lse;
 };
@@ -192,12 +194,12 @@ __device__ __forceinline__ void empty_rows(const Q8Args &a, int b, int kvh, int 
 // each: four columns a thread, the (row, column) pairs spread over the CTAs.  (A
 // function of its own, so that its registers do not add to the main loop's.)
 template <int DP>
-__device__ __noinline__ void join_cluster(const Q8Args &a, int b, int kvh, int rank, int ntiles, float *xrow,
-                                          float *xlse) {
+__device__ __noinline__ void join_cluster(const Q8Args &a, int b, int kvh, int row0, int rows, int rank, int ntiles,
+                                          float *xrow, float *xlse) {
     const AttnParams &p = a.p;
     auto cluster = cooperative_groups::this_cluster();
     const int C = a.cluster, C4 = p.Dv / 4;
-    for (int i = rank * kThreads + threadIdx.x; i < p.Q * p.G * C4; i += C * kThreads) {
+    for (int i = rank * kThreads + threadIdx.x; i < rows * C4; i += C * kThreads) {
         const int row = i / C4, c = i - row * C4;
         float lw[8], mx = -INFINITY;
         float4 v[8];
@@ -224,7 +226,7 @@ __device__ __noinline__ void join_cluster(const Q8Args &a, int b, int kvh, int r
             acc.z = fmaf(w, v[r].z, acc.z);
             acc.w = fmaf(w, v[r].w, acc.w);
         }
-        put_row(a, b, kvh, row, c, acc, sum, mx);
+        put_row(a, b, kvh, row0 + row, c, acc, sum, mx);
     }
 }
 
@@ -240,10 +242,11 @@ __global__ void __launch_bounds__(kThreads, resident(DP, NT))
     const AttnParams &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, tig = lane & 3;
-    // shares: CTA (share, head); clusters: (sequence, head, rank)
+    // shares: CTA (share, head, row group); clusters: (sequence, head, row group, rank)
     const int C = a.cluster;
-    const int xi = C ? blockIdx.x / C : blockIdx.x;
-    const int share_i = xi / p.Hkv, kvh = xi - share_i * p.Hkv;
+    const int xi = C ? blockIdx.x / C : blockIdx.x, vheads = p.Hkv * a.groups;
+    const int share_i = xi / vheads, head_i = xi - share_i * vheads;
+    const int kvh = head_i / a.groups, row0 = (head_i - kvh * a.groups) * R;
     const int rank = C ? blockIdx.x - xi * C : 0;
     const uint32_t sbase = smem_u32(smem);
     const uint32_t full = sbase + L::BARS, empty = full + 8 * NS;
@@ -298,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, resident(DP, NT))
             if (here) {
                 share[1] = b0 + lane;
                 share[2] = t0 - first;
-                if (kvh == 0) {
+                if (head_i == 0) {
                     // where the sequence's first seam is this share's beginning
                     int4 v = make_int4(-1, 0, 0, 0);
                     const int c0 = (int)sh.of(first);
@@ -317,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, resident(DP, NT))
             look(b0, b0 + lane < p.B ? unit_of(a, b0 + lane).ntiles : 0);
         if (lane == 0) {
             share[0] = left;
-            if (left == 0 && kvh == 0) a.seam[share_i] = make_int4(-1, 0, 0, 0);
+            if (left == 0 && head_i == 0) a.seam[share_i] = make_int4(-1, 0, 0, 0);
         }
     } else if (C == 0) {
         // meanwhile: the rows of sequences without keys, +0 and -inf (each lane
@@ -341,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, resident(DP, NT))
     if (C) {
         b = share_i;
         if (un.ntiles == 0) {  // (so it is for the whole cluster)
-            if (rank == 0 && warp == 0) empty_rows(a, b, kvh, lane);
+            if (rank == 0 && row0 == 0 && warp == 0) empty_rows(a, b, kvh, lane);
             return;
         }
         tile = rank * un.ntiles / C;  // (some ranks have none where there are few)
@@ -444,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, resident(DP, NT))
     // (clusters: the CTA's rows and log2 sums in the drained ring)
     float *xrow = reinterpret_cast<float *>(smem), *xlse = xrow + R * DP;
     const int G = p.G;
-    const int nrows = p.Q * G;  // rows of a unit (<= R)
+    const int nrows = min(R, p.Q * G - row0);  // rows of the CTA's group
     const int kw0 = warp * 32;
     float *stat_m = reinterpret_cast<float *>(smem + L::STATS), *stat_l = stat_m + 4 * R;
     float *stat_u = stat_l + 4 * R;
@@ -453,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, resident(DP, NT))
     bool ok = true;
     for (bool first_seg = true; left > 0 && warp < 4; first_seg = false) {
         const int n = (int)min((long long)(un.ntiles - tile), left);
-        const int nvalid = un.si.Qb * G;
+        const int nvalid = un.si.Qb * G - row0;
         // Q^T fragments (B operand of S^T): column n = row g; in each 16 columns
         // lane tig holds columns 4 tig to 4 tig + 3, paired as the codes' bytes are.
         uint32_t qf[DP / 16][NT][2];
@@ -466,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, resident(DP, NT))
 #pragma unroll
             for (int kk = 0; kk < DP / 16; ++kk) raw[kk] = make_uint2(0, 0);
             if (row < nvalid) {
-                const int qi = row / G, h = kvh * G + row % G;
+                const int qi = (row0 + row) / G, h = kvh * G + (row0 + row) % G;
                 const uint16_t *src = static_cast<const uint16_t *>(p.q) +
                                       ((un.si.q_off + qi) * p.Hq + h) * (long long)p.D + 4 * tig;
 #pragma unroll
@@ -510,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, resident(DP, NT))
             for (int e = 0; e < 2; ++e) {
                 const int row = nt * 8 + 2 * tig + e;
                 int lo = 0, hi = 0;
-                if (row < nvalid) legal_range(row / G, un.si.Qb, un.si.Kb, p.window, p.mask, lo, hi);
+                if (row < nvalid) legal_range((row0 + row) / G, un.si.Qb, un.si.Kb, p.window, p.mask, lo, hi);
                 rlo[nt][e] = lo;
                 rhi[nt][e] = hi;
                 if (row < nrows) {
@@ -785,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, resident(DP, NT))
                     const float unit = U;
                     const float lse2 = ls != ls ? ls : ls > 0.f ? M[nt][e] - kPOff + __log2f(ls) : -INFINITY;
                     if (whole) {
-                        const int qi = row / G, h = kvh * G + row % G;
+                        const int qi = (row0 + row) / G, h = kvh * G + (row0 + row) % G;
                         const long long orow = (un.si.q_off + qi) * p.Hq + h;
                         uint16_t *dst = static_cast<uint16_t *>(p.o) + orow * p.Dv + 2 * g;
 #pragma unroll
@@ -815,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, resident(DP, NT))
     if (C <= 1) return;
 
     cooperative_groups::this_cluster().sync();
-    join_cluster<DP>(a, b, kvh, rank, un.ntiles, xrow, xlse);
+    join_cluster<DP>(a, b, kvh, row0, nrows, rank, un.ntiles, xrow, xlse);
     cooperative_groups::this_cluster().sync();  // every CTA's rows are read before it exits
 }
 
@@ -855,8 +858,8 @@ __global__ void __launch_bounds__(kMergeThreads) q8_merge_kernel(const __grid_co
     // the first share's last partial (unless it begins with the sequence), the
     // others' first
     auto part = [&](int i) -> long long {
-        const long long cta = (long long)(seam.y + i) * p.Hkv + kvh;
-        return (2 * cta + (i == 0 ? seam.w : 0)) * R + row;
+        const long long cta = ((long long)(seam.y + i) * p.Hkv + kvh) * a.groups + row / R;
+        return (2 * cta + (i == 0 ? seam.w : 0)) * R + row % R;
     };
     // a running maximum a thread, four partials loaded at a time
     float mx = -INFINITY, sum = 0.f;
@@ -971,7 +974,7 @@ int launch_t(const Q8Args &a, cudaStream_t stream) {
         return 3;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.cluster ? a.p.B * a.p.Hkv * a.cluster : a.shares * a.p.Hkv));
+    cfg.gridDim = dim3((unsigned)((a.cluster ? a.p.B * a.cluster : a.shares) * a.p.Hkv * a.groups));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = L::SMEM;
     cfg.stream = stream;
@@ -1022,6 +1025,8 @@ template <int CODE> int launch_code(const Q8Args &a, cudaStream_t stream) {
     return launch_nt<CODE, 256>(a, stream);
 }
 
+int groups_of(const AttnParams &p) { return (p.Q * p.G + 15) / 16; }
+
 int resident_ctas(const AttnParams &p, int nsm) {
     const int w = p.D > p.Dv ? p.D : p.Dv;
     return (nsm < 1 ? 1 : nsm) * resident(w <= 64 ? 64 : w <= 128 ? 128 : 256, p.Q * p.G <= 8 ? 1 : 2);
@@ -1030,21 +1035,29 @@ int resident_ctas(const AttnParams &p, int nsm) {
 // CTAs of a (sequence, head) in cluster mode, 0 for shares: as many as are all
 // resident, and no more than its tiles, when that leaves a CTA at most four.
 int cluster_of(const AttnParams &p, int nsm) {
-    const long long units = (long long)p.B * p.Hkv, tiles = ((long long)p.K + kTile - 1) / kTile;
+    const long long units = (long long)p.B * p.Hkv * groups_of(p), tiles = ((long long)p.K + kTile - 1) / kTile;
     int c = 8;
     while (c > 1 && (units * c > resident_ctas(p, nsm) || c >= 2 * tiles)) c /= 2;
     return tiles <= 4 * c && units < (1LL << 31) ? c : 0;
 }
 
-// Shares: as many as give each resident CTA one of a head; where that is few of
-// them and leaves CTAs over (more than a 40th), four times as many.  No more than
-// the tables' capacity has tiles.
+// Shares: a wave of resident CTAs, or up to four where one would leave many of them
+// over: as many as take the least time, a wave's launch and first tile counted as
+// eight tiles (256 rows of 8 heads, D 64, over 2000 keys: 25 us, 49 with the four waves that
+// fill the GPU best).  No more than the tables' capacity has tiles.
 int shares_of(const AttnParams &p, int nsm) {
-    const long long ctas = resident_ctas(p, nsm);
-    long long n = ctas / p.Hkv;
-    if ((ctas - n * p.Hkv) * 40 > ctas) n = (4 * ctas + p.Hkv - 1) / p.Hkv;
+    const long long ctas = resident_ctas(p, nsm), heads = (long long)p.Hkv * groups_of(p);
     const long long tiles = (long long)p.B * (((long long)p.K + kTile - 1) / kTile);
-    return (int)(tiles < 1 ? 1 : tiles < n ? tiles : n);
+    long long best = 1, least = LLONG_MAX;
+    for (int w = 1; w <= 4; ++w) {
+        const long long m = w * ctas / heads, n = m < 1 ? 1 : m > tiles && tiles > 0 ? tiles : m;
+        const long long cost = (n * heads + ctas - 1) / ctas * (8 + (tiles + n - 1) / n);
+        if (cost < least) {
+            least = cost;
+            best = n;
+        }
+    }
+    return (int)best;
 }
 
 }  // namespace
@@ -1053,16 +1066,34 @@ bool q8_decode_supported(const AttnParams &p, int dtype) {
     if (dtype != 1 && dtype != 2) return false;
     // TMA copies rows of D bytes from 16-byte boundaries, and whole 8-row swizzle atoms
     if (p.D % 16 || p.Dv % 16 || p.D > 256 || p.Dv > 256 || p.page_size < 8) return false;
-    if ((long long)p.Q * p.G > 16 || p.Q < 1) return false;
+    if ((long long)p.Q * p.G > kMaxRows || p.Q < 1) return false;
     // CTAs, merge blocks and tiles are counted in 32 bits
     return p.Hkv <= 65535 && (long long)p.B * p.Hkv <= (1LL << 30) &&
            (long long)p.B * (((long long)p.K + kTile - 1) / kTile) < (1LL << 31);
 }
 
+// More than 16 rows of a KV group are row groups of 16, each of which reads the codes
+// (mostly from the L2: the groups of a head run at the same time), against an
+// expansion of twice the codes' bytes and a prefill that does not split the keys.
+// The groups win with few rows, and with more while they fill the GPU about once.
+// Of the GPU's time, int8, up to K keys a sequence, groups and expansion (us):
+//   D 128, 24 rows: 2 sequences of 25744, 4 heads 41 and 584; 64 of 4096, 8 heads 193
+//     and 351; 64 rows: 58 and 560, 339 and 345
+//   D 128, 8 heads: 256 rows over 25744 (0.8 groups an SM) 205 and 379; 4 x 128 over
+//     8192 (1.7) 99 and 189, 4 x 256 (3.4) 182 and 146
+//   D 256, 8 heads: 48 rows over 300 keys 23 and 21; 96 over 2000 (0.3) 36 and 41; 128
+//     over 25744 (0.4) 258 and 370, 256 (0.8) 480 and 367
+bool q8_decode_wins(const AttnParams &p, int nsm) {
+    const int rows = p.Q * p.G;
+    const long long all = (long long)p.B * p.Hkv * groups_of(p);
+    if (p.D <= 128 && p.Dv <= 128) return rows <= 64 || all <= 2LL * nsm;
+    return rows <= 32 || (2 * all <= nsm && p.K >= 1024);
+}
+
 unsigned long long q8_decode_workspace(const AttnParams &p, int nsm) {
     if (cluster_of(p, nsm)) return 0;
     const unsigned long long shares = shares_of(p, nsm);
-    const unsigned long long rows = 2 * shares * p.Hkv * (p.Q * p.G <= 8 ? 8 : 16);
+    const unsigned long long rows = 2 * shares * p.Hkv * groups_of(p) * (p.Q * p.G <= 8 ? 8 : 16);
     return shares * sizeof(int4) + rows * 4 * (p.Dv + 1ull);
 }
 
@@ -1077,9 +1108,10 @@ int launch_q8_decode(const AttnParams &p, const Q8Cache &c, int dtype, int nsm, 
     while ((1 << a.box_shift) < a.box_rows) ++a.box_shift;
     a.cluster = cluster_of(p, nsm);
     a.shares = shares_of(p, nsm);
+    a.groups = groups_of(p);
     a.seam = static_cast<int4 *>(ws);
     a.part_o = reinterpret_cast<float *>(a.seam + a.shares);
-    a.part_lse = a.part_o + 2ull * a.shares * p.Hkv * (p.Q * p.G <= 8 ? 8 : 16) * p.Dv;
+    a.part_lse = a.part_o + 2ull * a.shares * p.Hkv * a.groups * (p.Q * p.G <= 8 ? 8 : 16) * p.Dv;
     return c.code == kCodeE4m3 ? launch_code<kCodeE4m3>(a, stream)
                                : launch_code<kCodeInt8>(a, stream);
 }

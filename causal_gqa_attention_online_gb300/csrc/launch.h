@@ -124,6 +124,7 @@ int launch_q8_expand(const AttnParams &p, const Q8Cache &c, void *k_out, void *v
 // multiples of 16 up to 256, pages of 8 rows or more), with a workspace of the
 // given number of bytes at a 16-byte aligned address.
 bool q8_decode_supported(const AttnParams &p, int dtype);
+bool q8_decode_wins(const AttnParams &p, int nsm);
 unsigned long long q8_decode_workspace(const AttnParams &p, int nsm);
 int launch_q8_decode(const AttnParams &p, const Q8Cache &c, int dtype, int nsm, void *ws,
                      cudaStream_t stream);

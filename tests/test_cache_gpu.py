@@ -302,6 +302,42 @@ def test_attention_of_small_problems(i):
                     max_pages=M, algo="decode")
 
 
+ROWS = [
+    # dtype, kind, Hq, Hkv, Q, D, Dv, lens, page, block, options: row groups of 16
+    ("bf16", "e4m3", 17, 1, 1, 128, 128, [700, 0, 1, 129], 64, 64, {}),
+    ("f16", "int8", 16, 2, 3, 64, 64, [2053, 2, 500], 128, 32, {}),              # 24 rows
+    ("bf16", "int8", 32, 4, 4, 128, 128, [300, 7000, 64], 64, 16, {}),           # 32
+    ("bf16", "e4m3", 6, 2, 11, 96, 80, [900, 10, 333], 64, 64, {}),              # 33: a group of one row
+    ("f16", "e4m3", 12, 4, 16, 256, 256, [400, 16], 32, 8, {}),                  # 48
+    ("bf16", "int8", 8, 1, 8, 64, 128, [3000, 5], 64, 64, dict(window=200)),     # 64
+    ("bf16", "e4m3", 8, 2, 9, 128, 128, [300, 2, 0, 9], 16, 16, dict(mask="causal_top_left")),
+    ("bf16", "int8", 8, 2, 9, 128, 128, [300, 2, 0, 9], 16, 16, dict(mask="none")),
+    ("f16", "int8", 8, 2, 40, 64, 64, [900, 100, 5], 64, 64, dict(window=1)),
+    ("bf16", "e4m3", 8, 2, 20, 128, 128, [700, 33, 20, 90], 64, 64, dict(sq=[3, 0, 20, 17])),
+    ("f16", "e4m3", 4, 1, 250, 64, 64, [1000, 3], 64, 32, {}),                   # 1000
+    ("bf16", "int8", 4, 1, 256, 80, 80, [256, 2000, 0], 128, 128, dict(window=100)),
+    ("bf16", "int8", 40, 20, 9, 128, 128, [300, 500, 41, 77, 1, 0, 64] * 3, 64, 64, {}),
+    ("bf16", "int8", 36, 36, 30, 64, 64, [30, 600, 0, 64] * 2, 64, 64, {}),       # 72 groups
+]
+
+
+@pytest.mark.parametrize("i", range(len(ROWS)))
+def test_attention_of_many_rows_over_the_codes(i):
+    dtype, kind, Hq, Hkv, Q, D, Dv, lens, page, block, kw = ROWS[i]
+    check_attention(np.random.default_rng(900 + i), dtype, kind, len(lens), Hq, Hkv, Q, D, Dv,
+                    lens, page, block, algo="decode", **kw)
+
+
+@pytest.mark.parametrize("algo", ["tcgen05", "mma"])
+@pytest.mark.parametrize("i", [i for i, c in enumerate(ATTEND) if c[4] >= 20])
+def test_attention_of_many_rows_over_expanded_keys(i, algo):
+    dtype, kind, Hq, Hkv, Q, D, Dv, lens, page, block, kw = ATTEND[i]
+    if algo == "mma" and D > 128:
+        pytest.skip("wider than the kernel takes")
+    check_attention(np.random.default_rng(950 + i), dtype, kind, len(lens), Hq, Hkv, Q, D, Dv,
+                    lens, page, block, algo=algo, **kw)
+
+
 # -------------------------------------------------------------------- append
 
 def run_append(g, dtype, kind, lens, new, N, Hkv, D, Dv, page, block, packed=False, extra_pages=0,

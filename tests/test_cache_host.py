@@ -111,7 +111,7 @@ def test_attention_refuses(lib, kw, needle):
 
 
 @pytest.mark.parametrize("kw", [dict(D=40), dict(Dv=8), dict(D=272, Dv=272), dict(page=4, block=4),
-                                dict(Q=9), dict(dtype=0)])
+                                dict(Q=513), dict(dtype=0)])
 def test_decode_kernel_refuses_what_it_does_not_take(lib, kw):
     assert _fwd(lib, algo=3, **kw) == 2
     assert "8-bit decode kernel" in lib.attn_last_error().decode()
