@@ -242,12 +242,21 @@ __global__ void __launch_bounds__(kThreads, resident(DP, NT))
     const AttnParams &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, tig = lane & 3;
-    // shares: CTA (share, head, row group); clusters: (sequence, head, row group, rank)
-    const int C = a.cluster;
-    const int xi = C ? blockIdx.x / C : blockIdx.x, vheads = p.Hkv * a.groups;
-    const int share_i = xi / vheads, head_i = xi - share_i * vheads;
-    const int kvh = head_i / a.groups, row0 = (head_i - kvh * a.groups) * R;
-    const int rank = C ? blockIdx.x - xi * C : 0;
+    // shares: CTA (share: y; head, row group: x); clusters: (sequence, head, row
+    // group, rank).  (A division by what the host chose costs the prologue 0.3 us.)
+    const int C = a.cluster, vheads = p.Hkv * a.groups;
+    int share_i = blockIdx.y, head_i = blockIdx.x;
+    if (C) {
+        head_i /= C;
+        share_i = head_i / vheads;
+        head_i -= share_i * vheads;
+    }
+    int kvh = head_i, row0 = 0;
+    if (a.groups > 1) {
+        kvh /= a.groups;
+        row0 = (head_i - kvh * a.groups) * R;
+    }
+    const int rank = C ? blockIdx.x % C : 0;
     const uint32_t sbase = smem_u32(smem);
     const uint32_t full = sbase + L::BARS, empty = full + 8 * NS;
     long long *share = reinterpret_cast<long long *>(smem + L::SHARE);
@@ -325,8 +334,8 @@ __global__ void __launch_bounds__(kThreads, resident(DP, NT))
     } else if (C == 0) {
         // meanwhile: the rows of sequences without keys, +0 and -inf (each lane
         // looks at one of the CTA's sequences and heads, the warp writes)
-        const uint32_t units = (uint32_t)p.B * p.Hkv, step = gridDim.x;
-        for (uint64_t x0 = blockIdx.x + (uint64_t)warp * 32 * step; x0 < units; x0 += 128ull * step) {
+        const uint32_t units = (uint32_t)p.B * p.Hkv, step = gridDim.x * gridDim.y;
+        for (uint64_t x0 = blockIdx.y * gridDim.x + blockIdx.x + (uint64_t)warp * 32 * step; x0 < units; x0 += 128ull * step) {
             const uint64_t x = x0 + (uint64_t)lane * step;
             const uint32_t b = x < units ? (uint32_t)x / (uint32_t)p.Hkv : 0u;
             unsigned todo = __ballot_sync(0xffffffffu, x < units && unit_of(a, b).ntiles == 0);
@@ -775,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, resident(DP, NT))
         // or its last.
         if (warp == 0) {
             const bool whole = n == un.ntiles && C <= 1;
-            const long long slot = 2LL * blockIdx.x + (first_seg ? 0 : 1);
+            const long long slot = 2LL * (blockIdx.y * gridDim.x + blockIdx.x) + (first_seg ? 0 : 1);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -854,12 +863,14 @@ __global__ void __launch_bounds__(kMergeThreads) q8_merge_kernel(const __grid_co
     const int4 seam = __ldcg(a.seam + at_share);
     if (seam.x < 0) return;
     const int np = seam.z - seam.y + 1;
+    // the row's group and place in it (R is 8, of one group, or 16)
+    const int head_i = kvh * a.groups + (a.groups > 1 ? row >> 4 : 0), r = a.groups > 1 ? row & 15 : row;
     const int C4 = p.Dv / 4, ngrp = kMergeThreads / C4, grp = tid / C4, c = tid - grp * C4;
     // the first share's last partial (unless it begins with the sequence), the
     // others' first
     auto part = [&](int i) -> long long {
-        const long long cta = ((long long)(seam.y + i) * p.Hkv + kvh) * a.groups + row / R;
-        return (2 * cta + (i == 0 ? seam.w : 0)) * R + row % R;
+        const long long cta = (long long)(seam.y + i) * (p.Hkv * a.groups) + head_i;
+        return (2 * cta + (i == 0 ? seam.w : 0)) * R + r;
     };
     // a running maximum a thread, four partials loaded at a time
     float mx = -INFINITY, sum = 0.f;
@@ -974,7 +985,8 @@ int launch_t(const Q8Args &a, cudaStream_t stream) {
         return 3;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((a.cluster ? a.p.B * a.cluster : a.shares) * a.p.Hkv * a.groups));
+    const unsigned heads = (unsigned)(a.p.Hkv * a.groups);
+    cfg.gridDim = a.cluster ? dim3(a.p.B * a.cluster * heads) : dim3(heads, a.shares);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = L::SMEM;
     cfg.stream = stream;
