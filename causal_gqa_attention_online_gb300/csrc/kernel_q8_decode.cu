@@ -230,7 +230,9 @@ __device__ __noinline__ void join_cluster(const Q8Args &a, int b, int kvh, int r
     }
 }
 
-template <int CODE, int DP, int NT>
+// GROUPED: a KV head's rows are more than one group (a form of its own: the group's
+// first row, carried along, costs the others 1 us of 36).
+template <int CODE, int DP, int NT, bool GROUPED>
 __global__ void __launch_bounds__(kThreads, resident(DP, NT))
     q8_decode_kernel(const __grid_constant__ Q8Args a, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV) {
@@ -252,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, resident(DP, NT))
         head_i -= share_i * vheads;
     }
     int kvh = head_i, row0 = 0;
-    if (a.groups > 1) {
+    if (GROUPED) {
         kvh /= a.groups;
         row0 = (head_i - kvh * a.groups) * R;
     }
@@ -970,7 +972,7 @@ int pool_map(CUtensorMap *map, const void *ptr, int D, int Hkv, uint64_t rows, i
     return 0;
 }
 
-template <int CODE, int DP, int NT>
+template <int CODE, int DP, int NT, bool GROUPED>
 int launch_t(const Q8Args &a, cudaStream_t stream) {
     using L = Ring<DP, NT>;
     CUtensorMap tk, tv;
@@ -978,7 +980,7 @@ int launch_t(const Q8Args &a, cudaStream_t stream) {
     int rc = pool_map(&tk, a.c.k, a.p.D, a.p.Hkv, rows, L::HALF, a.box_rows);
     if (rc == 0) rc = pool_map(&tv, a.c.v, a.p.Dv, a.p.Hkv, rows, L::HALF, a.box_rows);
     if (rc) return rc;
-    auto kern = q8_decode_kernel<CODE, DP, NT>;
+    auto kern = q8_decode_kernel<CODE, DP, NT, GROUPED>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
     if (e != cudaSuccess) {
         set_error("8-bit decode kernel: cudaFuncSetAttribute: %s", cudaGetErrorString(e));
@@ -1026,8 +1028,9 @@ int launch_t(const Q8Args &a, cudaStream_t stream) {
 }
 
 template <int CODE, int DP> int launch_nt(const Q8Args &a, cudaStream_t stream) {
-    return a.p.Q * a.p.G <= 8 ? launch_t<CODE, DP, 1>(a, stream)
-                              : launch_t<CODE, DP, 2>(a, stream);
+    if (a.groups > 1) return launch_t<CODE, DP, 2, true>(a, stream);
+    return a.p.Q * a.p.G <= 8 ? launch_t<CODE, DP, 1, false>(a, stream)
+                              : launch_t<CODE, DP, 2, false>(a, stream);
 }
 
 template <int CODE> int launch_code(const Q8Args &a, cudaStream_t stream) {
