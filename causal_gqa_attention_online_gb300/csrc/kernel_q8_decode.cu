@@ -337,7 +337,8 @@ __global__ void __launch_bounds__(kThreads, resident(DP, NT))
         // meanwhile: the rows of sequences without keys, +0 and -inf (each lane
         // looks at one of the CTA's sequences and heads, the warp writes)
         const uint32_t units = (uint32_t)p.B * p.Hkv, step = gridDim.x * gridDim.y;
-        for (uint64_t x0 = blockIdx.y * gridDim.x + blockIdx.x + (uint64_t)warp * 32 * step; x0 < units; x0 += 128ull * step) {
+        const uint32_t cta = blockIdx.y * gridDim.x + blockIdx.x;
+        for (uint64_t x0 = cta + (uint64_t)warp * 32 * step; x0 < units; x0 += 128ull * step) {
             const uint64_t x = x0 + (uint64_t)lane * step;
             const uint32_t b = x < units ? (uint32_t)x / (uint32_t)p.Hkv : 0u;
             unsigned todo = __ballot_sync(0xffffffffu, x < units && unit_of(a, b).ntiles == 0);
