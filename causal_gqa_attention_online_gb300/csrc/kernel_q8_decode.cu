@@ -16,9 +16,10 @@
 //   softmax scale; its sign goes to Q), so that bf16's 8 bits stay exact down to
 //   2^-29 of the row's largest element.
 // * Probabilities are in (0, 2^14]: f16's 11 bits down to 2^-28 of the largest,
-//   steps of 2^-38 below.  u is the largest value scale a warp has seen, so
-//   p * vs / u stays in range; O is rescaled when m or u grow.  The 2^14 cancels
-//   against the row sum, u comes back in the final normalisation.
+//   steps of 2^-38 below.  u is the largest value scale a warp has seen, and 2^-126
+//   at the least (the reciprocal of less is no fp32 number), so p * vs / u stays in
+//   range; O is rescaled when m or u grow.  The 2^14 cancels against the row sum, u
+//   comes back in the final normalisation.
 // * Which bytes pair up is chosen so that no byte is moved across lanes: the two
 //   pairs of a 32-bit word are the two halves of a k16 step (K: Q's columns are
 //   permuted to match) or the rows dv = 2g and 2g + 1 (V: a transposed ldmatrix of
@@ -77,6 +78,7 @@ namespace {
 constexpr int kTile = 128;  // keys a tile: 4 warps x 32
 constexpr int kThreads = 160;
 constexpr float kPOff = 14.f;  // p is scaled by 2^14
+constexpr float kLeastUnit = 1.17549435e-38f;  // 2^-126
 constexpr int kMaxRows = 1024;  // rows of a KV group at most
 
 struct Q8Args {
@@ -516,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, resident(DP, NT))
         // Legal keys of the two rows (per n-tile) this thread's columns hold, and
         // of all rows.
         int rlo[NT][2], rhi[NT][2];
-        float m[NT][2], l[NT][2], u = 0.f;  // m: the largest x
+        float m[NT][2], l[NT][2], u = kLeastUnit;  // m: the largest x
         float oacc[DP / 16][NT][4];
         int lo_all = 0, hi_all = INT_MAX;
 #pragma unroll
@@ -582,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, resident(DP, NT))
             uint32_t ub = __float_as_uint(sc[kTile + lane]) & 0x7fffffffu;
             if (ub >= 0x7f800000u || (EDGE && !(uk >= un.klo && uk < un.kend))) ub = 0u;
             const float unew = fmaxf(u, __uint_as_float(__reduce_max_sync(0xffffffffu, ub)));
-            const float inv_u = unew > 0.f ? 1.f / unew : 0.f;
+            const float inv_u = 1.f / unew;
 
             float kscale[4], vw[4];  // keys g, g + 8, g + 16, g + 24
 #pragma unroll
@@ -727,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, resident(DP, NT))
         ok = sm100::bar_red_and(1, 128, ok);
         if (!ok) break;
         const float U = fmaxf(fmaxf(stat_u[0], stat_u[1]), fmaxf(stat_u[2], stat_u[3]));
-        const float to_u = U > 0.f ? u / U : 1.f;
+        const float to_u = u / U;
         float M[NT][2], Lsum[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)

@@ -1,0 +1,146 @@
+"""Attention over the 8-bit cache where its numbers are at their ends -- value
+scales of any size, scales and codes that are no numbers -- on every path of the
+kernel that reads the codes, against the definition in 64 bits."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import causal_gqa_attention_online_gb300 as attn
+from tests import cache_ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+DT = {"bf16": torch.bfloat16, "f16": torch.float16}
+HALF = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11}      # half a step of the type, relative
+LEAST = {"bf16": 2.0 ** -134, "f16": 2.0 ** -25}   # half of its smallest step
+PAGE, D = 64, 64
+
+# one cluster a sequence and head; shares of a long sequence that a merge joins; many
+# sequences a share, whole and cut; the same with row groups of 16
+PATHS = {
+    "cluster": dict(lens=[500, 129], Q=1, Hq=4, Hkv=2),
+    "merge": dict(lens=[20000, 300], Q=1, Hq=4, Hkv=2),
+    "whole": dict(lens=[700, 0, 65] + [100 + 9 * i for i in range(57)], Q=1, Hq=8, Hkv=4),
+    "groups": dict(lens=[500, 129], Q=12, Hq=4, Hkv=2),
+    "groups merge": dict(lens=[9000, 77], Q=12, Hq=4, Hkv=2),
+}
+
+
+def i32(x):
+    return torch.as_tensor(np.asarray(x), dtype=torch.int32, device=DEV)
+
+
+class Problem:
+    """Random codes in shuffled pages, scales that a test may change, random queries."""
+
+    def __init__(self, g, path, block=32, kind="int8", dtype="bf16", window=0, **more):
+        self.__dict__.update({**PATHS[path], **more})
+        self.kind, self.dtype, self.window, self.block = kind, dtype, window, block
+        need = [-(-n // PAGE) for n in self.lens]
+        P = sum(need) + 2
+        order = iter(g.permutation(P))
+        self.table = np.full((len(self.lens), max(need)), -1, np.int32)
+        for b, n in enumerate(need):
+            for j in range(n):
+                self.table[b, j] = next(order)
+        self.codes = [g.integers(0, 256, (P, PAGE, self.Hkv, D), dtype=np.uint8) for _ in "kv"]
+        for c in self.codes:
+            c[(c == 128) if kind == "int8" else (c & 127) == 127] = 1
+        s = 2.0 ** g.integers(-8, -5, (2, P, PAGE // block, self.Hkv))
+        self.scales = list((s if kind == "int8" else s / 4).astype(np.float32))
+        q = g.standard_normal((len(self.lens), self.Q, self.Hq, D)).astype(np.float32)
+        self.q = torch.from_numpy(q).to(DT[dtype])
+
+    def at(self, b, j):
+        """Index of key j of sequence b among the pages' rows, and among their blocks."""
+        pg = int(self.table[b, j // PAGE])
+        return (pg, j % PAGE), (pg, j % PAGE // self.block)
+
+    def run(self, **kw):
+        t = cache_ref.TORCH_CODE[self.kind]
+        pages = [torch.from_numpy(c.copy()).to(DEV).view(t) for c in self.codes]
+        scales = [torch.from_numpy(s.copy()).to(DEV) for s in self.scales]
+        kw.setdefault("algo", "decode")
+        o, lse = attn.attn_fwd_paged_q8(self.q.to(DEV), *pages, *scales, i32(self.table),
+                                        i32(self.lens), window=self.window, **kw)
+        torch.cuda.synchronize()
+        return o.double().cpu().numpy(), lse.double().cpu().numpy()
+
+    def keys(self, b, i):
+        """The keys that row i of sequence b attends to, [lo, hi)."""
+        n = self.lens[b]
+        hi = max(0, n - self.Q + i + 1)
+        return (max(0, hi - self.window) if self.window else 0), hi
+
+    def exact(self):
+        """(o, lse, how far o and lse may be off).
+
+        Over the keys a row attends to, with p relative to its largest and w = p times
+        the value's scale: a score's fp32 accumulation is off by at most (D + 8) 2^-24 of
+        scale * sum |q||k|, which moves p by twice that relative to it; sums over n keys
+        are off by n 2^-24 each, ex2 by 2^-22; w is rounded to fp16 under the row's own
+        power, so that its largest is at least 2^13 -- by 2^-11 of itself, or by 2^-25 of
+        2^-13 of the largest -- and to fp32 before that (2^-150 at the least); o once at
+        the end."""
+        B, Q, Hq, G = len(self.lens), self.Q, self.Hq, self.Hq // self.Hkv
+        codes = [cache_ref.code_values(c, self.kind) for c in self.codes]
+        q = self.q.double().numpy()
+        o = np.zeros((B, Q, Hq, D))
+        lse = np.full((B, Q, Hq), -math.inf)
+        to, tl = np.zeros(o.shape), np.zeros(lse.shape)
+        for b in range(B):
+            n = self.lens[b]
+            if not n:
+                continue
+            pg, r = self.table[b, np.arange(n) // PAGE], np.arange(n) % PAGE
+            kc, vc = (c[pg, r] for c in codes)
+            ks, vs = (s.astype(np.float64)[pg, r // self.block] for s in self.scales)
+            for h in range(Hq):
+                k, sv, cv = kc[:, h // G] * ks[:, h // G, None], vs[:, h // G], vc[:, h // G]
+                for i in range(Q):
+                    lo, hi = self.keys(b, i)
+                    if lo >= hi:
+                        continue
+                    s = k[lo:hi] @ q[b, i, h] / math.sqrt(D)
+                    big = np.max(np.abs(k[lo:hi]) @ np.abs(q[b, i, h])) / math.sqrt(D)
+                    m = s.max()
+                    p = np.exp(s - m)
+                    w, c = p * sv[lo:hi], cv[lo:hi]
+                    total = p.sum()
+                    o[b, i, h] = w @ c / total
+                    lse[b, i, h] = m + math.log(total)
+                    ds = (D + 8) * 2.0 ** -24 * big
+                    rel = 2 * ds + 2 * (hi - lo) * 2.0 ** -24 + 2.0 ** -20
+                    small = np.abs(c).sum(0) * (2.0 ** -38 * w.max() + 2.0 ** -150)
+                    to[b, i, h] = ((2.0 ** -11 + rel) * (w @ np.abs(c)) + small) / total
+                    tl[b, i, h] = ds + (hi - lo) * 2.0 ** -24 + 2.0 ** -20 + 2.0 ** -22 * abs(lse[b, i, h])
+        to += HALF[self.dtype] * (np.abs(o) + to) + LEAST[self.dtype]
+        return o, lse, to, tl
+
+    def check(self, **kw):
+        o, lse = self.run(**kw)
+        ro, rl, to, tl = self.exact()
+        empty = rl == -math.inf
+        assert np.isfinite(o).all() and np.isfinite(lse[~empty]).all()
+        assert (o[empty] == 0).all() and (lse[empty] == -math.inf).all()
+        eo, el = np.abs(o - ro)[~empty] / to[~empty], np.abs(lse[~empty] - rl[~empty]) / tl[~empty]
+        assert eo.max() <= 1, f"o off by {eo.max():.3g} of the bound"
+        assert el.max() <= 1, f"lse off by {el.max():.3g} of the bound"
+        return o, lse
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("small", [2.0 ** -149, 2.6e-41, 2.0 ** -127, 0.0])
+@pytest.mark.parametrize("mixed", [False, True])
+def test_value_scales_next_to_zero(path, small, mixed):
+    """Scales whose reciprocal is no fp32 number: everywhere, or in the first half of
+    each sequence (what every warp meets first) and here and there behind it."""
+    g = np.random.default_rng(1)
+    x = Problem(g, path)
+    for b, n in enumerate(x.lens):
+        for j in range(0, n, x.block):
+            if not mixed or j < n // 2 or g.random() < 0.3:
+                x.scales[1][x.at(b, j)[1]] = small
+    x.check()
