@@ -144,3 +144,25 @@ def test_value_scales_next_to_zero(path, small, mixed):
             if not mixed or j < n // 2 or g.random() < 0.3:
                 x.scales[1][x.at(b, j)[1]] = small
     x.check()
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("which", ["key", "value"])
+def test_scales_that_are_no_numbers_poison_the_rows_that_attend(path, bad, which):
+    """One block of one head: every row of its heads is not finite, across the merge of
+    shares and the joins of a cluster too, and all others have the bits they had."""
+    g = np.random.default_rng(2)
+    x = Problem(g, path)
+    before = x.run()
+    x.scales[which == "value"][x.at(0, 40)[1] + (1,)] = bad
+    o, lse = x.run()
+    G = x.Hq // x.Hkv
+    hit = np.zeros(lse.shape, bool)
+    hit[0, :, G:2 * G] = True
+    assert not np.isfinite(o[hit]).any()
+    if which == "value":
+        assert np.array_equal(lse[hit], before[1][hit])
+    elif math.isnan(bad):
+        assert np.isnan(lse[hit]).all()
+    assert np.array_equal(o[~hit], before[0][~hit]) and np.array_equal(lse[~hit], before[1][~hit])
