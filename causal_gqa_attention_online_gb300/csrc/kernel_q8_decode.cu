@@ -15,11 +15,16 @@
 // * Q rows are brought to [2^14, 2^15) by a power of two (in f[row], with the
 //   softmax scale; its sign goes to Q), so that bf16's 8 bits stay exact down to
 //   2^-29 of the row's largest element.
-// * Probabilities are in (0, 2^14]: f16's 11 bits down to 2^-28 of the largest,
-//   steps of 2^-38 below.  u is the largest value scale a warp has seen, and 2^-126
-//   at the least (the reciprocal of less is no fp32 number), so p * vs / u stays in
-//   range; O is rescaled when m or u grow.  The 2^14 cancels against the row sum, u
-//   comes back in the final normalisation.
+// * Probabilities are in (0, 2^14], times vs / u in f16, where u is the largest value
+//   scale a warp has seen (2^-112 at the least: its reciprocal times 2^14 is an fp32
+//   number): 11 bits down to 2^-28 of p = 2^14 and vs = u, steps of 2^-38 below.  O is
+//   rescaled when m or u grow.  The 2^14 cancels against the row sum, u comes back in the
+//   final normalisation.
+// * That serves every row while the scales seen lie within a factor of 64 (kSpread): a
+//   row's largest weight p * vs is then 2^8 or more, whichever keys it attends to.  A warp
+//   that meets a wider spread does the rest of the sequence with a unit for each row,
+//   which brings the step's largest weight of the row to [2^13, 2^14) (own_steps): a large
+//   scale on a key that a row does not attend to, or that hardly counts, costs it nothing.
 // * Which bytes pair up is chosen so that no byte is moved across lanes: the two
 //   pairs of a 32-bit word are the two halves of a k16 step (K: Q's columns are
 //   permuted to match) or the rows dv = 2g and 2g + 1 (V: a transposed ldmatrix of
@@ -63,7 +68,6 @@
 
 #include <cooperative_groups.h>
 #include <cstring>
-#include <type_traits>
 
 #include "common.cuh"
 #include "launch.h"
@@ -78,7 +82,10 @@ namespace {
 constexpr int kTile = 128;  // keys a tile: 4 warps x 32
 constexpr int kThreads = 160;
 constexpr float kPOff = 14.f;  // p is scaled by 2^14
-constexpr float kLeastUnit = 1.17549435e-38f;  // 2^-126
+constexpr float kLeastUnit = 1.92592994e-34f;  // 2^-112
+// Value scales under one unit lie within this factor.  64 sequences of up to 8192 keys, D
+// 128: 98 us, and 137 with scales spread over 2^24, where every row has its unit.
+constexpr float kSpread = 64.f;
 constexpr int kMaxRows = 1024;  // rows of a KV group at most
 
 struct Q8Args {
@@ -113,8 +120,8 @@ template <int DP, int NT> struct Ring {
     static constexpr int MC = DP == 64 ? 64 : DP / NT;
     static constexpr int PITCH = MC + 4;
     static constexpr int MERGE = NS * STAGE;
-    static constexpr int STATS = MERGE + 2 * R * PITCH * 4;  // m, l [4][R], u [4]
-    static constexpr int BARS = STATS + (2 * 4 * R + 4) * 4;
+    static constexpr int STATS = MERGE + 2 * R * PITCH * 4;  // m, l, u [4][R]
+    static constexpr int BARS = STATS + 3 * 4 * R * 4;
     static constexpr int SHARE = BARS + 16 * NS;  // {left, sequence, tile}, abort flag
     static constexpr int SMEM = SHARE + 32;
     // (an SM has 228 KB, a CTA takes 1 KB more than its own)
@@ -230,6 +237,252 @@ __device__ __noinline__ void join_cluster(const Q8Args &a, int b, int kvh, int r
         }
         put_row(a, b, kvh, row0 + row, c, acc, sum, mx);
     }
+}
+
+// 2^x as a float, -126 <= x <= 127.
+__device__ __forceinline__ float pow2(int x) { return __uint_as_float((uint32_t)(127 + x) << 23); }
+
+// The unit of a row for a step whose largest weight (p at most 1) is w, and the factor
+// that brings O, whose elements are o at most, to it: w * 2^14 in [2^13, 2^14), but for
+// weights so far below what O may hold that it would pass 2^100.
+__device__ __forceinline__ float own_unit(float w, float o, float &unit) {
+    const int ew = min(max((int)(__float_as_uint(w) >> 23) - 127, -113), 125);
+    const int eo = min(max((int)(__float_as_uint(o) >> 23) - 127, -27), 127);
+    const float next = pow2(-1 - ew), f = next / unit, most = pow2(99 - eo);
+    if (f <= most) {
+        unit = next;
+        return f;
+    }
+    unit *= most;
+    return most;
+}
+
+// What a warp holds of a sequence.  A thread's columns of S^T and O^T are rows 2 tig and
+// 2 tig + 1 of each eight.
+template <int DP, int NT> struct Rows {
+    uint32_t q[DP / 16][NT][2];  // Q^T fragments
+    float f[NT][2];              // x to log2 units
+    int lo[NT][2], hi[NT][2];    // legal keys
+    float m[NT][2], l[NT][2];    // the largest x; the sum of p
+    float o[DP / 16][NT][4];
+    float u, u_min;              // value scales seen: O's unit, and the least
+};
+
+// One step: the warp's 32 keys from key0 on, codes at ks and vs, scales at sc (values'
+// kTile behind).  EDGE: some row may not attend to all of them, and some may be outside
+// [klo, kend), where no row does.  OWN: rows have units of their own, with bounds of O; a
+// step without gives up, with nothing changed, where scales spread too far for one.
+template <int CODE, int DP, int NT, bool EDGE, bool OWN>
+__device__ __forceinline__ bool q8_step(Rows<DP, NT> &w, uint32_t ks, uint32_t vs, const float *sc, int kw0, int key0,
+                                        int klo, int kend, float (&unit)[NT][2], float (&bound)[NT][2]) {
+    using Op = CodeOps<CODE>;
+    const int lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
+    // S^T = K Q^T
+    float sacc[2][NT][4];
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sacc[mt][nt][j] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < DP / 16; kk += 2) {
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+            uint32_t r[4];
+            ldmatrix_x4(r, ks + chunk_at<DP>(kw0 + mt * 16 + (lane & 15), kk + (lane >> 4)));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t f[4];
+                Op::k_pairs(r[2 * h], f[0], f[2]);
+                Op::k_pairs(r[2 * h + 1], f[1], f[3]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    MmaOp<__half>::run(sacc[mt][nt], f, w.q[kk + h][nt][0], w.q[kk + h][nt][1]);
+            }
+        }
+    }
+
+    float unew = 1.f, least = 0.f, inv_u = 1.f;
+    if (!OWN) {
+        // the finite value scales so far, of keys some row attends to
+        const int uk = key0 + lane;
+        uint32_t ub = __float_as_uint(sc[kTile + lane]) & 0x7fffffffu;
+        const bool no = ub >= 0x7f800000u || (EDGE && !(uk >= klo && uk < kend));
+        unew = fmaxf(w.u, __uint_as_float(__reduce_max_sync(0xffffffffu, no ? 0u : ub)));
+        least = fminf(w.u_min, __uint_as_float(__reduce_min_sync(0xffffffffu, no ? 0x7f800000u : ub)));
+        inv_u = 1.f / unew;
+    }
+
+    float kscale[4], vw[4];  // keys g, g + 8, g + 16, g + 24
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        kscale[i] = sc[g + 8 * i];
+        vw[i] = sc[kTile + g + 8 * i] * inv_u;
+    }
+    float x[NT][2][4], mx[NT][2];
+    const bool spread = !OWN && unew > kSpread * least;
+    bool grew = OWN || unew > w.u || spread;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[nt][e][i] = sacc[i >> 1][nt][2 * (i & 1) + e] * kscale[i];
+                if (EDGE) {
+                    const int key = key0 + g + 8 * i;
+                    if (!(key >= w.lo[nt][e] && key < w.hi[nt][e])) x[nt][e][i] = -INFINITY;
+                }
+            }
+            float v = tcfwd::fmax3(x[nt][e][0], x[nt][e][1], fmaxf(x[nt][e][2], x[nt][e][3]));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+            v = tcfwd::fmax3(v, __shfl_xor_sync(0xffffffffu, v, 16), w.m[nt][e]);
+            mx[nt][e] = v;
+            grew |= v > w.m[nt][e];
+        }
+    float to[NT][2];  // (OWN) what O is multiplied by for its new unit
+    if (OWN) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float most = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (x[nt][e][i] != -INFINITY)
+                        most = fmaxf(most, fabsf(tcfwd::ex2((x[nt][e][i] - mx[nt][e]) * w.f[nt][e]) * vw[i]));
+#pragma unroll
+                for (int d = 4; d <= 16; d *= 2) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+                if (mx[nt][e] > w.m[nt][e])
+                    bound[nt][e] *= tcfwd::ex2((w.m[nt][e] - mx[nt][e]) * w.f[nt][e]);
+                to[nt][e] = own_unit(most, bound[nt][e], unit[nt][e]);
+                // (a step adds 32 weights of 2^15 times codes of 448 at most)
+                bound[nt][e] = bound[nt][e] * to[nt][e] + 0x1p29f;
+            }
+    }
+    if (__any_sync(0xffffffffu, grew)) {
+        if (spread) return false;
+        const float ru = unew > w.u ? w.u * inv_u : 1.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                // (no key yet: both -inf, and nothing to rescale)
+                const float alpha =
+                    mx[nt][e] > w.m[nt][e] ? tcfwd::ex2((w.m[nt][e] - mx[nt][e]) * w.f[nt][e]) : 1.f;
+                w.m[nt][e] = mx[nt][e];
+                w.l[nt][e] *= alpha;
+                const float f = alpha * (OWN ? to[nt][e] : ru);
+#pragma unroll
+                for (int mt = 0; mt < DP / 16; ++mt) {
+                    w.o[mt][nt][e] *= f;
+                    w.o[mt][nt][2 + e] *= f;
+                }
+            }
+        if (!OWN) w.u = unew;
+    }
+    if (!OWN) w.u_min = least;
+    uint32_t pb[2][NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        float pv[4][2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float ref = w.m[nt][e] == -INFINITY ? 0.f : kPOff - w.m[nt][e] * w.f[nt][e];
+            float pe[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) pe[i] = tcfwd::ex2(fmaf(x[nt][e][i], w.f[nt][e], ref));
+            w.l[nt][e] += (pe[0] + pe[1]) + (pe[2] + pe[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)  // (a scale that is no number counts only where its key does)
+                pv[i][e] = EDGE && x[nt][e][i] == -INFINITY ? 0.f : (OWN ? pe[i] * unit[nt][e] : pe[i]) * vw[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            pb[i >> 1][nt][i & 1] = movmatrix_trans(MmaOp<__half>::pack(pv[i][0], pv[i][1]));
+    }
+
+    // O^T += V^T P^T: rows g and g + 8 of a 16-column step are its columns
+    // 2 g and 2 g + 1
+    uint32_t vmask[2][2];
+    if (EDGE) {
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = key0 + kt * 16 + h * 8 + 2 * tig;
+                vmask[kt][h] = (k >= klo && k < kend ? 0xffffu : 0u) |
+                               (k + 1 >= klo && k + 1 < kend ? 0xffff0000u : 0u);
+            }
+    }
+#pragma unroll
+    for (int cc = 0; cc < DP / 16; cc += 2) {
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) {
+            uint32_t r[4];
+            ldmatrix_x4_trans(r, vs + chunk_at<DP>(kw0 + kt * 16 + (lane & 15), cc + (lane >> 4)));
+            if (EDGE) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) r[i] &= vmask[kt][i & 1];
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t f[4];
+                Op::even_odd(r[2 * h], f[0], f[1]);
+                Op::even_odd(r[2 * h + 1], f[2], f[3]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    MmaOp<__half>::run(w.o[cc + h][nt], f, pb[kt][nt][0], pb[kt][nt][1]);
+            }
+        }
+    }
+    return true;
+}
+
+// The rest of a sequence's tiles, [t, end), in stages from it on, with a unit for each row:
+// unit[] is what O is in at the end.  (A function of its own: its code would cost the
+// others' steps registers.)
+template <int CODE, int DP, int NT>
+__device__ __noinline__ bool own_steps(const Q8Args &a, Rows<DP, NT> &rows, float (&unit)[NT][2], uint8_t *smem,
+                                       int kbeg, int klo, int kend, int t, int end, uint32_t it) {
+    using L = Ring<DP, NT>;
+    constexpr int NS = L::NS;
+    const uint32_t sbase = smem_u32(smem), full = sbase + L::BARS, empty = full + 8 * NS;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::SHARE + 24);
+    const int kw0 = (threadIdx.x >> 5) * 32;
+    Rows<DP, NT> w = rows;
+    float bound[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            unit[nt][e] = 1.f / w.u;
+            bound[nt][e] = 0x1p55f;  // (of 2^31 keys)
+        }
+    bool ok = true;
+    for (; t < end; ++t, ++it) {
+        const uint32_t s = it % NS;
+        const bool got = sm100::mbar_wait(full + 8 * s, (it / NS) & 1u, abort_flag, a.p.wait_ns);
+        if (!__all_sync(0xffffffffu, got)) {
+            if ((threadIdx.x & 31) == 0) {
+                *abort_flag = 1;
+                report_status(a.p.status, kStatusTimeoutDecode);
+            }
+            ok = false;
+            break;
+        }
+        const int key0 = kbeg + t * kTile + kw0;
+        const uint32_t st = sbase + s * L::STAGE;
+        const float *sc = reinterpret_cast<const float *>(smem + s * L::STAGE + 2 * L::TILE) + kw0;
+        if (key0 < kend)
+            q8_step<CODE, DP, NT, true, true>(w, st, st + L::TILE, sc, kw0, key0, klo, kend, unit, bound);
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) sm100::mbar_arrive(empty + 8 * s);
+    }
+    rows = w;
+    return ok;
 }
 
 // GROUPED: a KV head's rows are more than one group (a form of its own: the group's
@@ -473,8 +726,7 @@ __global__ void __launch_bounds__(kThreads, resident(DP, NT))
         const int nvalid = un.si.Qb * G - row0;
         // Q^T fragments (B operand of S^T): column n = row g; in each 16 columns
         // lane tig holds columns 4 tig to 4 tig + 3, paired as the codes' bytes are.
-        uint32_t qf[DP / 16][NT][2];
-        float rowf[NT][2];
+        Rows<DP, NT> w;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int row = nt * 8 + g;
@@ -491,8 +743,8 @@ __global__ void __launch_bounds__(kThreads, resident(DP, NT))
                     if (kk * 16 < p.D) raw[kk] = __ldg(reinterpret_cast<const uint2 *>(src + kk * 16));
             }
             auto val = [&](int kk, int j) -> float {
-                const uint32_t w = j < 2 ? raw[kk].x : raw[kk].y;
-                const uint16_t hb = (uint16_t)(w >> (16 * (j & 1)));
+                const uint32_t two = j < 2 ? raw[kk].x : raw[kk].y;
+                const uint16_t hb = (uint16_t)(two >> (16 * (j & 1)));
                 return a.bf16 ? __uint_as_float((uint32_t)hb << 16) : __half2float(__ushort_as_half(hb));
             };
 #pragma unroll
@@ -509,17 +761,16 @@ __global__ void __launch_bounds__(kThreads, resident(DP, NT))
             constexpr int J1 = Op::kPerm ? 2 : 1, J2 = Op::kPerm ? 1 : 2;
 #pragma unroll
             for (int kk = 0; kk < DP / 16; ++kk) {
-                qf[kk][nt][0] = MmaOp<__half>::pack(val(kk, 0) * up, val(kk, J1) * up);
-                qf[kk][nt][1] = MmaOp<__half>::pack(val(kk, J2) * up, val(kk, 3) * up);
+                w.q[kk][nt][0] = MmaOp<__half>::pack(val(kk, 0) * up, val(kk, J1) * up);
+                w.q[kk][nt][1] = MmaOp<__half>::pack(val(kk, J2) * up, val(kk, 3) * up);
             }
-            rowf[nt][0] = __shfl_sync(0xffffffffu, f, 8 * tig);
-            rowf[nt][1] = __shfl_sync(0xffffffffu, f, 8 * tig + 4);
+            w.f[nt][0] = __shfl_sync(0xffffffffu, f, 8 * tig);
+            w.f[nt][1] = __shfl_sync(0xffffffffu, f, 8 * tig + 4);
         }
         // Legal keys of the two rows (per n-tile) this thread's columns hold, and
         // of all rows.
-        int rlo[NT][2], rhi[NT][2];
-        float m[NT][2], l[NT][2], u = kLeastUnit;  // m: the largest x
-        float oacc[DP / 16][NT][4];
+        w.u = kLeastUnit;
+        w.u_min = INFINITY;
         int lo_all = 0, hi_all = INT_MAX;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -528,14 +779,14 @@ __global__ void __launch_bounds__(kThreads, resident(DP, NT))
                 const int row = nt * 8 + 2 * tig + e;
                 int lo = 0, hi = 0;
                 if (row < nvalid) legal_range((row0 + row) / G, un.si.Qb, un.si.Kb, p.window, p.mask, lo, hi);
-                rlo[nt][e] = lo;
-                rhi[nt][e] = hi;
+                w.lo[nt][e] = lo;
+                w.hi[nt][e] = hi;
                 if (row < nrows) {
                     lo_all = max(lo_all, lo);
                     hi_all = min(hi_all, hi);
                 }
-                m[nt][e] = -INFINITY;
-                l[nt][e] = 0.f;
+                w.m[nt][e] = -INFINITY;
+                w.l[nt][e] = 0.f;
             }
         lo_all = __reduce_max_sync(0xffffffffu, lo_all);
         hi_all = __reduce_min_sync(0xffffffffu, hi_all);
@@ -544,151 +795,10 @@ __global__ void __launch_bounds__(kThreads, resident(DP, NT))
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) oacc[mt][nt][j] = 0.f;
+                for (int j = 0; j < 4; ++j) w.o[mt][nt][j] = 0.f;
 
-        // One step: the warp's 32 keys from key0 on, in stage s.  EDGE: some row may
-        // not attend to all of them.
-        auto step = [&](auto edge, int key0, uint32_t s) {
-            constexpr bool EDGE = decltype(edge)::value;
-            const uint32_t ks = sbase + s * L::STAGE, vs = ks + L::TILE;
-            const float *sc = reinterpret_cast<const float *>(smem + s * L::STAGE + 2 * L::TILE) + kw0;
-
-            // S^T = K Q^T
-            float sacc[2][NT][4];
-#pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) sacc[mt][nt][j] = 0.f;
-#pragma unroll
-            for (int kk = 0; kk < DP / 16; kk += 2) {
-#pragma unroll
-                for (int mt = 0; mt < 2; ++mt) {
-                    uint32_t r[4];
-                    ldmatrix_x4(r, ks + chunk_at<DP>(kw0 + mt * 16 + (lane & 15), kk + (lane >> 4)));
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t f[4];
-                        Op::k_pairs(r[2 * h], f[0], f[2]);
-                        Op::k_pairs(r[2 * h + 1], f[1], f[3]);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            MmaOp<__half>::run(sacc[mt][nt], f, qf[kk + h][nt][0], qf[kk + h][nt][1]);
-                    }
-                }
-            }
-
-            // the largest finite value scale so far, of keys some row attends to
-            const int uk = key0 + lane;
-            uint32_t ub = __float_as_uint(sc[kTile + lane]) & 0x7fffffffu;
-            if (ub >= 0x7f800000u || (EDGE && !(uk >= un.klo && uk < un.kend))) ub = 0u;
-            const float unew = fmaxf(u, __uint_as_float(__reduce_max_sync(0xffffffffu, ub)));
-            const float inv_u = 1.f / unew;
-
-            float kscale[4], vw[4];  // keys g, g + 8, g + 16, g + 24
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                kscale[i] = sc[g + 8 * i];
-                vw[i] = sc[kTile + g + 8 * i] * inv_u;
-            }
-            float x[NT][2][4], mx[NT][2];
-            bool grew = unew > u;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        x[nt][e][i] = sacc[i >> 1][nt][2 * (i & 1) + e] * kscale[i];
-                        if (EDGE) {
-                            const int key = key0 + g + 8 * i;
-                            if (!(key >= rlo[nt][e] && key < rhi[nt][e])) x[nt][e][i] = -INFINITY;
-                        }
-                    }
-                    float v = tcfwd::fmax3(x[nt][e][0], x[nt][e][1], fmaxf(x[nt][e][2], x[nt][e][3]));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-                    v = tcfwd::fmax3(v, __shfl_xor_sync(0xffffffffu, v, 16), m[nt][e]);
-                    mx[nt][e] = v;
-                    grew |= v > m[nt][e];
-                }
-            if (__any_sync(0xffffffffu, grew)) {
-                const float ru = unew > u ? u * inv_u : 1.f;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        // (no key yet: both -inf, and nothing to rescale)
-                        const float alpha =
-                            mx[nt][e] > m[nt][e] ? tcfwd::ex2((m[nt][e] - mx[nt][e]) * rowf[nt][e]) : 1.f;
-                        m[nt][e] = mx[nt][e];
-                        l[nt][e] *= alpha;
-                        const float f = alpha * ru;
-#pragma unroll
-                        for (int mt = 0; mt < DP / 16; ++mt) {
-                            oacc[mt][nt][e] *= f;
-                            oacc[mt][nt][2 + e] *= f;
-                        }
-                    }
-                u = unew;
-            }
-            uint32_t pb[2][NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float pv[4][2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float ref = m[nt][e] == -INFINITY ? 0.f : kPOff - m[nt][e] * rowf[nt][e];
-                    float pe[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) pe[i] = tcfwd::ex2(fmaf(x[nt][e][i], rowf[nt][e], ref));
-                    l[nt][e] += (pe[0] + pe[1]) + (pe[2] + pe[3]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)  // (a scale that is no number counts only where its key does)
-                        pv[i][e] = EDGE && x[nt][e][i] == -INFINITY ? 0.f : pe[i] * vw[i];
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    pb[i >> 1][nt][i & 1] = movmatrix_trans(MmaOp<__half>::pack(pv[i][0], pv[i][1]));
-            }
-
-            // O^T += V^T P^T: rows g and g + 8 of a 16-column step are its columns
-            // 2 g and 2 g + 1
-            uint32_t vmask[2][2];
-            if (EDGE) {
-#pragma unroll
-                for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int k = key0 + kt * 16 + h * 8 + 2 * tig;
-                        vmask[kt][h] = (k >= un.klo && k < un.kend ? 0xffffu : 0u) |
-                                       (k + 1 >= un.klo && k + 1 < un.kend ? 0xffff0000u : 0u);
-                    }
-            }
-#pragma unroll
-            for (int cc = 0; cc < DP / 16; cc += 2) {
-#pragma unroll
-                for (int kt = 0; kt < 2; ++kt) {
-                    uint32_t r[4];
-                    ldmatrix_x4_trans(r, vs + chunk_at<DP>(kw0 + kt * 16 + (lane & 15), cc + (lane >> 4)));
-                    if (EDGE) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) r[i] &= vmask[kt][i & 1];
-                    }
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t f[4];
-                        Op::even_odd(r[2 * h], f[0], f[1]);
-                        Op::even_odd(r[2 * h + 1], f[2], f[3]);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            MmaOp<__half>::run(oacc[cc + h][nt], f, pb[kt][nt][0], pb[kt][nt][1]);
-                    }
-                }
-            }
-        };
-
+        float ur[NT][2], none[NT][2];  // ur: what a 1 in O is
+        bool own = false;              // rows have units of their own
         for (int t = tile; t < tile + n && ok; ++t, ++it) {
             const uint32_t s = it % NS;
             const bool got = sm100::mbar_wait(full + 8 * s, (it / NS) & 1u, abort_flag, p.wait_ns);
@@ -701,79 +811,104 @@ __global__ void __launch_bounds__(kThreads, resident(DP, NT))
                 break;
             }
             const int key0 = un.kbeg + t * kTile + kw0;
-            if (key0 >= lo_all && hi_all - key0 >= 32) step(std::false_type{}, key0, s);
-            else if (key0 < un.kend) step(std::true_type{}, key0, s);
+            const uint32_t st = sbase + s * L::STAGE;
+            const float *sc = reinterpret_cast<const float *>(smem + s * L::STAGE + 2 * L::TILE) + kw0;
+            bool fits = true;
+            if (key0 >= lo_all && hi_all - key0 >= 32)
+                fits = q8_step<CODE, DP, NT, false, false>(w, st, st + L::TILE, sc, kw0, key0, 0, 0, none, none);
+            else if (key0 < un.kend)
+                fits = q8_step<CODE, DP, NT, true, false>(w, st, st + L::TILE, sc, kw0, key0, un.klo, un.kend, none,
+                                                          none);
+            if (!fits) {
+                Rows<DP, NT> rest = w;
+                float unit[NT][2];
+                ok = own_steps<CODE, DP, NT>(a, rest, unit, smem, un.kbeg, un.klo, un.kend, t, tile + n, it);
+                w = rest;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) ur[nt][e] = 1.f / unit[nt][e];
+                own = true;
+                it += tile + n - t;
+                break;
+            }
             __syncwarp();
             if (lane == 0) sm100::mbar_arrive(empty + 8 * s);
         }
 
-        // Merge the four warps: their maxima, sums and scale units through shared
-        // memory, then O, brought to the common ones: warps 2 and 3 hand theirs to
-        // 0 and 1, warp 1 to warp 0.
+        // Merge the four warps: their maxima, sums and units through shared memory,
+        // then O, brought to the common ones: warps 2 and 3 hand theirs to 0 and 1,
+        // warp 1 to warp 0.
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float ls = l[nt][e];
+                if (!own) ur[nt][e] = w.u;
+                float ls = w.l[nt][e];
                 ls += __shfl_xor_sync(0xffffffffu, ls, 4);
                 ls += __shfl_xor_sync(0xffffffffu, ls, 8);
                 ls += __shfl_xor_sync(0xffffffffu, ls, 16);
-                m[nt][e] *= rowf[nt][e];  // in log2 units from here on
+                w.m[nt][e] *= w.f[nt][e];  // in log2 units from here on
                 if (g == 0) {
-                    stat_m[warp * R + nt * 8 + 2 * tig + e] = m[nt][e];
+                    stat_m[warp * R + nt * 8 + 2 * tig + e] = w.m[nt][e];
                     stat_l[warp * R + nt * 8 + 2 * tig + e] = ls;
+                    stat_u[warp * R + nt * 8 + 2 * tig + e] = ur[nt][e];
                 }
             }
-        if (lane == 0) stat_u[warp] = u;
         // the four warps go on or give up together
         ok = sm100::bar_red_and(1, 128, ok);
         if (!ok) break;
-        const float U = fmaxf(fmaxf(stat_u[0], stat_u[1]), fmaxf(stat_u[2], stat_u[3]));
-        const float to_u = u / U;
-        float M[NT][2], Lsum[NT][2];
+        float M[NT][2], Lsum[NT][2], U[NT][2];  // U: the largest ur, brought to M
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const float *sm = stat_m + nt * 8 + 2 * tig + e, *sl = stat_l + nt * 8 + 2 * tig + e;
+                const float *su = stat_u + nt * 8 + 2 * tig + e;
                 const float mx = fmaxf(fmaxf(sm[0], sm[R]), fmaxf(sm[2 * R], sm[3 * R]));
                 const float mref = mx == -INFINITY ? 0.f : mx;
-                float ls = 0.f;
+                float ls = 0.f, um = 0.f;
 #pragma unroll
-                for (int w = 0; w < 4; ++w) ls += sl[w * R] * exp2f(sm[w * R] - mref);
+                for (int k = 0; k < 4; ++k) {
+                    const float e2 = exp2f(sm[k * R] - mref);
+                    ls += sl[k * R] * e2;
+                    um = fmaxf(um, su[k * R] * e2);
+                }
                 M[nt][e] = mx;
                 Lsum[nt][e] = ls;
-                const float f = exp2f(m[nt][e] - mref) * to_u;
+                U[nt][e] = um;
+                // (a row without keys: 0, and so is O)
+                const float f = um > 0.f ? exp2f(w.m[nt][e] - mref) * ur[nt][e] / um : 0.f;
 #pragma unroll
                 for (int mt = 0; mt < DP / 16; ++mt) {
-                    oacc[mt][nt][e] *= f;
-                    oacc[mt][nt][2 + e] *= f;
+                    w.o[mt][nt][e] *= f;
+                    w.o[mt][nt][2 + e] *= f;
                 }
             }
 #pragma unroll
         for (int c0 = 0; c0 < DP / 16; c0 += L::MC / 16) {
-            auto at = [&](int w, int mt, int nt, int e) -> float2 * {
-                return reinterpret_cast<float2 *>(mbuf + (w * R + nt * 8 + 2 * tig + e) * L::PITCH + mt * 16 + 2 * g);
+            auto at = [&](int k, int mt, int nt, int e) -> float2 * {
+                return reinterpret_cast<float2 *>(mbuf + (k * R + nt * 8 + 2 * tig + e) * L::PITCH + mt * 16 + 2 * g);
             };
-            auto put = [&](int w) {
+            auto put = [&](int k) {
 #pragma unroll
                 for (int mt = 0; mt < L::MC / 16; ++mt)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
-                            *at(w, mt, nt, e) = make_float2(oacc[c0 + mt][nt][e], oacc[c0 + mt][nt][2 + e]);
+                            *at(k, mt, nt, e) = make_float2(w.o[c0 + mt][nt][e], w.o[c0 + mt][nt][2 + e]);
             };
-            auto add = [&](int w) {
+            auto add = [&](int k) {
 #pragma unroll
                 for (int mt = 0; mt < L::MC / 16; ++mt)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const float2 v = *at(w, mt, nt, e);
-                            oacc[c0 + mt][nt][e] += v.x;
-                            oacc[c0 + mt][nt][2 + e] += v.y;
+                            const float2 v = *at(k, mt, nt, e);
+                            w.o[c0 + mt][nt][e] += v.x;
+                            w.o[c0 + mt][nt][2 + e] += v.y;
                         }
             };
             if (c0 > 0) sm100::named_bar_sync(1, 128);
@@ -799,7 +934,7 @@ __global__ void __launch_bounds__(kThreads, resident(DP, NT))
                     // a row without keys: +0 and -inf; one with a NaN key: NaN
                     const float ls = Lsum[nt][e];
                     const float inv = ls == 0.f ? 0.f : 1.f / ls;
-                    const float unit = U;
+                    const float unit = U[nt][e];
                     const float lse2 = ls != ls ? ls : ls > 0.f ? M[nt][e] - kPOff + __log2f(ls) : -INFINITY;
                     if (whole) {
                         const int qi = (row0 + row) / G, h = kvh * G + (row0 + row) % G;
@@ -808,7 +943,7 @@ __global__ void __launch_bounds__(kThreads, resident(DP, NT))
 #pragma unroll
                         for (int mt = 0; mt < DP / 16; ++mt)
                             if (mt * 16 < p.Dv) {
-                                const float x = oacc[mt][nt][e] * inv * unit, y = oacc[mt][nt][2 + e] * inv * unit;
+                                const float x = w.o[mt][nt][e] * inv * unit, y = w.o[mt][nt][2 + e] * inv * unit;
                                 *reinterpret_cast<uint32_t *>(dst + mt * 16) =
                                     a.bf16 ? MmaOp<__nv_bfloat16>::pack(x, y) : MmaOp<__half>::pack(x, y);
                             }
@@ -820,7 +955,7 @@ __global__ void __launch_bounds__(kThreads, resident(DP, NT))
                         for (int mt = 0; mt < DP / 16; ++mt)
                             if (mt * 16 < p.Dv)
                                 *reinterpret_cast<float2 *>(dst + mt * 16) = make_float2(
-                                    oacc[mt][nt][e] * inv * unit, oacc[mt][nt][2 + e] * inv * unit);
+                                    w.o[mt][nt][e] * inv * unit, w.o[mt][nt][2 + e] * inv * unit);
                         // (+inf, so that the merge's maximum does not pass a NaN by)
                         if (g == 0) (C ? xlse : a.part_lse)[prow] = lse2 != lse2 ? INFINITY : lse2;
                     }

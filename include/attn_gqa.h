@@ -415,8 +415,11 @@ ATTN_API int attn_cache_append_varlen(const void *k, const void *v, void *k_page
  * bf16/fp16, Q * Hq / Hkv <= 1024, D and Dv multiples of 16 up to 256, pages of 8
  * rows or more) where Q * Hq / Hkv <= 64 (32 with D or Dv above 128) or where few
  * sequences and heads leave the other kernels too little to do at once.  Scales
- * then multiply scores and probabilities in fp32 and no key or value is rounded;
- * small problems take one launch without a workspace, others a second one that
+ * then multiply scores and probabilities in fp32 and no key or value is rounded; a
+ * key's weight (probability times value scale) is rounded to fp16 in a unit that keeps
+ * 11 bits down to 2^-22 of the largest weight among the keys that the row attends to,
+ * and steps of 2^-32 of it below; probabilities under 2^-126 of the row's largest count
+ * as 0.  Small problems take one launch without a workspace, others a second one that
  * merges the partials of sequences cut between blocks.  Other problems, and the other values of algo
  * (as in attn_fwd_ex), run on a copy of the keys and values in q's type, made
  * group by group of sequences in a workspace from the library's pool (512 MB, or

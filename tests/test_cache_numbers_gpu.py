@@ -81,9 +81,9 @@ class Problem:
         the value's scale: a score's fp32 accumulation is off by at most (D + 8) 2^-24 of
         scale * sum |q||k|, which moves p by twice that relative to it; sums over n keys
         are off by n 2^-24 each, ex2 by 2^-22; w is rounded to fp16 under the row's own
-        power, so that its largest is at least 2^13 -- by 2^-11 of itself, or by 2^-25 of
-        2^-13 of the largest -- and to fp32 before that (2^-150 at the least); o once at
-        the end."""
+        unit, in which its largest is 2^8 or more -- by 2^-11 of itself, or by half of a step
+        of 2^-24, which is 2^-33 of the largest -- and to fp32 before that (2^-150 at the
+        least); o once at the end."""
         B, Q, Hq, G = len(self.lens), self.Q, self.Hq, self.Hq // self.Hkv
         codes = [cache_ref.code_values(c, self.kind) for c in self.codes]
         q = self.q.double().numpy()
@@ -113,7 +113,7 @@ class Problem:
                     lse[b, i, h] = m + math.log(total)
                     ds = (D + 8) * 2.0 ** -24 * big
                     rel = 2 * ds + 2 * (hi - lo) * 2.0 ** -24 + 2.0 ** -20
-                    small = np.abs(c).sum(0) * (2.0 ** -38 * w.max() + 2.0 ** -150)
+                    small = np.abs(c).sum(0) * (2.0 ** -33 * w.max() + 2.0 ** -150)
                     to[b, i, h] = ((2.0 ** -11 + rel) * (w @ np.abs(c)) + small) / total
                     tl[b, i, h] = ds + (hi - lo) * 2.0 ** -24 + 2.0 ** -20 + 2.0 ** -22 * abs(lse[b, i, h])
         to += HALF[self.dtype] * (np.abs(o) + to) + LEAST[self.dtype]
@@ -166,3 +166,58 @@ def test_scales_that_are_no_numbers_poison_the_rows_that_attend(path, bad, which
     elif math.isnan(bad):
         assert np.isnan(lse[hit]).all()
     assert np.array_equal(o[~hit], before[0][~hit]) and np.array_equal(lse[~hit], before[1][~hit])
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("path", PATHS)
+def test_value_scales_of_any_spread(path, kind):
+    """Blocks of 2^-100 to 2^100 in any order: what a row weighs least does not cost what
+    it weighs most its bits."""
+    g = np.random.default_rng(3)
+    x = Problem(g, path, block=8, kind=kind)
+    x.scales[1][...] = 2.0 ** g.integers(-100, 101, x.scales[1].shape)
+    x.check()
+
+
+# rows that end (or begin, under the window) inside a block's last (first) key
+RAGGED = {"cluster": dict(lens=[500, 132], Q=4), "merge": dict(lens=[20004, 300], Q=4),
+          "whole": dict(lens=[100 + 8 * i for i in range(57)], Q=2), "groups": dict(lens=[500, 132]),
+          "groups merge": dict(lens=[9004, 84])}
+
+
+@pytest.mark.parametrize("huge", [2.0 ** 40, 2.0 ** 100])
+@pytest.mark.parametrize("path", PATHS)
+def test_a_value_scale_counts_only_where_its_key_does(path, huge):
+    """The last key, which the last row alone attends to, and the keys that only the first
+    row's window still holds, are in blocks of very large scales: the bounds of the
+    other rows know nothing of them."""
+    g = np.random.default_rng(4)
+    x = Problem(g, path, block=8, **{**RAGGED[path], "lens": [n - 3 for n in RAGGED[path]["lens"]]})
+    for b, n in enumerate(x.lens):     # n = 1 mod 8
+        x.scales[1][x.at(b, n - 1)[1]] *= huge
+    x.check()
+    x = Problem(g, path, block=8, **RAGGED[path])
+    x.window = 54 - x.Q                # row 0 begins at n - 53 = 7 mod 8: at a block's last key
+    for b, n in enumerate(x.lens):
+        lo, _ = x.keys(b, 0)
+        x.scales[1][x.at(b, lo - lo % 8)[1]] *= huge
+    x.check()
+
+
+@pytest.mark.parametrize("path", PATHS)
+def test_a_large_value_scale_of_a_key_that_hardly_counts(path):
+    """A block in the first tile (and one in the middle) whose probability is about 2^-73
+    and whose values are 2^67 times the others': 2^-6 of the whole, and no reason for the
+    others to lose bits."""
+    g = np.random.default_rng(5)
+    x = Problem(g, path, block=8)
+    sign = np.where(g.random(D) < 0.5, -1.0, 1.0)
+    x.q = (x.q.float().abs() * torch.from_numpy(sign).float()).to(x.q.dtype)
+    away = np.where(sign > 0, -127, 127).astype(np.int8).view(np.uint8)
+    for b, n in enumerate(x.lens):
+        for j in {0, n // 2 // 8 * 8} if n else ():
+            row, blk = x.at(b, j)
+            x.codes[0][row[0], row[1]:row[1] + 8] = away
+            x.scales[0][blk] = 2.0 ** -4
+            x.scales[1][blk] = 2.0 ** 60
+    x.check()
