@@ -38,8 +38,9 @@
 // all completing on the stage's mbarrier; consumers free a stage with one
 // arrival a warp, so no warp waits for another within a tile.  Tiles that every
 // row attends to whole take a step without tests; in the others masked scores
-// are -inf and V's words are cleared where a key takes no part (a code there may
-// be e4m3's NaN).
+// are -inf and V's words are cleared where a key takes no part for any row (a code there
+// may be anything); e4m3's NaN codes on the others' keys count as 0, and put_nans marks
+// the rows that attend to them.
 //
 // Work: the 128-key tiles of all sequences, in order, are cut into equal shares
 // whatever the lengths, and a CTA takes one share for one KV head (and row group) -- as many
@@ -268,6 +269,69 @@ template <int DP, int NT> struct Rows {
     float u, u_min;              // value scales seen: O's unit, and the least
 };
 
+// Which halves of a word of V^T codes (columns 2 g, 2 g + 1 of keys k and k + 1) belong to
+// keys that some row attends to.
+__device__ __forceinline__ uint32_t key_mask(int k, int klo, int kend) {
+    return (k >= klo && k < kend ? 0xffffu : 0u) | (k + 1 >= klo && k + 1 < kend ? 0xffff0000u : 0u);
+}
+
+// The sign bits of the bytes that are e4m3's NaN codes.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t x) { return ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+
+// NaN in O's elements whose row attends to a key whose value is NaN there: how many do is
+// the product of [code is NaN] and [row attends].  (For steps that some rows' keys end in
+// and that hold such a code; the product with P, where 0 * NaN would reach every row,
+// takes those codes as 0.)
+template <int DP, int NT>
+__device__ __noinline__ void put_nans(Rows<DP, NT> &w, uint32_t vs, int kw0, int key0, int klo, int kend) {
+    using Op = CodeOps<kCodeE4m3>;
+    const int lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
+    uint32_t pb[2][NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int key = key0 + g + 8 * i;
+            float on[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) on[e] = key >= w.lo[nt][e] && key < w.hi[nt][e] ? 1.f : 0.f;
+            pb[i >> 1][nt][i & 1] = movmatrix_trans(MmaOp<__half>::pack(on[0], on[1]));
+        }
+#pragma unroll
+    for (int cc = 0; cc < DP / 16; cc += 2) {
+        float n[2][NT][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) n[h][nt][j] = 0.f;
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) {
+            uint32_t r[4];
+            ldmatrix_x4_trans(r, vs + chunk_at<DP>(kw0 + kt * 16 + (lane & 15), cc + (lane >> 4)));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)  // 0x38 is 1
+                r[i] = (nan_codes(r[i] & key_mask(key0 + kt * 16 + (i & 1) * 8 + 2 * tig, klo, kend)) >> 7) * 0x38u;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t f[4];
+                Op::even_odd(r[2 * h], f[0], f[1]);
+                Op::even_odd(r[2 * h + 1], f[2], f[3]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) MmaOp<__half>::run(n[h][nt], f, pb[kt][nt][0], pb[kt][nt][1]);
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (n[h][nt][j] > 0.f) w.o[cc + h][nt][j] = __int_as_float(0x7fffffff);
+    }
+}
+
 // One step: the warp's 32 keys from key0 on, codes at ks and vs, scales at sc (values'
 // kTile behind).  EDGE: some row may not attend to all of them, and some may be outside
 // [klo, kend), where no row does.  OWN: rows have units of their own, with bounds of O; a
@@ -406,16 +470,12 @@ __device__ __forceinline__ bool q8_step(Rows<DP, NT> &w, uint32_t ks, uint32_t v
 
     // O^T += V^T P^T: rows g and g + 8 of a 16-column step are its columns
     // 2 g and 2 g + 1
-    uint32_t vmask[2][2];
+    uint32_t vmask[2][2], nans = 0;
     if (EDGE) {
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int k = key0 + kt * 16 + h * 8 + 2 * tig;
-                vmask[kt][h] = (k >= klo && k < kend ? 0xffffu : 0u) |
-                               (k + 1 >= klo && k + 1 < kend ? 0xffff0000u : 0u);
-            }
+            for (int h = 0; h < 2; ++h) vmask[kt][h] = key_mask(key0 + kt * 16 + h * 8 + 2 * tig, klo, kend);
     }
 #pragma unroll
     for (int cc = 0; cc < DP / 16; cc += 2) {
@@ -425,7 +485,14 @@ __device__ __forceinline__ bool q8_step(Rows<DP, NT> &w, uint32_t ks, uint32_t v
             ldmatrix_x4_trans(r, vs + chunk_at<DP>(kw0 + kt * 16 + (lane & 15), cc + (lane >> 4)));
             if (EDGE) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) r[i] &= vmask[kt][i & 1];
+                for (int i = 0; i < 4; ++i) {
+                    r[i] &= vmask[kt][i & 1];
+                    if (CODE == kCodeE4m3) {
+                        const uint32_t n = nan_codes(r[i]);
+                        nans |= n;
+                        r[i] &= ~((n >> 7) * 0xffu);
+                    }
+                }
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -437,6 +504,11 @@ __device__ __forceinline__ bool q8_step(Rows<DP, NT> &w, uint32_t ks, uint32_t v
                     MmaOp<__half>::run(w.o[cc + h][nt], f, pb[kt][nt][0], pb[kt][nt][1]);
             }
         }
+    }
+    if (EDGE && CODE == kCodeE4m3 && __any_sync(0xffffffffu, nans != 0)) {
+        Rows<DP, NT> with = w;
+        put_nans<DP, NT>(with, vs, kw0, key0, klo, kend);
+        w = with;
     }
     return true;
 }

@@ -426,7 +426,9 @@ ATTN_API int attn_cache_append_varlen(const void *k, const void *v, void *k_page
  * one sequence): exact with the powers of two that attn_cache_append writes (fp16:
  * within +-65504), rounded once with other scales.  A sequence's key that a row
  * attends to and whose scale or code is NaN makes that row what attn_fwd gives for
- * a NaN key or value (ATTN_ALGO_DECODE: NaN).
+ * a NaN key or value (the kernel that reads the codes: NaN, for a value's code in its
+ * column, and no other row changes; the others may, as in attn_fwd, give NaN to rows of
+ * the same tile that do not attend to a NaN value as well).
  * Return codes as attn_fwd.
  */
 ATTN_API int attn_fwd_paged_q8(const void *q, const void *k_pages, const void *v_pages,

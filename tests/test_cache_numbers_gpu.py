@@ -221,3 +221,32 @@ def test_a_large_value_scale_of_a_key_that_hardly_counts(path):
             x.scales[0][blk] = 2.0 ** -4
             x.scales[1][blk] = 2.0 ** 60
     x.check()
+
+
+@pytest.mark.parametrize("spread", [False, True])
+@pytest.mark.parametrize("path", PATHS)
+def test_a_value_code_that_is_no_number_reaches_only_rows_that_attend(path, spread):
+    """e4m3's NaN code in a value column: rows that attend to the key are NaN there (and
+    only there), all others keep their bits.  Keys: the last one, which only the last row
+    attends to; the first one of the first row's window; one that all attend to."""
+    g = np.random.default_rng(6)
+    x = Problem(g, path, block=8, kind="e4m3", **RAGGED[path])
+    x.window = 54 - x.Q
+    if spread:
+        x.scales[1][...] = 2.0 ** g.integers(-20, 20, x.scales[1].shape)
+    before = x.run()
+    codes = x.codes[1].copy()
+    for column, code in ((0, 127), (37, 255)):
+        for where in ("last", "first", "all"):
+            x.codes[1] = codes.copy()
+            hit = np.zeros(before[0].shape, bool)
+            for b, n in enumerate(x.lens):
+                j = {"last": n - 1, "first": x.keys(b, 0)[0], "all": x.keys(b, x.Q - 1)[0] + 3}[where]
+                x.codes[1][x.at(b, j)[0] + (1, column)] = code
+                G = x.Hq // x.Hkv
+                for i in range(x.Q):
+                    lo, hi = x.keys(b, i)
+                    hit[b, i, G:2 * G, column] = lo <= j < hi
+            o, lse = x.run()
+            assert np.isnan(o[hit]).all() and hit.any()
+            assert np.array_equal(o[~hit], before[0][~hit]) and np.array_equal(lse, before[1])
