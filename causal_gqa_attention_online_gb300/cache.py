@@ -34,12 +34,19 @@ ATTN_CACHE_E4M3, ATTN_CACHE_INT8 = 0, 1
 _CACHE_CODE = {torch.float8_e4m3fn: ATTN_CACHE_E4M3, torch.int8: ATTN_CACHE_INT8}
 
 
-# The handle of device i's current stream and the current device: what
-# torch.cuda.current_stream(i).cuda_stream and torch.cuda.current_device() give,
-# without their objects and checks (0.2 us against 4 a call).
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+def _public_stream(i):
+    return torch.cuda.current_stream(i).cuda_stream
 
+
+def _public_device():
+    return torch.cuda.current_device()
+
+
+# The handle of device i's current stream and the current device: what the functions
+# above give, without their objects and checks (0.2 us against 4 a call) where torch has
+# what it takes (a build without CUDA has not).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", _public_device)
 
 # Checks of many tensors go through these (half the time of a loop's method calls).
 _is_contiguous, _get_device = torch.Tensor.is_contiguous, torch.Tensor.get_device
