@@ -25,6 +25,9 @@
 //   that meets a wider spread does the rest of the sequence with a unit for each row,
 //   which brings the step's largest weight of the row to [2^13, 2^14) (own_steps): a large
 //   scale on a key that a row does not attend to, or that hardly counts, costs it nothing.
+//   So does one that meets scores past 2^22 (kMaxScore), whose product with f is rounded
+//   by too much for x f - m f: there the difference comes first, and a power of two of f
+//   goes to the key scales, so that x is an fp32 number wherever the score is.
 // * Which bytes pair up is chosen so that no byte is moved across lanes: the two
 //   pairs of a 32-bit word are the two halves of a k16 step (K: Q's columns are
 //   permuted to match) or the rows dv = 2g and 2g + 1 (V: a transposed ldmatrix of
@@ -87,6 +90,7 @@ constexpr float kLeastUnit = 1.92592994e-34f;  // 2^-112
 // Value scales under one unit lie within this factor.  64 sequences of up to 8192 keys, D
 // 128: 98 us, and 137 with scales spread over 2^24, where every row has its unit.
 constexpr float kSpread = 64.f;
+constexpr float kMaxScore = 4194304.f;  // 2^22: x f - m f is off by 2^-2 at most, for all keys alike
 constexpr int kMaxRows = 1024;  // rows of a KV group at most
 
 struct Q8Args {
@@ -258,6 +262,12 @@ __device__ __forceinline__ float own_unit(float w, float o, float &unit) {
     return most;
 }
 
+// What own_steps keeps for each row: the power of two of f that key scales are
+// multiplied by, O's unit, and a bound of O's elements.
+template <int NT> struct Own {
+    float kf[NT][2], unit[NT][2], bound[NT][2];
+};
+
 // What a warp holds of a sequence.  A thread's columns of S^T and O^T are rows 2 tig and
 // 2 tig + 1 of each eight.
 template <int DP, int NT> struct Rows {
@@ -334,11 +344,11 @@ __device__ __noinline__ void put_nans(Rows<DP, NT> &w, uint32_t vs, int kw0, int
 
 // One step: the warp's 32 keys from key0 on, codes at ks and vs, scales at sc (values'
 // kTile behind).  EDGE: some row may not attend to all of them, and some may be outside
-// [klo, kend), where no row does.  OWN: rows have units of their own, with bounds of O; a
-// step without gives up, with nothing changed, where scales spread too far for one.
+// [klo, kend), where no row does.  OWN: rows have units of their own; a step without gives
+// up, with nothing changed, where scales spread too far for one or scores are too large.
 template <int CODE, int DP, int NT, bool EDGE, bool OWN>
 __device__ __forceinline__ bool q8_step(Rows<DP, NT> &w, uint32_t ks, uint32_t vs, const float *sc, int kw0, int key0,
-                                        int klo, int kend, float (&unit)[NT][2], float (&bound)[NT][2]) {
+                                        int klo, int kend, Own<NT> &own) {
     using Op = CodeOps<CODE>;
     const int lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
     // S^T = K Q^T
@@ -384,16 +394,16 @@ __device__ __forceinline__ bool q8_step(Rows<DP, NT> &w, uint32_t ks, uint32_t v
         kscale[i] = sc[g + 8 * i];
         vw[i] = sc[kTile + g + 8 * i] * inv_u;
     }
-    float x[NT][2][4], mx[NT][2];
+    float x[NT][2][4], mx[NT][2], ref[NT][2];
     const bool spread = !OWN && unew > kSpread * least;
-    bool grew = OWN || unew > w.u || spread;
+    bool grew = OWN || unew > w.u || spread, leave = spread;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                x[nt][e][i] = sacc[i >> 1][nt][2 * (i & 1) + e] * kscale[i];
+                x[nt][e][i] = sacc[i >> 1][nt][2 * (i & 1) + e] * (OWN ? kscale[i] * own.kf[nt][e] : kscale[i]);
                 if (EDGE) {
                     const int key = key0 + g + 8 * i;
                     if (!(key >= w.lo[nt][e] && key < w.hi[nt][e])) x[nt][e][i] = -INFINITY;
@@ -404,7 +414,11 @@ __device__ __forceinline__ bool q8_step(Rows<DP, NT> &w, uint32_t ks, uint32_t v
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
             v = tcfwd::fmax3(v, __shfl_xor_sync(0xffffffffu, v, 16), w.m[nt][e]);
             mx[nt][e] = v;
+            ref[nt][e] = v == -INFINITY ? 0.f : OWN ? v : kPOff - v * w.f[nt][e];
             grew |= v > w.m[nt][e];
+            // (-inf: a row that attends to keys here, and every score of it so far is)
+            if (!OWN && v == -INFINITY && (!EDGE || (key0 < w.hi[nt][e] && key0 + 31 >= w.lo[nt][e])))
+                grew = leave = true;
         }
     float to[NT][2];  // (OWN) what O is multiplied by for its new unit
     if (OWN) {
@@ -420,14 +434,20 @@ __device__ __forceinline__ bool q8_step(Rows<DP, NT> &w, uint32_t ks, uint32_t v
 #pragma unroll
                 for (int d = 4; d <= 16; d *= 2) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
                 if (mx[nt][e] > w.m[nt][e])
-                    bound[nt][e] *= tcfwd::ex2((w.m[nt][e] - mx[nt][e]) * w.f[nt][e]);
-                to[nt][e] = own_unit(most, bound[nt][e], unit[nt][e]);
+                    own.bound[nt][e] *= tcfwd::ex2((w.m[nt][e] - mx[nt][e]) * w.f[nt][e]);
+                to[nt][e] = own_unit(most, own.bound[nt][e], own.unit[nt][e]);
                 // (a step adds 32 weights of 2^15 times codes of 448 at most)
-                bound[nt][e] = bound[nt][e] * to[nt][e] + 0x1p29f;
+                own.bound[nt][e] = own.bound[nt][e] * to[nt][e] + 0x1p29f;
             }
     }
     if (__any_sync(0xffffffffu, grew)) {
-        if (spread) return false;
+        if (!OWN) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) leave |= fabsf(ref[nt][e]) > kMaxScore;
+            if (__any_sync(0xffffffffu, leave)) return false;
+        }
         const float ru = unew > w.u ? w.u * inv_u : 1.f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -454,14 +474,15 @@ __device__ __forceinline__ bool q8_step(Rows<DP, NT> &w, uint32_t ks, uint32_t v
         float pv[4][2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const float ref = w.m[nt][e] == -INFINITY ? 0.f : kPOff - w.m[nt][e] * w.f[nt][e];
             float pe[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) pe[i] = tcfwd::ex2(fmaf(x[nt][e][i], w.f[nt][e], ref));
+            for (int i = 0; i < 4; ++i)
+                pe[i] = tcfwd::ex2(OWN ? fmaf(x[nt][e][i] - ref[nt][e], w.f[nt][e], kPOff)
+                                       : fmaf(x[nt][e][i], w.f[nt][e], ref[nt][e]));
             w.l[nt][e] += (pe[0] + pe[1]) + (pe[2] + pe[3]);
 #pragma unroll
             for (int i = 0; i < 4; ++i)  // (a scale that is no number counts only where its key does)
-                pv[i][e] = EDGE && x[nt][e][i] == -INFINITY ? 0.f : (OWN ? pe[i] * unit[nt][e] : pe[i]) * vw[i];
+                pv[i][e] = EDGE && x[nt][e][i] == -INFINITY ? 0.f : (OWN ? pe[i] * own.unit[nt][e] : pe[i]) * vw[i];
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -513,8 +534,8 @@ __device__ __forceinline__ bool q8_step(Rows<DP, NT> &w, uint32_t ks, uint32_t v
     return true;
 }
 
-// The rest of a sequence's tiles, [t, end), in stages from it on, with a unit for each row:
-// unit[] is what O is in at the end.  (A function of its own: its code would cost the
+// The rest of a sequence's tiles, [t, end), in stages from it on, with a unit for each row
+// (unit[]: what O is in at the end).  (A function of its own: its code would cost the
 // others' steps registers.)
 template <int CODE, int DP, int NT>
 __device__ __noinline__ bool own_steps(const Q8Args &a, Rows<DP, NT> &rows, float (&unit)[NT][2], uint8_t *smem,
@@ -525,13 +546,17 @@ __device__ __noinline__ bool own_steps(const Q8Args &a, Rows<DP, NT> &rows, floa
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::SHARE + 24);
     const int kw0 = (threadIdx.x >> 5) * 32;
     Rows<DP, NT> w = rows;
-    float bound[NT][2];
+    Own<NT> own;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            unit[nt][e] = 1.f / w.u;
-            bound[nt][e] = 0x1p55f;  // (of 2^31 keys)
+            own.unit[nt][e] = 1.f / w.u;
+            own.bound[nt][e] = 0x1p55f;  // (of 2^31 keys)
+            const int ef = min(max((int)(__float_as_uint(w.f[nt][e]) >> 23) - 127, -60), 0);
+            own.kf[nt][e] = pow2(ef);
+            w.f[nt][e] *= pow2(-ef);
+            w.m[nt][e] *= pow2(ef);
         }
     bool ok = true;
     for (; t < end; ++t, ++it) {
@@ -549,11 +574,15 @@ __device__ __noinline__ bool own_steps(const Q8Args &a, Rows<DP, NT> &rows, floa
         const uint32_t st = sbase + s * L::STAGE;
         const float *sc = reinterpret_cast<const float *>(smem + s * L::STAGE + 2 * L::TILE) + kw0;
         if (key0 < kend)
-            q8_step<CODE, DP, NT, true, true>(w, st, st + L::TILE, sc, kw0, key0, klo, kend, unit, bound);
+            q8_step<CODE, DP, NT, true, true>(w, st, st + L::TILE, sc, kw0, key0, klo, kend, own);
         __syncwarp();
         if ((threadIdx.x & 31) == 0) sm100::mbar_arrive(empty + 8 * s);
     }
     rows = w;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) unit[nt][e] = own.unit[nt][e];
     return ok;
 }
 
@@ -869,8 +898,9 @@ __global__ void __launch_bounds__(kThreads, resident(DP, NT))
 #pragma unroll
                 for (int j = 0; j < 4; ++j) w.o[mt][nt][j] = 0.f;
 
-        float ur[NT][2], none[NT][2];  // ur: what a 1 in O is
-        bool own = false;              // rows have units of their own
+        float ur[NT][2];   // what a 1 in O is
+        bool own = false;  // rows have units of their own
+        Own<NT> none;
         for (int t = tile; t < tile + n && ok; ++t, ++it) {
             const uint32_t s = it % NS;
             const bool got = sm100::mbar_wait(full + 8 * s, (it / NS) & 1u, abort_flag, p.wait_ns);
@@ -887,10 +917,9 @@ __global__ void __launch_bounds__(kThreads, resident(DP, NT))
             const float *sc = reinterpret_cast<const float *>(smem + s * L::STAGE + 2 * L::TILE) + kw0;
             bool fits = true;
             if (key0 >= lo_all && hi_all - key0 >= 32)
-                fits = q8_step<CODE, DP, NT, false, false>(w, st, st + L::TILE, sc, kw0, key0, 0, 0, none, none);
+                fits = q8_step<CODE, DP, NT, false, false>(w, st, st + L::TILE, sc, kw0, key0, 0, 0, none);
             else if (key0 < un.kend)
-                fits = q8_step<CODE, DP, NT, true, false>(w, st, st + L::TILE, sc, kw0, key0, un.klo, un.kend, none,
-                                                          none);
+                fits = q8_step<CODE, DP, NT, true, false>(w, st, st + L::TILE, sc, kw0, key0, un.klo, un.kend, none);
             if (!fits) {
                 Rows<DP, NT> rest = w;
                 float unit[NT][2];

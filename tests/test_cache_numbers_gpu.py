@@ -250,3 +250,46 @@ def test_a_value_code_that_is_no_number_reaches_only_rows_that_attend(path, spre
             o, lse = x.run()
             assert np.isnan(o[hit]).all() and hit.any()
             assert np.array_equal(o[~hit], before[0][~hit]) and np.array_equal(lse, before[1])
+
+
+@pytest.mark.parametrize("algo", ["decode", "generic"])
+@pytest.mark.parametrize("big", [2.0 ** 14, 2.0 ** 24, 2.0 ** 50, 2.0 ** 108])
+@pytest.mark.parametrize("path", PATHS)
+def test_scores_up_to_the_largest_numbers(path, big, algo):
+    """One key with a scale of 2^14 to 2^108: a score of about +2^10 times that leaves the key
+    alone, a negative one drops it as a scale of 2^10 does, to the bit.  All keys with such
+    scores, but one with half of their size: it is left alone."""
+    g = np.random.default_rng(7)
+    x = Problem(g, path, block=1)
+    sign = np.where(g.random(D) < 0.5, -1, 1)
+    x.q = (x.q.float().abs() * torch.from_numpy(sign).float()).to(x.q.dtype)
+    at = {b: x.at(b, n // 3) for b, n in enumerate(x.lens) if n}
+
+    def put(code, scale):
+        for row, blk in at.values():
+            x.codes[0][row] = (code * sign).astype(np.int8).view(np.uint8)
+            x.scales[0][blk] = scale
+
+    put(-127, 2.0 ** 10)
+    below = x.run(algo=algo)
+    put(-127, big)
+    o, lse = x.run(algo=algo)
+    assert np.array_equal(o, below[0]) and np.array_equal(lse, below[1])
+    q = x.q.double().numpy()
+
+    def check_alone(code):
+        o, lse = x.run(algo=algo)
+        for b, (row, blk) in at.items():
+            v = cache_ref.code_values(x.codes[1][row], x.kind) * x.scales[1][blk].astype(np.float64)[:, None]
+            v = v.repeat(x.Hq // x.Hkv, axis=0)[None]
+            # (the probability is 1, the others 0: o is a value, rounded once)
+            assert (np.abs(o[b] - v) <= HALF[x.dtype] * np.abs(v) + LEAST[x.dtype]).all()
+            s = np.abs(q[b]).sum(-1) * code * big / math.sqrt(D)
+            assert (np.abs(lse[b] - s) <= ((D + 8) * 2.0 ** -24 + 2.0 ** -20) * np.abs(s)).all()
+
+    put(127, big)
+    check_alone(127)
+    x.codes[0][...] = (-127 * sign).astype(np.int8).view(np.uint8)
+    x.scales[0][...] = big
+    put(-64, big)
+    check_alone(-64)
