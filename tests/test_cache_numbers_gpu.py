@@ -293,3 +293,40 @@ def test_scores_up_to_the_largest_numbers(path, big, algo):
     x.scales[0][...] = big
     put(-64, big)
     check_alone(-64)
+
+
+@pytest.mark.parametrize("algo", ["tcgen05", "mma", "generic"])
+@pytest.mark.parametrize("what", ["key scale", "value scale", "value code"])
+def test_numbers_that_are_none_over_expanded_keys(what, algo):
+    """The kernels over expanded keys give what attn_fwd gives over the same keys and values,
+    NaN among them, to the bit."""
+    g = np.random.default_rng(8)
+    x = Problem(g, "groups", block=8, kind="e4m3", lens=[497, 129])
+    if what == "value code":
+        x.codes[1][x.at(0, 496)[0] + (1, 3)] = 127
+    else:
+        x.scales[what == "value scale"][x.at(0, 496)[1] + (1,)] = math.nan
+    o, lse = x.run(algo=algo)
+    K = x.table.shape[1] * PAGE
+    dense = [cache_ref.gather(cache_ref.as_values(c, s, x.kind), x.table, x.lens, K)
+             for c, s in zip(x.codes, x.scales)]
+    k, v = (torch.from_numpy(d).to(DEV).to(DT[x.dtype]) for d in dense)
+    assert torch.isnan(v if what[0] == "v" else k).any()
+    ro, rl = attn.attn_fwd(x.q.to(DEV), k, v, seqlens_k=i32(x.lens), algo=algo)
+    assert np.array_equal(o, ro.double().cpu().numpy(), equal_nan=True)
+    assert np.array_equal(lse, rl.double().cpu().numpy(), equal_nan=True)
+
+
+@pytest.mark.parametrize("path", PATHS)
+def test_a_table_far_wider_than_the_sequences(path):
+    """A table for 131072 keys, as a serving program keeps one: the kernels are chosen by its
+    width, and the expanded keys of one to eight sequences at a time take the workspace."""
+    g = np.random.default_rng(9)
+    x = Problem(g, path)
+    fitted = x.run(algo="tcgen05")
+    wide = np.full((len(x.lens), 131072 // PAGE), -1, np.int32)
+    wide[:, :x.table.shape[1]] = x.table
+    x.table = wide
+    x.check()
+    o, lse = x.run(algo="tcgen05")
+    assert np.array_equal(o, fitted[0]) and np.array_equal(lse, fitted[1])
