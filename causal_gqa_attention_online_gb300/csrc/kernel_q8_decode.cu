@@ -417,7 +417,7 @@ __device__ __forceinline__ bool q8_step(Rows<DP, NT> &w, uint32_t ks, uint32_t v
             ref[nt][e] = v == -INFINITY ? 0.f : OWN ? v : kPOff - v * w.f[nt][e];
             grew |= v > w.m[nt][e];
             // (-inf: a row that attends to keys here, and every score of it so far is)
-            if (!OWN && v == -INFINITY && (!EDGE || (key0 < w.hi[nt][e] && key0 + 31 >= w.lo[nt][e])))
+            if (!OWN && v == -INFINITY && (!EDGE || max(w.lo[nt][e], key0) < min(w.hi[nt][e], key0 + 32)))
                 grew = leave = true;
         }
     float to[NT][2];  // (OWN) what O is multiplied by for its new unit
