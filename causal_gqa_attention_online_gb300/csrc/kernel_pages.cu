@@ -7,7 +7,7 @@
 // work is latency bound (a few thousand entries); it runs as one cluster of
 // kPlanCtas blocks that meet at cluster barriers, so a plan is one launch
 // whatever its phases.  Per-page counts live in the cluster's shared memory where
-// they fit (80 thousand pages), and there is no workspace then; where few bytes
+// they fit (fork: 65536 pages, compaction: 136528), and there is no workspace then; where few bytes
 // can move (kSmallBytes) the cluster copies them itself, otherwise a second launch
 // does, which finds the pairs in the new version.  Larger pools, and calls that can
 // move more than kListBytes, keep counts and lists in a workspace, and the table
@@ -432,7 +432,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     const int per_p = 1 << sf.part_shift, pmask = per_p - 1;
     const int per_s = (a.N + kPlanCtas - 1) / kPlanCtas;
     // (entries are numbered in 32 bits here: the 64-bit minimum on another block's
-    // shared memory was seen to lose updates)
+    // shared memory was seen to lose updates; the cause was not found)
     int2 *moves = reinterpret_cast<int2 *>(dyn);                   // [per_s] pages to copy
     unsigned *claim = reinterpret_cast<unsigned *>(moves + per_s);  // [per_p]
     int *was = reinterpret_cast<int *>(claim + per_p), *full = was + per_p, *held = full + per_p;

@@ -59,12 +59,12 @@
 // to eight CTAs, which split its tiles and join their states through distributed
 // shared memory: one launch and no workspace.
 //
-// Measured: 64 ragged sequences up to 8192 keys (Hq 32, Hkv 8, D 128) in 100 us
-// with int8 codes (5.44 TB/s, 0.80 of a plain copy) and 93 with e4m3; the copies
-// without any arithmetic take 90, ten of them launch and first tile.  Two sequences
-// of 100003 keys, four rows each of 16 heads over 4, D 64, e4m3: 35 us (2.6 TB/s),
-// bound by the softmax's chain of 16 rows and by the prologue.  One sequence of 700
-// keys: 10 us on the GPU.
+// Measured: 64 ragged sequences up to 8192 keys (Hq 32, Hkv 8, D 128) in 102 us
+// with int8 codes (5.36 TB/s, 0.79 of a plain copy) and 95 with e4m3; in a graph 98, of
+// which 89 remain without the arithmetic, ten of them launch and first tile.  Two
+// sequences of 100003 keys, four rows each of 16 heads over 4, D 64, e4m3: 37 us (2.45
+// TB/s); in a graph 35, of which 26 remain without the arithmetic: launch, first tile,
+// the end of the shares and the merge.  One sequence of 700 keys: 8.4 us in a graph.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -88,7 +88,7 @@ constexpr int kThreads = 160;
 constexpr float kPOff = 14.f;  // p is scaled by 2^14
 constexpr float kLeastUnit = 1.92592994e-34f;  // 2^-112
 // Value scales under one unit lie within this factor.  64 sequences of up to 8192 keys, D
-// 128: 98 us, and 137 with scales spread over 2^24, where every row has its unit.
+// 128: 98 us in a graph, and 135 with scales spread over 2^24, where every row has its unit.
 constexpr float kSpread = 64.f;
 constexpr float kMaxScore = 4194304.f;  // 2^22: x f - m f is off by 2^-2 at most, for all keys alike
 constexpr int kMaxRows = 1024;  // rows of a KV group at most
@@ -1331,12 +1331,12 @@ bool q8_decode_supported(const AttnParams &p, int dtype) {
 // expansion of twice the codes' bytes and a prefill that does not split the keys.
 // The groups win with few rows, and with more while they fill the GPU about once.
 // Of the GPU's time, int8, up to K keys a sequence, groups and expansion (us):
-//   D 128, 24 rows: 2 sequences of 25744, 4 heads 41 and 584; 64 of 4096, 8 heads 193
-//     and 351; 64 rows: 58 and 560, 339 and 345
-//   D 128, 8 heads: 256 rows over 25744 (0.8 groups an SM) 205 and 379; 4 x 128 over
-//     8192 (1.7) 99 and 189, 4 x 256 (3.4) 182 and 146
-//   D 256, 8 heads: 48 rows over 300 keys 23 and 21; 96 over 2000 (0.3) 36 and 41; 128
-//     over 25744 (0.4) 258 and 370, 256 (0.8) 480 and 367
+//   D 128, 24 rows: 2 sequences of 25744, 4 heads 41 and 580; 64 of 4096, 8 heads 196
+//     and 344; 64 rows: 57 and 557, 352 and 337
+//   D 128, 8 heads: 256 rows over 25744 (0.8 groups an SM) 202 and 376; 4 x 128 over
+//     8192 (1.7) 99 and 185, 4 x 256 (3.4) 183 and 142
+//   D 256, 8 heads: 48 rows over 300 keys 21 and 16; 96 over 2000 (0.3) 33 and 38; 128
+//     over 25744 (0.4) 264 and 364, 256 (0.8) 482 and 365
 bool q8_decode_wins(const AttnParams &p, int nsm) {
     const int rows = p.Q * p.G;
     const long long all = (long long)p.B * p.Hkv * groups_of(p);

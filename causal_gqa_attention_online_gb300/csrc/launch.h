@@ -120,7 +120,7 @@ int launch_cache_append(const void *k, const void *v, void *k_pages, void *v_pag
 int launch_q8_expand(const AttnParams &p, const Q8Cache &c, void *k_out, void *v_out, int dtype,
                      cudaStream_t stream);
 
-// Split-KV decode that reads the codes themselves (bf16/fp16, Q * G <= 16, widths
+// Split-KV decode that reads the codes themselves (bf16/fp16, Q * G <= 1024, widths
 // multiples of 16 up to 256, pages of 8 rows or more), with a workspace of the
 // given number of bytes at a 16-byte aligned address.
 bool q8_decode_supported(const AttnParams &p, int dtype);

@@ -423,8 +423,13 @@ ATTN_API int attn_cache_append_varlen(const void *k, const void *v, void *k_page
  * merges the partials of sequences cut between blocks.  Other problems, and the other values of algo
  * (as in attn_fwd_ex), run on a copy of the keys and values in q's type, made
  * group by group of sequences in a workspace from the library's pool (512 MB, or
- * one sequence): exact with the powers of two that attn_cache_append writes (fp16:
- * within +-65504), rounded once with other scales.  A sequence's key that a row
+ * one sequence; eight where a sequence's rows of q or o are no multiple of 16 bytes).
+ * The copy is exact with the powers of two that attn_cache_append writes, but for
+ * fp16: there values past +-65504 become +-65504 and values below 2^-14 are rounded
+ * to steps of 2^-24, which the kernel that reads the codes does not do.  Other scales
+ * round once.  Kernels, groups and workspaces go by max_pages, not by lengths, which
+ * the host does not know: a table no wider than the longest sequence is the fastest.
+ * A sequence's key that a row
  * attends to and whose scale or code is NaN makes that row what attn_fwd gives for
  * a NaN key or value (the kernel that reads the codes: NaN, for a value's code in its
  * column, and no other row changes; the others may, as in attn_fwd, give NaN to rows of
