@@ -42,8 +42,8 @@
 // arrival a warp, so no warp waits for another within a tile.  Tiles that every
 // row attends to whole take a step without tests; in the others masked scores
 // are -inf and V's words are cleared where a key takes no part for any row (a code there
-// may be anything); e4m3's NaN codes on the others' keys count as 0, and put_nans marks
-// the rows that attend to them.
+// may be anything); e4m3's NaN codes on the others' keys count as 0, and find_nans finds
+// the elements of the rows that attend to them.
 //
 // Work: the 128-key tiles of all sequences, in order, are cut into equal shares
 // whatever the lengths, and a CTA takes one share for one KV head (and row group) -- as many
@@ -288,14 +288,21 @@ __device__ __forceinline__ uint32_t key_mask(int k, int klo, int kend) {
 // The sign bits of the bytes that are e4m3's NaN codes.
 __device__ __forceinline__ uint32_t nan_codes(uint32_t x) { return ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
-// NaN in O's elements whose row attends to a key whose value is NaN there: how many do is
-// the product of [code is NaN] and [row attends].  (For steps that some rows' keys end in
-// and that hold such a code; the product with P, where 0 * NaN would reach every row,
-// takes those codes as 0.)
+// O's elements whose row attends to a key whose value is NaN there, a bit each (o[mt][nt][j]
+// of word mt / 4, bit (mt % 4 * NT + nt) * 4 + j): the product of [code is NaN] and [row
+// attends] is not 0.  (For steps that some rows' keys end in and that hold such a code; the
+// product with P, where 0 * NaN would reach every row, takes those codes as 0.)
+struct NanBits {
+    uint32_t w[4];
+};
+template <int NT> struct Legal {
+    int lo[NT][2], hi[NT][2];
+};
 template <int DP, int NT>
-__device__ __noinline__ void put_nans(Rows<DP, NT> &w, uint32_t vs, int kw0, int key0, int klo, int kend) {
+__device__ __noinline__ NanBits find_nans(Legal<NT> w, uint32_t vs, int kw0, int key0, int klo, int kend) {
     using Op = CodeOps<kCodeE4m3>;
     const int lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
+    NanBits bits = {{0, 0, 0, 0}};
     uint32_t pb[2][NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -338,8 +345,9 @@ __device__ __noinline__ void put_nans(Rows<DP, NT> &w, uint32_t vs, int kw0, int
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (n[h][nt][j] > 0.f) w.o[cc + h][nt][j] = __int_as_float(0x7fffffff);
+                    if (n[h][nt][j] > 0.f) bits.w[(cc + h) / 4] |= 1u << (((cc + h) % 4 * NT + nt) * 4 + j);
     }
+    return bits;
 }
 
 // One step: the warp's 32 keys from key0 on, codes at ks and vs, scales at sc (values'
@@ -527,9 +535,23 @@ __device__ __forceinline__ bool q8_step(Rows<DP, NT> &w, uint32_t ks, uint32_t v
         }
     }
     if (EDGE && CODE == kCodeE4m3 && __any_sync(0xffffffffu, nans != 0)) {
-        Rows<DP, NT> with = w;
-        put_nans<DP, NT>(with, vs, kw0, key0, klo, kend);
-        w = with;
+        Legal<NT> legal;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                legal.lo[nt][e] = w.lo[nt][e];
+                legal.hi[nt][e] = w.hi[nt][e];
+            }
+        const NanBits bits = find_nans<DP, NT>(legal, vs, kw0, key0, klo, kend);
+#pragma unroll
+        for (int mt = 0; mt < DP / 16; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if ((bits.w[mt / 4] >> ((mt % 4 * NT + nt) * 4 + j)) & 1u)
+                        w.o[mt][nt][j] = __int_as_float(0x7fffffff);
     }
     return true;
 }
