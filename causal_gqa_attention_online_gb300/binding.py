@@ -29,7 +29,8 @@ EXPORTED = ("attn_fwd", "attn_fwd_varlen", "attn_fwd_algo", "attn_fwd_varlen_alg
             "attn_bwd", "attn_bwd_varlen", "attn_lse_combine", "attn_lse_combine_ex",
             "attn_fwd_decode_noalloc", "attn_fwd_staged", "attn_cache_append",
             "attn_cache_append_varlen", "attn_fwd_paged_q8", "attn_pages_copy",
-            "attn_pages_fork", "attn_pages_compact", "attn_last_error",
+            "attn_pages_fork", "attn_pages_compact", "attn_rope", "attn_rope_append",
+            "attn_rope_append_q8", "attn_fwd_paged_shared", "attn_last_error",
             "attn_device_status", "attn_set_wait_limit", "attn_kernel_launches", "attn_version")
 
 _lock = threading.Lock()
@@ -102,8 +103,17 @@ def load_library(path: str | None = None):
         lib.attn_pages_fork.argtypes = ([vp, vp, ip, vp, vp, vp] + [ip] * 4 + [vp, vp, ip] +
                                         [vp] * 5)
         lib.attn_pages_compact.argtypes = [vp, vp, ip, vp, vp, ip, ip, ip] + [vp] * 5
+        lib.attn_fwd_paged_shared.argtypes = ([vp] * 5 + [ip] * 6 + [vp, ip, ip, ip] + [vp] * 4 +
+                                              [ip, fp, ip, ip, vp])
+        lp = ctypes.c_longlong
+        lib.attn_rope.argtypes = [vp] * 6 + [ip] * 7 + [lp, lp, vp, ip, ip, ip, vp]
+        rows = [vp, vp] + [ip] * 9 + [lp] * 3 + [vp] * 3 + [ip, vp, vp, ip, ip, ip]
+        lib.attn_rope_append.argtypes = [vp] * 6 + rows + [ip, vp]
+        lib.attn_rope_append_q8.argtypes = [vp] * 8 + rows + [ip, ip, ip, vp]
         for f in (lib.attn_cache_append, lib.attn_cache_append_varlen, lib.attn_fwd_paged_q8,
-                  lib.attn_pages_copy, lib.attn_pages_fork, lib.attn_pages_compact):
+                  lib.attn_pages_copy, lib.attn_pages_fork, lib.attn_pages_compact,
+                  lib.attn_rope, lib.attn_rope_append, lib.attn_rope_append_q8,
+                  lib.attn_fwd_paged_shared):
             f.restype = ip
         lib.attn_last_error.argtypes = []
         lib.attn_last_error.restype = ctypes.c_char_p

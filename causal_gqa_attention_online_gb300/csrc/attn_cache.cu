@@ -10,17 +10,7 @@
 #include "q8.cuh"
 
 namespace attn {
-namespace {
 
-constexpr int kMaxCount = 1 << 30;  // pages of a pool and slots of a table, in the plans
-
-int log2_of(long long n) {  // n a power of two
-    int s = 0;
-    while ((1LL << s) < n) ++s;
-    return s;
-}
-
-// Checks of a cache that its entry points share.
 int validate_cache(const void *k_pages, const void *v_pages, const float *k_scale,
                    const float *v_scale, int Hkv, int D, int Dv, int max_pages, int page_size,
                    int num_pages, int block_size, int cache_dtype) {
@@ -64,6 +54,16 @@ int validate_cache(const void *k_pages, const void *v_pages, const float *k_scal
     return ATTN_OK;
 }
 
+namespace {
+
+constexpr int kMaxCount = 1 << 30;  // pages of a pool and slots of a table, in the plans
+
+int log2_of(long long n) {  // n a power of two
+    int s = 0;
+    while ((1LL << s) < n) ++s;
+    return s;
+}
+
 int append_common(const void *k, const void *v, void *k_pages, void *v_pages, float *k_scale,
                   float *v_scale, int B, int N, long long total, int Hkv, int D, int Dv,
                   const int32_t *seqlens_new, const int32_t *cu_new, const int32_t *seqlens_k,
@@ -93,30 +93,6 @@ int append_common(const void *k, const void *v, void *k_pages, void *v_pages, fl
                                seqlens_new, cu_new, total, seqlens_k, block_table, max_pages,
                                log2_of(page_size), num_pages, page_size / block_size,
                                log2_of(block_size), cache_dtype, dtype, stream);
-}
-
-// f's launches with a workspace from the library's pool.
-template <typename F> int with_workspace(unsigned long long bytes, cudaStream_t stream, F f) {
-    if (bytes == 0) return f(static_cast<void *>(nullptr));
-    int dev = 0;
-    int rc = current_device(&dev);
-    if (rc) return rc;
-    cudaMemPool_t pool = nullptr;
-    rc = pool_for(dev, &pool);
-    if (rc) return rc;
-    void *ws = nullptr;
-    cudaError_t e = cudaMallocFromPoolAsync(&ws, (size_t)bytes, pool, stream);
-    if (e != cudaSuccess) {
-        set_error("workspace cudaMallocFromPoolAsync(%llu): %s", bytes, cudaGetErrorString(e));
-        return ATTN_ERR_CUDA;
-    }
-    rc = f(ws);
-    e = cudaFreeAsync(ws, stream);
-    if (e != cudaSuccess && rc == 0) {
-        set_error("workspace cudaFreeAsync: %s", cudaGetErrorString(e));
-        rc = ATTN_ERR_CUDA;
-    }
-    return rc;
 }
 
 // Bytes of expanded keys and values that one group of sequences may take (a

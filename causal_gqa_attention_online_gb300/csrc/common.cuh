@@ -19,6 +19,7 @@ enum : int {
     kStatusTimeoutSoftmax = 0x104,
     kStatusTimeoutEpilogue = 0x105,
     kStatusTimeoutQ = 0x106,
+    kStatusTimeoutShared = 0x107,
     kStatusTimeoutDecode = 0x201,
 };
 

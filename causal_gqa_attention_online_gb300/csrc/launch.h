@@ -26,6 +26,30 @@ bool ptr_aligned16(const void *p);
 // Kernel choice, workspace and launches of one forward problem (algo: attn_algo).
 int run_forward(AttnParams &p, int dtype, int algo, cudaStream_t stream);
 
+// f's launches with a workspace from the library's pool.
+template <typename F> int with_workspace(unsigned long long bytes, cudaStream_t stream, F f) {
+    if (bytes == 0) return f(static_cast<void *>(nullptr));
+    int dev = 0;
+    int rc = current_device(&dev);
+    if (rc) return rc;
+    cudaMemPool_t pool = nullptr;
+    rc = pool_for(dev, &pool);
+    if (rc) return rc;
+    void *ws = nullptr;
+    cudaError_t e = cudaMallocFromPoolAsync(&ws, (size_t)bytes, pool, stream);
+    if (e != cudaSuccess) {
+        set_error("workspace cudaMallocFromPoolAsync(%llu): %s", bytes, cudaGetErrorString(e));
+        return 3;
+    }
+    rc = f(ws);
+    e = cudaFreeAsync(ws, stream);
+    if (e != cudaSuccess && rc == 0) {
+        set_error("workspace cudaFreeAsync: %s", cudaGetErrorString(e));
+        rc = 3;
+    }
+    return rc;
+}
+
 // Host-side argument checks shared by the entry points (dtype, algo, sizes,
 // pointers, 16-byte alignment); 0 or an attn_status code with a message.
 int validate(const void *q, const void *k, const void *v, const void *o, const float *lse,
@@ -108,6 +132,11 @@ int launch_bwd(const BwdParams &bp, int dtype, int mode, cudaStream_t stream);
 
 struct Q8Cache;
 
+// Checks of an 8-bit cache that its entry points share.
+int validate_cache(const void *k_pages, const void *v_pages, const float *k_scale,
+                   const float *v_scale, int Hkv, int D, int Dv, int max_pages, int page_size,
+                   int num_pages, int block_size, int cache_dtype);
+
 // New rows into the cache; every size is positive (checked by the entry point).
 int launch_cache_append(const void *k, const void *v, void *k_pages, void *v_pages, float *k_scale,
                         float *v_scale, int B, int N, int Hkv, int D, int Dv,
@@ -128,6 +157,29 @@ bool q8_decode_wins(const AttnParams &p, int nsm);
 unsigned long long q8_decode_workspace(const AttnParams &p, int nsm);
 int launch_q8_decode(const AttnParams &p, const Q8Cache &c, int dtype, int nsm, void *ws,
                      cudaStream_t stream);
+
+// ---- the position rotation (rope.cuh)
+
+struct RopeArgs;
+
+// Elements (of es bytes) of the vectors that a problem's widths, strides and addresses
+// allow; heads of V hold a multiple of v_unit of them.
+int rope_vector(const RopeArgs &a, int es, int v_unit);
+// Rows into rows, or into 16- or 32-bit pages (a.block_table); sizes are positive.
+int launch_rope(const RopeArgs &a, int dtype, cudaStream_t stream);
+// Rows into the 8-bit cache (a.ko, a.vo: its pools).
+int launch_rope_q8(const RopeArgs &a, float *k_scale, float *v_scale, int nblk, int blk_shift,
+                   int code, int dtype, cudaStream_t stream);
+
+// ---- attention over shared beginnings (shared.cuh): the tcgen05 kernels take bf16/fp16,
+// D and Dv multiples of 16 in [64, 128], Hq / Hkv <= 128, pages of 8 rows or more, with a
+// workspace of the given number of bytes at a 16-byte aligned address.
+bool shared_tc_supported(const AttnParams &p, int dtype);
+unsigned long long shared_tc_workspace(const AttnParams &p, int N, int nsm);
+int launch_shared_tc(const AttnParams &p, const int32_t *cu_groups, const int32_t *shared_lens, int N,
+                     int dtype, int nsm, void *ws, cudaStream_t stream);
+
+// ---- pages
 
 constexpr int kMaxPools = 64;  // pools one launch copies
 int launch_pages_copy(const void *const *src_pools, void *const *dst_pools, const long long *bytes,

@@ -509,6 +509,119 @@ ATTN_API int attn_pages_compact(void *const *pools, const long long *page_bytes,
                                 int32_t *refcount_out, int32_t *remap, int32_t *n_live,
                                 attn_stream_t stream);
 
+/*
+ * The position rotation.  A serving and training companion of the attention (the
+ * pages have no counterpart).  The first `rot` columns (even, 0 .. D) of a head
+ * are pairs (x1, x2) -- columns i and i + rot / 2 with ATTN_ROPE_HALF, 2 i and
+ * 2 i + 1 with ATTN_ROPE_ADJACENT -- and become
+ *     y1 = x1 c - x2 s,   y2 = x2 c + x1 s,   c = cos[pos, i],  s = sin[pos, i]
+ * for tables cos, sin of float32 [max_pos, rot / 2] on the device; the other
+ * columns are copied.  Products and sums are rounded one by one in fp32 and the
+ * result once to the type.  A row whose position is outside [0, max_pos) has NaN in
+ * its rotated columns.
+ *
+ * attn_rope -- q [B, N, Hq, D] and k [B, N, Hkv, D] to q_out, k_out of those
+ * shapes.  positions: int32 [B, N] on the device, or NULL for row i of each
+ * sequence at position i.  inverse != 0 turns the other way: given gradients of
+ * q_out and k_out it gives those of q and k (the rotation's transpose).  Either of
+ * q and k may be NULL, with 0 heads.
+ *   q_stride, k_stride   elements from one token's row of heads to the next (row
+ *                        (b, i) is b * N + i rows in): Hq * D when dense, more for
+ *                        views of a fused projection
+ * Outputs are dense; each may be its own input where that is dense too (in place),
+ * and overlaps no other one.  Tensors need the alignment of their elements only;
+ * 16-byte aligned ones with widths and strides to match are the fastest.
+ *
+ * attn_rope_append -- the rows of a serving step: q is rotated into q_out, k is
+ * rotated and, like v as it is, written into the pages of attn_fwd_paged behind
+ * the seqlens_k rows each sequence has (seqlens_k is not changed: the caller adds
+ * the new rows to it).  Row i of sequence b goes to its row seqlens_k[b] + i, and
+ * that is its position too unless `positions` says otherwise.
+ *   q [B, N, Hq, D], k [B, N, Hkv, D], v [B, N, Hkv, Dv]   rows, strides as above
+ *                (q and q_out may be NULL together, with Hq 0)
+ *   seqlens_new  int32 [B], new rows of each sequence (clamped to [0, N]), or NULL
+ *                for N of each; q_out gets +0 in the other rows
+ *   cu_seqlens_new   NULL, or int32 [B + 1]: the rows are packed [total_new, ..],
+ *                sequence b's are [cu[b], cu[b + 1]), at most N of them; rows of
+ *                q_out outside every sequence are left as they were
+ *   positions    int32, one for each row of the buffers, or NULL
+ *   rot 0 (cos and sin may be NULL then) appends without a rotation
+ *   k_pages [num_pages, page_size, Hkv, D], v_pages [.., Dv] in `dtype`,
+ *   block_table int32 [B, max_pages], as in attn_fwd_paged.  Every page that gets
+ *                rows must be there already and belong to one sequence only
+ *                (attn_pages_fork sees to both).  Rows whose entry is outside [0,
+ *                num_pages), or past the table, are dropped; nothing else of a page
+ *                is written.
+ * attn_rope_append_q8 -- the same into the 8-bit cache: scales, codes and earlier
+ * rows of a block as attn_cache_append writes them, for the rotated keys in fp32
+ * (not rounded to `dtype` first).
+ * Widths in [1, 512].  Return ATTN_OK, ATTN_ERR_INVALID, ATTN_ERR_UNSUPPORTED (2^31
+ * or more blocks of rows in a sequence) or ATTN_ERR_CUDA; one launch, no workspace;
+ * asynchronous on `stream`.
+ */
+enum attn_rope_pairs { ATTN_ROPE_HALF = 0, ATTN_ROPE_ADJACENT = 1 };
+ATTN_API int attn_rope(const void *q, const void *k, void *q_out, void *k_out, const float *cos,
+                       const float *sin, int B, int N, int Hq, int Hkv, int D, int rot,
+                       int max_pos, long long q_stride, long long k_stride,
+                       const int32_t *positions, int pairs, int inverse, int dtype,
+                       attn_stream_t stream);
+ATTN_API int attn_rope_append(const void *q, const void *k, const void *v, void *q_out,
+                              void *k_pages, void *v_pages, const float *cos, const float *sin,
+                              int B, int N, int total_new, int Hq, int Hkv, int D, int Dv, int rot,
+                              int max_pos, long long q_stride, long long k_stride,
+                              long long v_stride, const int32_t *seqlens_new,
+                              const int32_t *cu_seqlens_new, const int32_t *positions, int pairs,
+                              const int32_t *seqlens_k, const int32_t *block_table, int max_pages,
+                              int page_size, int num_pages, int dtype, attn_stream_t stream);
+ATTN_API int attn_rope_append_q8(const void *q, const void *k, const void *v, void *q_out,
+                                 void *k_pages, void *v_pages, float *k_scale, float *v_scale,
+                                 const float *cos, const float *sin, int B, int N, int total_new,
+                                 int Hq, int Hkv, int D, int Dv, int rot, int max_pos,
+                                 long long q_stride, long long k_stride, long long v_stride,
+                                 const int32_t *seqlens_new, const int32_t *cu_seqlens_new,
+                                 const int32_t *positions, int pairs, const int32_t *seqlens_k,
+                                 const int32_t *block_table, int max_pages, int page_size,
+                                 int num_pages, int block_size, int cache_dtype, int dtype,
+                                 attn_stream_t stream);
+
+/*
+ * attn_fwd_paged_shared -- attn_fwd_paged (bottom-right causal mask, no window) for a
+ * batch whose sequences begin alike, such as beams and samples of one prompt or
+ * requests behind one system prompt: the keys that a group shares are read once
+ * for the rows of all its members, and the results joined with those of the keys
+ * that each sequence has alone.
+ *   q [B, Q, Hq, D], pages, block_table [B, max_pages], seqlens_q, seqlens_k, o,
+ *   lse as in attn_fwd_paged (seqlens_k counts all keys of a sequence)
+ *   cu_groups    int32 [num_groups + 1] on the device, ascending: group n is the
+ *                sequences [cu_groups[n], cu_groups[n + 1]) of the batch; the others
+ *                share nothing
+ *   shared_lens  int32 [num_groups] on the device: the first shared_lens[n] keys of
+ *                the members are the same -- their table entries name the same pages,
+ *                or pages of equal contents (a partly filled page copied for each, as
+ *                attn_pages_fork does).  They are read through the table of the first
+ *                member, and never past its length; members may be shorter than that.
+ *   scale        finite
+ * Kernels (`algo`): ATTN_ALGO_AUTO and ATTN_ALGO_TCGEN05 take bf16/fp16, D and Dv
+ * multiples of 16 in [64, 128], Hq / Hkv <= 128, pages of 8 rows or more and fewer
+ * than 2^30 rows (B * Q * Hq), with at least one group for AUTO.  AUTO runs other
+ * problems, and the other values of algo run all of theirs, on the kernels of
+ * attn_fwd_paged, which read each sequence's own table for every key.  The tcgen05
+ * kernel rounds probabilities to q's type before the product with V, as attn_fwd
+ * does; partial results are joined in fp32 in a fixed order, so that results do not
+ * depend on timing.  A NaN or infinite value of a key that some row of the batch's
+ * tile attends to may, as in attn_fwd, give NaN to rows of the tile that do not;
+ * scores that are NaN give NaN.  Workspace (about 8 * (Dv + 2) * (2 * B * Q * Hq +
+ * 256 * SMs) bytes) from the library's pool.  Groups that overlap or descend give
+ * wrong results, never a bad address.  Return codes as attn_fwd.
+ */
+ATTN_API int attn_fwd_paged_shared(const void *q, const void *k_pages, const void *v_pages,
+                                   void *o, float *lse, int B, int Hq, int Hkv, int Q, int D,
+                                   int Dv, const int32_t *block_table, int max_pages,
+                                   int page_size, int num_pages, const int32_t *seqlens_q,
+                                   const int32_t *seqlens_k, const int32_t *cu_groups,
+                                   const int32_t *shared_lens, int num_groups, float scale,
+                                   int dtype, int algo, attn_stream_t stream);
+
 /* Message for the calling thread's most recent failed call ("" if none). */
 ATTN_API const char *attn_last_error(void);
 
