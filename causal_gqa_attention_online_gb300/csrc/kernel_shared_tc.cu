@@ -12,16 +12,15 @@
 // leaves a partial result.  Either way step x of a piece belongs to chain x & 1, and
 // the roles are the same:
 //   warps 0-3, 4-7  softmax of chain 0 / 1 (TMEM lane = row = thread)
-//   warp 8          issues all MMAs:  S(0) S(1) [ PV(x) S(x + 2) ] ...
-//   warp 10         finds the pieces and pages, and loads Q, K and V by TMA (a box of a
-//                   page, or of 128 rows of it)
+//   warps 11, 10    issue the MMAs of chain 0 / 1:  S(x) [ PV(x) S(x + 2) ] ...
+//   warp 8          finds the pieces
+//   warp 9          loads Q, K and V by TMA (a box of a page, or of 128 rows of it)
 //   warps 12-15     write finished O out of TMEM to the partials
 // Pieces are handed to the roles through a ring of descriptors, so that loads of the
 // next piece run ahead.  K/V tiles stream through a ring of shared-memory stages.
 //
-// shared_join_kernel.  One warp a row adds up the row's partials (at most two chains of
-// each CTA that its jobs' shares touch) in a fixed order: results do not depend on
-// timing.
+// shared_join_kernel adds up each row's partials (at most two chains of each CTA that its
+// jobs' shares touch) in a fixed order: results do not depend on timing.
 //
 // Bound: HBM for the keys while a group has few rows (a tile of 128 keys for both K and
 // V, D = 128, is 64 KB: 1.5 us of an SM's share of the bandwidth), the softmax and the
@@ -44,10 +43,13 @@ using namespace sm100;
 using namespace tcfwd;
 
 constexpr int kThreads = 512;
-constexpr int kMmaWarp = 8, kLoadWarp = 10, kEpiWarp0 = 12;
-// registers a lane: 2 x 184 (softmax) + 72 + 72 = 512, what 512 threads at 128 have
-constexpr uint32_t kRegsSoftmax = 184, kRegsOther = 72;
-static_assert(2 * kRegsSoftmax + 2 * kRegsOther <= 4 * (65536 / kThreads), "register split");
+// The MMA warps share their schedulers with the softmax's warps of rows 96 .. 127 and
+// 64 .. 95, which have nothing to do while a group has few rows.
+constexpr int kFindWarp = 8, kLoadWarp = 9, kMmaWarp1 = 10, kMmaWarp = 11, kEpiWarp0 = 12;
+// registers a lane: 2 x 176 (softmax) + 104 (MMA, loads, pieces) + 56 (epilogue) = 512,
+// what 512 threads at 128 have
+constexpr uint32_t kRegsSoftmax = 176, kRegsOther = 104, kRegsEpi = 56;
+static_assert(2 * kRegsSoftmax + kRegsOther + kRegsEpi <= 4 * (65536 / kThreads), "register split");
 constexpr uint32_t kChunkBytes = 128 * 128;  // 128 rows of 128 bytes (64 columns)
 constexpr int kPieces = 4;                   // descriptors in flight
 
@@ -55,20 +57,22 @@ struct Piece {
     int nx;          // steps; 0: the end
     int two;         // two tiles of rows
     int qslot;       // one tile: where Q is
-    int kind, b0, tok0, nrows;
-    int lo, end;     // keys of the entity / of this piece's rows
+    int chain0;      // chain of the first step (short pieces take turns)
+    int kind, b0, kvh, tok0, nrows;
+    int lo, end;     // keys of the entity
+    int Qb;          // a sequence's query tokens
     int key0;        // first key of the piece's first tile
     int key_end;     // end of the keys of the piece
-    int pad;
     long long base;  // first row of its partials
+    int pages[2][32];  // lanes' pages of the first tile: K, V
 };
-static_assert(sizeof(Piece) == 56, "descriptor");
+static_assert(sizeof(Piece) == 320, "descriptor");
 
 template <int D, int DV> struct Layout {
     static constexpr int QTILE = 128 * D * 2;
     static constexpr int KTILE = 128 * D * 2, VTILE = 128 * DV * 2;
     static constexpr int STAGE = KTILE > VTILE ? KTILE : VTILE;
-    static constexpr int TAIL = 1024;  // barriers, descriptors, scan
+    static constexpr int TAIL = 2048;  // barriers, descriptors, scan
     static constexpr int NS_FIT = (227 * 1024 - 1024 - TAIL - 2 * QTILE) / STAGE;
     static constexpr int NS = NS_FIT > 10 ? 10 : NS_FIT;
     static constexpr int KV_OFF = 2 * QTILE;
@@ -84,15 +88,20 @@ enum : int {
     B_Q_FULL = 8,      // [2] tiles of Q
     B_Q_EMPTY = 10,    // [2]
     B_S_FULL = 12,     // [2] chains
-    B_P_READY = 14,    // [2]
-    B_O_FULL = 16,     // [2]
-    B_O_EMPTY = 18,    // [2]
-    B_TEARDOWN = 20,
-    B_KV_FULL = 21,    // [NS] full, [NS] empty
+    B_P_READY = 14,    // [2] x [2] halves of a tile's keys
+    B_O_FULL = 18,     // [2]
+    B_O_EMPTY = 20,    // [2]
+    B_TEARDOWN = 22,   // [2]
+    B_ORDER = 24,      // [2] the other chain's MMAs of a tile are issued (two tiles of rows)
+    B_KV_FULL = 26,    // [NS] full, [NS] empty
 };
-constexpr int kBarBytes = (B_KV_FULL + 20) * 8;  // 328
-constexpr int kDescOff = 336, kScanOff = kDescOff + kPieces * (int)sizeof(Piece);  // 560
-static_assert(kBarBytes <= kDescOff && kScanOff + 16 * 8 + 64 <= 1024, "tail of shared memory");
+constexpr int kBarBytes = (B_KV_FULL + 20) * 8;  // 368
+constexpr int kDescOff = 368, kScanOff = kDescOff + kPieces * (int)sizeof(Piece);  // 1648
+constexpr int kBeginOff = kScanOff + 16 * 8, kSlotOff = kBeginOff + (int)sizeof(SharedBegin);
+static_assert(kBarBytes <= kDescOff && kSlotOff + 8 <= 2048, "tail of shared memory");
+// Lengths that are copied to shared memory (in place of the first tiles) while the shares
+// are found.
+constexpr int kCopied = 2048;
 
 template <typename T, int D, int DV>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -110,10 +119,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t bars = base + L::TAIL_OFF;
     auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
     Piece *desc = reinterpret_cast<Piece *>(tail + kDescOff);
-    long long *scan = reinterpret_cast<long long *>(tail + kScanOff);        // [16] warps' sums
-    long long *found = scan + 16;                                            // entity's first cost
-    int *found_e = reinterpret_cast<int *>(found + 1);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(found + 2);
+    long long *scan = reinterpret_cast<long long *>(tail + kScanOff);  // [16] warps' sums
+    SharedBegin *begin = reinterpret_cast<SharedBegin *>(tail + kBeginOff);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tail + kSlotOff);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const AttnParams &p = a.p;
@@ -122,27 +130,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // the join (a programmatic dependent launch) may be scheduled; it waits for this grid
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-    if (tid == 0) {
-        for (int i = 0; i < kPieces; ++i) {
-            mbar_init(bar(B_DESC_FULL + i), 1);
-            mbar_init(bar(B_DESC_EMPTY + i), 13);  // the MMA warp, 8 softmax and 4 epilogue warps
-        }
-        for (int t = 0; t < 2; ++t) {
-            mbar_init(bar(B_Q_FULL + t), 1);
-            mbar_init(bar(B_Q_EMPTY + t), 1);
-            mbar_init(bar(B_S_FULL + t), 1);
-            mbar_init(bar(B_P_READY + t), 128);
-            mbar_init(bar(B_O_FULL + t), 1);
-            mbar_init(bar(B_O_EMPTY + t), 128);
-        }
-        mbar_init(bar(B_TEARDOWN), 1);
-        for (int s = 0; s < NS; ++s) {
-            mbar_init(bar(B_KV_FULL + s), 1);
-            mbar_init(bar(B_KV_FULL + NS + s), 1);
-        }
-        *abort_flag = 0;
-        *found_e = a.N + p.B;
+    if (tid < B_KV_FULL + 2 * NS) {
+        // arrivals: descriptors go to the load warp, 2 MMA, 8 softmax and 4 epilogue warps;
+        // Q and the ring's slots come back from both MMA warps
+        const int i = tid;
+        const uint32_t n = i < B_DESC_EMPTY ? 1 : i < B_Q_FULL ? 15 : i < B_Q_EMPTY ? 1 : i < B_S_FULL ? 2
+                         : i < B_P_READY ? 1 : i < B_O_FULL ? 4 : i < B_O_EMPTY ? 1 : i < B_TEARDOWN ? 4
+                         : i < B_KV_FULL + NS ? 1 : 2;
+        mbar_init(bar(i), n);
         fence_mbar_init();
+    }
+    if (tid == 0) {
+        *abort_flag = 0;
+        begin->e = a.entities;
     }
     if (warp == kMmaWarp) {
         tmem_alloc(smem_addr(tmem_slot), 512);
@@ -155,15 +155,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tmV);
     }
 
-    // ---- the share: sums of the entities' costs, a run of them a thread
-    const int E = a.N + p.B, run = (E + kThreads - 1) / kThreads;
+    // ---- the share: sums of the entities' costs, a run of them a thread.  The lengths
+    // are copied first: what an entity costs hangs on several loads, one after the other.
+    const int E = a.entities, run = (E + kThreads - 1) / kThreads;
+    SharedLens z = shared_lens_of(a);
+    if (a.N < kCopied && p.B <= kCopied) {
+        int32_t *to = reinterpret_cast<int32_t *>(gbase + L::KV_OFF);
+        for (int i = tid; i <= a.N; i += kThreads) {
+            to[i] = z.cu[i];
+            if (i < a.N) to[kCopied + i] = z.shared[i];
+        }
+        for (int i = tid; i < p.B; i += kThreads) {
+            to[2 * kCopied + i] = z.k[i];
+            if (z.q) to[3 * kCopied + i] = z.q[i];
+        }
+        z = {to, to + kCopied, to + 2 * kCopied, z.q ? to + 3 * kCopied : nullptr};
+        __syncthreads();
+    }
     const int e0 = min(tid * run, E), e1 = min(e0 + run, E);
     long long mine = 0;
+    int n = -1;
     for (int e = e0; e < e1; ++e) {
-        const int n = e >= a.N ? shared_group_of(a, e - a.N) : -1;
-        const SharedEntity x = shared_entity(a, e, n);
+        n = e >= a.N ? shared_group_of(a, z, e - a.N) : -1;
+        const SharedEntity x = shared_entity(a, z, e, n);
         mine += (long long)x.jobs * x.cj;
-        if (blockIdx.x == 0 && e >= a.N) a.group[e - a.N] = n;
     }
     long long incl = mine;
 #pragma unroll
@@ -181,23 +196,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (w < warp) before += scan[w];
         W += scan[w];
     }
-    const long long x0 = shared_bound(W, blockIdx.x, a.ctas), x1 = shared_bound(W, blockIdx.x + 1, a.ctas);
-    const bool here = x0 < x1 && before <= x0 && x0 < before + mine;
-    if (here || blockIdx.x == 0) {
+    const int shares = shared_ctas(W, a.ctas);
+    const long long x0 = shared_bound(W, blockIdx.x, shares), x1 = shared_bound(W, blockIdx.x + 1, shares);
+    if (x0 < x1 && before <= x0 && x0 < before + mine) {  // the share begins in this thread's run
         long long at = before;
-        for (int e = e0; e < e1; ++e) {
-            const int n = e >= a.N ? shared_group_of(a, e - a.N) : -1;
-            const SharedEntity x = shared_entity(a, e, n);
-            const long long c = (long long)x.jobs * x.cj;
-            if (here && at <= x0 && x0 < at + c) {
-                *found = at;
-                *found_e = e;
+        int e = e0;
+        if (run > 1)
+            for (;; ++e) {
+                n = e >= a.N ? shared_group_of(a, z, e - a.N) : -1;
+                const SharedEntity x = shared_entity(a, z, e, n);
+                const long long c = (long long)x.jobs * x.cj;
+                if (x0 < at + c) break;
+                at += c;
             }
-            if (blockIdx.x == 0) a.start[e] = at;
-            at += c;
-        }
-        if (blockIdx.x == 0 && tid == 0) a.start[E] = W;
+        *begin = shared_begin(a, z, e, n, at);
     }
+    fence_proxy_async_smem();  // the copies' place is the loads' from here on
     __syncthreads();
     const uint32_t tmem = *tmem_slot;
     auto kv_full = [&](int s) { return bar(B_KV_FULL + s); };
@@ -207,52 +221,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp >= 8 && warp < kEpiWarp0) {
         regs_decrease<kRegsOther>();
         if (warp == kLoadWarp) {
-            // ------------------------------------------------- pieces and loads
-            SharedWalker wk(a, x0, x1, *found, *found_e);
+            // ------------------------------------------------------------ loads
             const int page = p.page_size, box = min(page, 128);  // rows of a box of keys
             constexpr int KC = D / 64, VC = DV / 64;             // boxes of 64 columns
-            uint32_t it = 0;      // fills of the ring
+            uint32_t it = 0;          // fills of the ring
             uint32_t nq[2] = {0, 0};  // fills of either Q tile
-            uint32_t armed = 0;   // ring slots that were filled
-            int qslot = 0;
+            uint32_t armed = 0;       // ring slots that were filled
             bool ok = true;
             for (uint32_t np = 0; ok; ++np) {
-                SharedJob k;
-                int t0 = 0, t1 = 0;
-                const bool more = wk.next(k, t0, t1);
                 const int slot = (int)(np % kPieces);
-                if (!warp_wait(bar(B_DESC_EMPTY + slot), ((np / kPieces) & 1u) ^ 1u, abort_flag, wl)) {
+                if (!warp_wait(bar(B_DESC_FULL + slot), (np / kPieces) & 1u, abort_flag, wl)) {
                     ok = false;
                     break;
                 }
-                const bool two = more && k.ntok > a.tile_tokens;
-                const int key0 = wk.x.kv_start + t0 * 128;
-                const int key_end = min(k.end, wk.x.kv_start + t1 * 128);
-                if (more && !two) qslot ^= 1;
-                if (lane == 0) {
-                    Piece d = {};
-                    if (more) {
-                        d.nx = two ? 2 * (t1 - t0) : t1 - t0;
-                        d.two = two;
-                        d.qslot = qslot;
-                        d.kind = wk.x.kind;
-                        d.b0 = wk.x.b0;
-                        d.tok0 = k.tok0;
-                        d.nrows = k.ntok * p.G;
-                        d.lo = wk.x.lo;
-                        d.end = wk.x.end;
-                        d.key0 = key0;
-                        d.key_end = key_end;
-                        d.base = shared_base(k.row0, blockIdx.x);
-                    }
-                    desc[slot] = d;
-                    mbar_arrive(bar(B_DESC_FULL + slot));
-                }
+                const volatile Piece *d = desc + slot;
+                const int nx = d->nx, two = d->two, qslot = d->qslot, kind = d->kind, kvh = d->kvh, tok0 = d->tok0;
+                const int key0 = d->key0, key_end = d->key_end, nt = two ? nx >> 1 : nx;
+                const int32_t *table = p.block_table + (long long)d->b0 * p.max_pages;
+                int pk = d->pages[0][lane], pv = d->pages[1][lane];
                 __syncwarp();
-                if (!more) break;
+                if (lane == 0) mbar_arrive(bar(B_DESC_EMPTY + slot));
+                if (nx == 0) break;
                 // Q: a box of a tile's tokens with the heads of the group
-                const CUtensorMap *tq = wk.x.kind == 0 ? &tmQ : &tmOwn;
-                const int qtok = wk.x.kind == 0 ? a.tile_tokens : min(p.Q, a.tile_tokens);
+                const int qtok = kind == 0 ? a.tile_tokens : min(p.Q, a.tile_tokens);
                 for (int t = 0; t < (two ? 2 : 1) && ok; ++t) {
                     const int qs = two ? t : qslot;
                     if (!warp_wait(bar(B_Q_EMPTY + qs), (nq[qs] & 1u) ^ 1u, abort_flag, wl)) {
@@ -260,28 +251,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                         break;
                     }
                     ++nq[qs];
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(bar(B_Q_FULL + qs), (uint32_t)(qtok * p.G * 128 * KC));
-                        for (int c = 0; c < KC; ++c)
-                            tma_load_4d(base + qs * L::QTILE + c * kChunkBytes, tq, bar(B_Q_FULL + qs),
-                                        c * 64, k.kvh * p.G, k.tok0 + t * a.tile_tokens, 0);
-                    }
+                    if (lane == 0) mbar_arrive_expect_tx(bar(B_Q_FULL + qs), (uint32_t)(qtok * p.G * 128 * KC));
+                    __syncwarp();
+                    if (lane < KC)
+                        tma_load_4d(base + qs * L::QTILE + lane * kChunkBytes, kind == 0 ? &tmQ : &tmOwn,
+                                    bar(B_Q_FULL + qs), lane * 64, kvh * p.G, tok0 + t * a.tile_tokens, 0);
                     __syncwarp();
                 }
                 // K and V: lane l's box of a tile is page l / columns, columns l % columns
-                const int32_t *table = p.block_table + (long long)wk.x.b0 * p.max_pages;
                 auto entry = [&](int j, int pages) -> int {
                     const int key = key0 + j * 128 + pages * box;
                     if (key >= key_end) return 0;
                     return min(max(__ldg(table + (key >> p.page_shift)), 0), p.num_pages - 1);
                 };
-                int pk = entry(0, lane / KC), pv = KC == VC ? pk : entry(0, lane / VC);
-                for (int j = 0; j < t1 - t0 && ok; ++j) {
+                for (int j = 0; j < nt && ok; ++j) {
                     const int k0 = key0 + j * 128;
                     const int nb = (min(128, key_end - k0) + box - 1) / box;  // boxes of rows
                     const int inpage = k0 & (page - 1);
                     const int krow = (pk << p.page_shift) + inpage, vrow = (pv << p.page_shift) + inpage;
-                    if (j + 1 < t1 - t0) {
+                    if (j + 1 < nt) {
                         pk = entry(j + 1, lane / KC);
                         pv = KC == VC ? pk : entry(j + 1, lane / VC);
                     }
@@ -299,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int pg = lane / nc, c = lane - pg * nc;
                         if (pg < nb)
                             tma_load_4d(stage(s) + c * kChunkBytes + pg * box * 128, which ? &tmV : &tmK,
-                                        kv_full(s), c * 64, k.kvh, which ? vrow : krow, 0);
+                                        kv_full(s), c * 64, kvh, which ? vrow : krow, 0);
                         __syncwarp();
                     }
                 }
@@ -315,10 +303,77 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mbar_wait_drain(kv_full(s), last & 1u);
                     }
             }
-        } else if (warp == kMmaWarp) {
-            // ------------------------------------------------------ MMA issuer
-            uint32_t kv = 0;  // fills used
-            uint32_t q_ph = 0, p_ph = 0, oe_ph = 0;  // parities, a bit a tile / chain
+        } else if (warp == kFindWarp) {
+            // ------------------------------------------------------------ pieces
+            constexpr int KC = D / 64, VC = DV / 64;
+            const int box = min(p.page_size, 128);
+            SharedWalker wk(a, x0, x1, *begin);
+            int qslot = 0, chain = 0;
+            for (uint32_t np = 0;; ++np) {
+                SharedJob k;
+                int t0 = 0, t1 = 0;
+                const bool more = wk.next(k, t0, t1);
+                const int key0 = wk.s.x.kv_start + t0 * 128, key_end = min(k.end, wk.s.x.kv_start + t1 * 128);
+                int pk = 0, pv = 0;
+                if (more) {  // the first tile's pages; every entry of a key before key_end is there
+                    const int32_t *table = p.block_table + (long long)wk.s.x.b0 * p.max_pages;
+                    const int ka = key0 + lane / KC * box, va = key0 + lane / VC * box;
+                    if (ka < key_end) pk = min(max(__ldg(table + (ka >> p.page_shift)), 0), p.num_pages - 1);
+                    if (KC == VC) pv = pk;
+                    else if (va < key_end) pv = min(max(__ldg(table + (va >> p.page_shift)), 0), p.num_pages - 1);
+                }
+                const int slot = (int)(np % kPieces);
+                if (!warp_wait(bar(B_DESC_EMPTY + slot), ((np / kPieces) & 1u) ^ 1u, abort_flag, wl)) {
+                    if (lane == 0) raise_abort(abort_flag, p.status, kStatusTimeoutShared);
+                    break;
+                }
+                Piece &d = desc[slot];
+                d.pages[0][lane] = pk;
+                d.pages[1][lane] = pv;
+                const bool two = more && k.ntok > a.tile_tokens;
+                if (more && !two) qslot ^= 1;
+                if (lane == 0) {
+                    d.nx = !more ? 0 : two ? 2 * (t1 - t0) : t1 - t0;
+                    if (more) {
+                        d.two = two;
+                        d.qslot = qslot;
+                        d.chain0 = two ? 0 : chain;
+                        d.kind = wk.s.x.kind;
+                        d.b0 = wk.s.x.b0;
+                        d.kvh = k.kvh;
+                        d.tok0 = k.tok0;
+                        d.nrows = k.ntok * p.G;
+                        d.lo = wk.s.x.lo;
+                        d.end = wk.s.x.end;
+                        d.Qb = wk.s.x.Qb;
+                        d.key0 = key0;
+                        d.key_end = key_end;
+                        d.base = shared_base(k.at, p.G, blockIdx.x);
+                        int2 *sp = a.span[wk.s.x.kind] + k.at;
+                        if (t0 == 0) sp->x = blockIdx.x;
+                        if (t1 == k.nt) sp->y = blockIdx.x;
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_DESC_FULL + slot));
+                if (!more) break;
+                if (!two) chain ^= (t1 - t0) & 1;
+            }
+        } else if (warp == kMmaWarp || warp == kMmaWarp1) {
+            // -------------------------------------- MMA issuers, one a chain
+            // The chain is  S(j) [softmax] PV(j) S(j')  ...: P comes in two halves, so that the
+            // product with the first one runs while the softmax is at the second.  (S in
+            // halves of 64 keys and two buffers, always one ahead, is slower: an MMA of 64
+            // columns takes as long as one of 128, the rows of Q have to be read for either.)
+            // What a tile needs beside P is waited for while the softmax runs.  Of the key
+            // tiles that belong to the other chain alone a warp only sees that they landed,
+            // and gives up its half of their slots.
+            const int t = warp == kMmaWarp ? 0 : 1;
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint32_t s_tm = tm + (uint32_t)t * 128u, o_tm = tm + (uint32_t)(L::O_COL + t * DV);
+            uint32_t kv = 0;  // fills of the pieces before
+            uint32_t q_ph = 0, p_ph = 0, oe_ph = 0;  // parities (a bit a tile of Q, a half)
+            uint32_t turn = 0;
             bool ok = true;
             for (uint32_t np = 0; ok; ++np) {
                 const int slot = (int)(np % kPieces);
@@ -327,103 +382,130 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 const volatile Piece *d = desc + slot;
-                const int nx = d->nx, two = d->two, qslot = d->qslot, key0 = d->key0, key_end = d->key_end;
+                // (shuffles: the compiler sees that the warp's values are one)
+                const int nx = __shfl_sync(0xffffffffu, d->nx, 0), two = __shfl_sync(0xffffffffu, d->two, 0);
+                const int qslot = __shfl_sync(0xffffffffu, d->qslot, 0), key0 = __shfl_sync(0xffffffffu, d->key0, 0);
+                const int key_end = __shfl_sync(0xffffffffu, d->key_end, 0);
+                const int chain0 = __shfl_sync(0xffffffffu, d->chain0, 0);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(B_DESC_EMPTY + slot));
                 if (nx == 0) break;
-                for (int t = 0; t < (two ? 2 : 1); ++t) {
-                    const int qs = two ? t : qslot;
-                    if (!warp_wait(bar(B_Q_FULL + qs), (q_ph >> qs) & 1u, abort_flag, wl)) ok = false;
-                    q_ph ^= 1u << qs;
-                }
-                if (!ok) break;
-                auto tile_of = [&](int x) { return two ? x >> 1 : x; };
-                // S of step x into its chain's columns; the last user of K releases it
-                auto issue_s = [&](int x) -> bool {
-                    const int t = x & 1, j = tile_of(x);
-                    const uint32_t f = kv + 2u * (uint32_t)j;
-                    const int s = (int)(f % NS);
-                    if (!(two && t == 1) && !warp_wait(kv_full(s), (f / NS) & 1u, abort_flag, wl)) return false;
-                    tc_fence_after();
-                    if (lane == 0) {
-                        const int qs = two ? t : qslot;
-                        const uint64_t qd = sw128_desc(base + qs * L::QTILE, 16, 1024);
-                        const uint64_t kd = sw128_desc(stage(s), 16, 1024);
-                        // only the key columns in use, in sixteens; the softmax masks
-                        // what is stale behind them
-                        const uint32_t ncols = (uint32_t)((min(128, key_end - (key0 + j * 128)) + 15) & ~15);
-                        const uint32_t idesc = (a.idesc_s & ~(0x3Fu << 17)) | ((ncols >> 3) << 17);
-#pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint32_t off = ((kk / 4) * kChunkBytes + (kk % 4) * 32) >> 4;
-                            mma_ss(tmem + (uint32_t)t * 128u, qd + off, kd + off, idesc, kk > 0);
-                        }
-                        mma_commit(bar(B_S_FULL + t));
-                        if (!two || t == 1) mma_commit(kv_empty(s));
-                        if (two ? x >= nx - 2 : x == nx - 1) mma_commit(bar(B_Q_EMPTY + qs));
-                    }
-                    __syncwarp();
+                const int nj = two ? nx >> 1 : nx;  // key tiles
+                const int qs = two ? t : qslot;
+                const uint64_t qd = sw128_desc(base + qs * L::QTILE, 16, 1024);
+                auto landed = [&](uint32_t f) -> bool {
+                    return warp_wait(kv_full((int)(f % NS)), (f / NS) & 1u, abort_flag, wl);
+                };
+                auto pass = [&](uint32_t f) -> bool {  // K or V of a tile of the other chain
+                    if (!landed(f)) return false;
+                    if (lane == 0) mbar_arrive(kv_empty((int)(f % NS)));
                     return true;
                 };
-                ok = issue_s(0) && (nx < 2 || issue_s(1));
-                for (int x = 0; x < nx && ok; ++x) {
-                    const int t = x & 1, j = tile_of(x);
-                    const uint32_t f = kv + 2u * (uint32_t)j + 1u;
-                    const int s = (int)(f % NS);
-                    const int nvalid = min(128, key_end - (key0 + j * 128));
-                    const int ksteps = (nvalid + 15) / 16;
-                    if (!(two && t == 1)) {
-                        if (!warp_wait(kv_full(s), (f / NS) & 1u, abort_flag, wl)) {
-                            ok = false;
-                            break;
-                        }
-                        // V rows behind the last key may hold anything: zeros, so that
-                        // their P = 0 adds 0
-                        const int nzero = ksteps * 16 - nvalid;
-                        if (nzero > 0) {
-                            uint8_t *vt = gbase + (stage(s) - base) + nvalid * 128;
+                // S of the keys in the ring's slot s.  Only the columns in use, in sixteens; the
+                // softmax masks what is stale behind them.
+                auto issue_s = [&](int s, int keys) {
+                    tc_fence_after();
+                    const uint32_t ncols = (uint32_t)((keys + 15) & ~15);
+                    warp_mma_ss<D / 16>(s_tm, qd, sw128_desc(stage(s), 16, 1024),
+                                        (a.idesc_s & ~(0x3Fu << 17)) | ((ncols >> 3) << 17));
+                };
+                // PV of a half, whose P is waited for
+                auto issue_pv = [&](int s, int half, int keys, uint32_t accumulate) -> bool {
+                    if (!warp_wait(bar(B_P_READY + 2 * t + half), (p_ph >> half) & 1u, abort_flag, wl)) return false;
+                    p_ph ^= 1u << half;
+                    tc_fence_after();
+                    const uint64_t vd = sw128_desc(stage(s) + half * 64 * 128, kChunkBytes, 1024);
+                    if (keys > 48) {
+                        warp_mma_ts4(o_tm, s_tm + half * 32, vd, a.idesc_o, accumulate);
+                    } else {
+                        for (int kk = 0; kk * 16 < keys; ++kk)
+                            warp_mma_ts(o_tm, s_tm + half * 32 + kk * 8, vd + (kk * 2048 >> 4), a.idesc_o,
+                                        accumulate | (kk > 0));
+                    }
+                    return true;
+                };
+                // V rows behind the last key may hold anything: zeros, so that their P = 0
+                // adds 0 (with two tiles of rows either warp writes the same ones)
+                auto zero_tail = [&](int s, int nvalid) {
+                    const int nzero = ((nvalid + 15) & ~15) - nvalid;
+                    if (nzero == 0) return;
+                    uint8_t *vt = gbase + (stage(s) - base) + nvalid * 128;
 #pragma unroll
-                            for (int c = 0; c < DV / 64; ++c)
-                                for (int i = lane; i < nzero * 8; i += 32)
-                                    *reinterpret_cast<uint4 *>(vt + c * kChunkBytes + i * 16) = make_uint4(0, 0, 0, 0);
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                        }
+                    for (int c = 0; c < DV / 64; ++c)
+                        for (int i = lane; i < nzero * 8; i += 32)
+                            *reinterpret_cast<uint4 *>(vt + c * kChunkBytes + i * 16) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                };
+                auto keys_of = [&](int j) { return min(128, key_end - (key0 + j * 128)); };
+                auto o_free = [&]() -> bool {  // the chain's O of the last piece has been read
+                    const bool w = warp_wait(bar(B_O_EMPTY + t), oe_ph ^ 1u, abort_flag, wl);
+                    oe_ph ^= 1u;
+                    return w;
+                };
+                if (!warp_wait(bar(B_Q_FULL + qs), (q_ph >> qs) & 1u, abort_flag, wl)) {
+                    ok = false;
+                    break;
+                }
+                q_ph ^= two ? 3u : 1u << qs;  // (with two tiles each warp waits for its own)
+                const int step = two ? 1 : 2, j0 = two ? 0 : t ^ chain0;
+                if (j0 == 1 && (!pass(kv) || !pass(kv + 1u))) ok = false;
+                if (j0 >= nj && lane == 0) mbar_arrive(bar(B_Q_EMPTY + qs));  // no tile of ours
+                // S of tile j, which has landed, and what it lets go of
+                auto step_s = [&](int j) {
+                    const int s = (int)((kv + 2u * (uint32_t)j) % NS);
+                    issue_s(s, keys_of(j));
+                    warp_mma_commit(bar(B_S_FULL + t));
+                    warp_mma_commit(kv_empty(s));
+                    if (j + step >= nj) {  // the last use of Q, whose barriers count two
+                        warp_mma_commit(bar(B_Q_EMPTY + qs));
+                        if (two) warp_mma_commit(bar(B_Q_EMPTY + qs));
                     }
-                    if (x < 2) {  // the chain's O of the last piece has been read
-                        if (!warp_wait(bar(B_O_EMPTY + t), ((oe_ph >> t) & 1u) ^ 1u, abort_flag, wl)) {
-                            ok = false;
-                            break;
-                        }
-                        oe_ph ^= 1u << t;
-                    }
-                    if (!warp_wait(bar(B_P_READY + t), (p_ph >> t) & 1u, abort_flag, wl)) {
+                };
+                if (ok && j0 < nj) {
+                    ok = landed(kv + 2u * (uint32_t)j0);
+                    if (ok) step_s(j0);
+                }
+                for (int j = j0; j < nj && ok; j += step) {
+                    const uint32_t f = kv + 2u * (uint32_t)j;
+                    const int sv = (int)((f + 1u) % NS), keys = keys_of(j);
+                    const bool last = j + step >= nj;
+                    if ((!two && j + 1 < nj && !pass(f + 2u)) || !landed(f + 1u) || (j == j0 && !o_free()) ||
+                        (two && !last && !landed(f + 2u))) {
                         ok = false;
                         break;
                     }
-                    p_ph ^= 1u << t;
-                    tc_fence_after();
-                    if (lane == 0) {
-                        const uint64_t vd = sw128_desc(stage(s), kChunkBytes, 1024);
-#pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            if (kk < ksteps)
-                                mma_ts(tmem + (uint32_t)(L::O_COL + t * DV), tmem + (uint32_t)t * 128u + kk * 8,
-                                       vd + (kk * 2048 >> 4), a.idesc_o, (x >= 2 || kk > 0) ? 1u : 0u);
-                        if (!two || t == 1) mma_commit(kv_empty(s));
-                        if (x + 2 >= nx) mma_commit(bar(B_O_FULL + t));
+                    zero_tail(sv, keys);
+                    if (keys > 64) ok = issue_pv(sv, 0, 64, j > j0);
+                    // With two tiles of rows the warps take turns at what closes a tile, so
+                    // that the chains stay half a tile apart: where their MMAs mix, both get
+                    // their S late and then run their softmax at the same time.
+                    if (ok && two) {
+                        ok = warp_wait(bar(B_ORDER + t), (turn & 1u) ^ (t == 0 ? 1u : 0u), abort_flag, wl);
+                        ++turn;
                     }
-                    __syncwarp();
-                    // S(x + 2) overwrites P(x): issued behind PV(x) by the same thread
-                    if (x + 2 < nx) ok = issue_s(x + 2);
+                    if (ok) ok = keys > 64 ? issue_pv(sv, 1, keys - 64, 1u) : issue_pv(sv, 0, keys, j > j0);
+                    if (!ok) break;
+                    // The next K has landed: its S goes right behind PV, and V is released
+                    // after both.
+                    if (two) {
+                        if (!last) step_s(j + step);
+                        if (lane == 0) mbar_arrive(bar(B_ORDER + (t ^ 1)));
+                    }
+                    warp_mma_commit(kv_empty(sv));
+                    if (last) warp_mma_commit(bar(B_O_FULL + t));
+                    if (two) continue;
+                    if (j + 1 < nj && !pass(f + 3u)) ok = false;
+                    if (ok && !last) {
+                        ok = landed(f + 4u);
+                        if (ok) step_s(j + step);
+                    }
                 }
-                kv += 2u * (uint32_t)(two ? nx / 2 : nx);
+                kv += 2u * (uint32_t)nj;
             }
             if (!ok && lane == 0) raise_abort(abort_flag, p.status, kStatusTimeoutShared);
-            if (lane == 0) {  // all MMAs have completed before TMEM is released
-                mma_commit(bar(B_TEARDOWN));
-                mbar_wait_drain(bar(B_TEARDOWN), 0);
-            }
+            warp_mma_commit(bar(B_TEARDOWN + t));  // all MMAs have completed before TMEM is released
+            mbar_wait_drain(bar(B_TEARDOWN + t), 0);
             __syncwarp();
         }
     } else if (warp < 8) {
@@ -445,17 +527,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const volatile Piece *d = desc + slot;
             const int nx = d->nx, two = d->two, key0 = d->key0, lo = d->lo, kind = d->kind;
+            const int rel = two ? t : t ^ d->chain0;    // step of the chain's first tile
             const int first = two ? t * tile_rows : 0;  // row of the piece in lane 0
-            const int nrows = min(d->nrows - first, tile_rows);
-            const long long at = d->base + (two ? first : t * d->nrows) + r;
+            const int nrows = min(d->nrows - first, tile_rows), key_end = d->key_end;
+            const long long at = d->base + (two ? first : rel * d->nrows) + r;
             // the row's keys [lo, hi)
             const bool valid = r < nrows;
             int hi = 0;
             if (valid && nx > 0) {
                 const int token = d->tok0 + (first + r) / p.G;
-                const int b = token / p.Q, i = token - b * p.Q;
-                const int len = clamp_len(__ldg(p.seqlens_k + b), p.K);
-                const int Qb = p.seqlens_q ? clamp_len(__ldg(p.seqlens_q + b), p.Q) : p.Q;
+                const int b = p.Q == 1 ? token : token / p.Q, i = token - b * p.Q;
+                int len = d->end, Qb = d->Qb;
+                if (kind == 0) {
+                    len = clamp_len(__ldg(p.seqlens_k + b), p.K);
+                    Qb = p.seqlens_q ? clamp_len(__ldg(p.seqlens_q + b), p.Q) : p.Q;
+                }
                 if (i < Qb) hi = min(len - Qb + i + 1, d->end);
             }
             __syncwarp();
@@ -463,55 +549,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (nx == 0) break;
             const bool idle = !__any_sync(0xffffffffu, valid);  // no row in this warp
             float m_run = -INFINITY, l_run = 0.f;
-            for (int x = t; x < nx; x += 2) {
-                if (!warp_wait(bar(B_S_FULL + t), s_ph, abort_flag, wl)) {
-                    ok = false;
-                    break;
-                }
-                s_ph ^= 1u;
-                if (idle) {
-                    mbar_arrive(bar(B_P_READY + t));
-                    continue;
-                }
-                tc_fence_after();
-                const int k0 = key0 + (two ? x >> 1 : x) * 128;
-                if (!__all_sync(0xffffffffu, !valid || (lo <= k0 && hi >= k0 + 128))) {
-                    // keys outside [lo, hi) become -inf in TMEM, in chunks of 32
-#pragma unroll 1
-                    for (int cc = 0; cc < 4; ++cc) {
-                        const int a0 = min(max(lo - k0 - cc * 32, 0), 32);
-                        const int b0 = min(max(hi - k0 - cc * 32, 0), 32);
-                        const uint32_t below_b = b0 >= 32 ? 0xffffffffu : (1u << b0) - 1u;
-                        const uint32_t below_a = a0 >= 32 ? 0xffffffffu : (1u << a0) - 1u;
-                        const uint32_t keep = below_b & ~below_a;
-                        if (__all_sync(0xffffffffu, keep == 0xffffffffu)) continue;
-                        uint32_t v[32];
-                        tmem_ld32(tS + cc * 32, v);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = ((keep >> i) & 1u) ? v[i] : 0xff800000u;
-                        tmem_st32(tS + cc * 32, v);
-                    }
-                    tmem_st_wait();
-                }
-                uint32_t sr[4][32];
-#pragma unroll
-                for (int cc = 0; cc < 4; ++cc) tmem_ld32(tS + cc * 32, sr[cc]);
-                tmem_ld_wait();
-                float mc[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) mc[i] = -INFINITY;
-#pragma unroll
-                for (int cc = 0; cc < 4; ++cc)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        mc[i & 7] = fmax3(mc[i & 7], __uint_as_float(sr[cc][2 * i]),
-                                          __uint_as_float(sr[cc][2 * i + 1]));
-                const float mx = fmax3(fmax3(mc[0], mc[1], mc[2]), fmax3(mc[3], mc[4], mc[5]),
-                                       fmaxf(mc[6], mc[7]));
-                const float m_tile = mx * c;
-                // O is rescaled only when the maximum grows by more than 2^8: a stale
-                // one serves as well, it is what the sum and the partial refer to
+            // A tile's maximum: the factor for what was summed before, and minus the maximum
+            // to exponentiate with.  O is rescaled only when the maximum grows by more than
+            // 2^8: a stale one serves as well, the partial refers to it.
+            auto step_max = [&](float m_tile, float &neg_m) -> float {
                 float alpha = 1.f;
                 bool rescale = false;
                 if (m_run == -INFINITY) {
@@ -521,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     m_run = m_tile;
                     rescale = true;
                 }
-                const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
+                neg_m = m_run == -INFINITY ? 0.f : -m_run;
                 if (__any_sync(0xffffffffu, rescale)) {
                     // every PV of this chain before S(x) is in O, none after
 #pragma unroll
@@ -534,44 +575,143 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_st16(tO + cc * 16, ov);
                     }
                 }
-                const uint64_t c2 = f2pack(c, c), nm2 = f2pack(neg_m, neg_m);
-                uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t pk[32];
-#pragma unroll
-                    for (int cc = 2 * half; cc < 2 * half + 2; ++cc)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const uint64_t x2 = ffma2(f2pack(__uint_as_float(sr[cc][2 * i]),
-                                                             __uint_as_float(sr[cc][2 * i + 1])), c2, nm2);
-                            float f0, f1;
-                            f2unpack(x2, f0, f1);
-                            const float p0 = ex2(f0), p1 = ex2(f1);
-                            acc2[i & 3] = fadd2(acc2[i & 3], f2pack(p0, p1));
-                            // P is rounded to the storage type, as the MMA takes it; the
-                            // sum is over the unrounded values
-                            pk[(cc & 1) * 16 + i] = pack2<T>(p0, p1);
-                        }
-                    tmem_st32(tS + 32 * half, pk);
-                }
-                float sa[8];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) f2unpack(acc2[i], sa[2 * i], sa[2 * i + 1]);
-                l_run = l_run * alpha + (((sa[0] + sa[1]) + (sa[2] + sa[3])) + ((sa[4] + sa[5]) + (sa[6] + sa[7])));
+                return alpha;
+            };
+            auto p_ready = [&](int half) {
                 tmem_st_wait();
                 tc_fence_before();
-                mbar_arrive(bar(B_P_READY + t));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_P_READY + 2 * t + half));
+            };
+            for (int x = rel; x < nx; x += 2) {
+                const int k0 = key0 + (two ? x >> 1 : x) * 128, keys = min(128, key_end - k0);
+                if (!warp_wait(bar(B_S_FULL + t), s_ph, abort_flag, wl)) {
+                    ok = false;
+                    break;
+                }
+                s_ph ^= 1u;
+                tc_fence_after();
+                if (idle) {  // nothing to do for these rows
+                    p_ready(0);
+                    if (keys > 64) p_ready(1);
+                } else if (__all_sync(0xffffffffu, !valid || (lo <= k0 && hi >= k0 + 128))) {
+                    uint32_t sr[4][32];
+#pragma unroll
+                    for (int cc = 0; cc < 4; ++cc) tmem_ld32(tS + cc * 32, sr[cc]);
+                    tmem_ld_wait();
+                    float mc[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) mc[i] = -INFINITY;
+#pragma unroll
+                    for (int cc = 0; cc < 4; ++cc)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            mc[i & 7] = fmax3(mc[i & 7], __uint_as_float(sr[cc][2 * i]),
+                                              __uint_as_float(sr[cc][2 * i + 1]));
+                    const float mx = fmax3(fmax3(mc[0], mc[1], mc[2]), fmax3(mc[3], mc[4], mc[5]),
+                                           fmaxf(mc[6], mc[7]));
+                    float neg_m;
+                    const float alpha = step_max(mx * c, neg_m);
+                    const uint64_t c2 = f2pack(c, c), nm2 = f2pack(neg_m, neg_m);
+                    uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int cc = 2 * half; cc < 2 * half + 2; ++cc)
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const uint64_t x2 = ffma2(f2pack(__uint_as_float(sr[cc][2 * i]),
+                                                                 __uint_as_float(sr[cc][2 * i + 1])), c2, nm2);
+                                float f0, f1;
+                                f2unpack(x2, f0, f1);
+                                const float p0 = ex2(f0), p1 = ex2(f1);
+                                acc2[i & 3] = fadd2(acc2[i & 3], f2pack(p0, p1));
+                                // P is rounded to the storage type, as the MMA takes it; the
+                                // sum is over the unrounded values
+                                pk[(cc & 1) * 16 + i] = pack2<T>(p0, p1);
+                            }
+                        tmem_st32(tS + 32 * half, pk);
+                        p_ready(half);
+                    }
+                    float sa[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) f2unpack(acc2[i], sa[2 * i], sa[2 * i + 1]);
+                    l_run = l_run * alpha + (((sa[0] + sa[1]) + (sa[2] + sa[3])) + ((sa[4] + sa[5]) + (sa[6] + sa[7])));
+                } else {
+                    // A tile that ends before 128 keys, or where a row's keys do: 32 keys at a
+                    // time, those outside [lo, hi) as -inf, and none past the last that the
+                    // product with V takes.
+                    const int nch = (keys + 31) / 32;
+                    auto load = [&](int cc, uint32_t (&v)[32]) {
+                        const int a0 = min(max(lo - k0 - cc * 32, 0), 32);
+                        const int b0 = min(max(hi - k0 - cc * 32, 0), 32);
+                        const uint32_t below_b = b0 >= 32 ? 0xffffffffu : (1u << b0) - 1u;
+                        const uint32_t below_a = a0 >= 32 ? 0xffffffffu : (1u << a0) - 1u;
+                        const uint32_t keep = below_b & ~below_a;
+                        tmem_ld32(tS + cc * 32, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = ((keep >> i) & 1u) ? v[i] : 0xff800000u;
+                    };
+                    float mx = -INFINITY;
+#pragma unroll 1
+                    for (int cc = 0; cc < nch; ++cc) {
+                        uint32_t v[32];
+                        load(cc, v);
+                        float m4[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) m4[i] = mx;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            m4[i & 3] = fmax3(m4[i & 3], __uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                        mx = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
+                    }
+                    float neg_m;
+                    const float alpha = step_max(mx * c, neg_m);
+                    float sum = 0.f;
+#pragma unroll 1
+                    for (int cc = 0; cc < nch; ++cc) {
+                        uint32_t v[32], pk[16];
+                        load(cc, v);
+                        float s2[2] = {0.f, 0.f};
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float p0 = ex2(fmaf(__uint_as_float(v[2 * i]), c, neg_m));
+                            const float p1 = ex2(fmaf(__uint_as_float(v[2 * i + 1]), c, neg_m));
+                            s2[i & 1] += p0 + p1;
+                            pk[i] = pack2<T>(p0, p1);
+                        }
+                        sum += s2[0] + s2[1];
+                        tmem_st16(tS + 16 * cc, pk);  // over keys that have been read
+                        if (cc == 3 || cc == nch - 1) p_ready(cc >> 1);
+                        else if (cc == 1) p_ready(0);
+                    }
+                    l_run = l_run * alpha + sum;
+                }
             }
-            if (ok && valid && t < nx) a.part_ml[kind][at] = make_float2(m_run, l_run);
+            // (a chain without a step says so)
+            if (ok && valid) a.part_ml[kind][at] = make_float2(m_run, l_run);
         }
         if (!ok && lane == 0) raise_abort(abort_flag, p.status, kStatusTimeoutShared);
     } else {
         // ------------------------------------------------ epilogue warpgroup
-        regs_decrease<kRegsOther>();
+        regs_decrease<kRegsEpi>();
         const int r = (warp & 3) * 32 + lane;
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const int tile_rows = a.tile_tokens * p.G;
+        if (blockIdx.x == 0) {  // for the join, while the first tiles are on their way
+            const SharedLens z = shared_lens_of(a);
+            for (int b = tid - kEpiWarp0 * 32; b < p.B; b += 128) {
+                const int n = shared_group_of(a, z, b);
+                int g0 = b, s = 1, keys = 0;
+                if (n >= 0) {
+                    shared_group(a, z, n, g0, s);
+                    keys = shared_keys(a, z, n, g0, s);
+                }
+                a.info[b] = make_int4(g0, s, keys, 0);
+            }
+        }
         uint32_t o_ph = 0;
         bool ok = true;
         for (uint32_t np = 0; ok; ++np) {
@@ -581,12 +721,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             const volatile Piece *d = desc + slot;
-            const int nx = d->nx, two = d->two, all = d->nrows, kind = d->kind;
+            const int nx = d->nx, two = d->two, all = d->nrows, kind = d->kind, chain0 = d->chain0;
             const long long at = d->base;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(B_DESC_EMPTY + slot));
             if (nx == 0) break;
-            for (int t = 0; t < 2 && t < nx; ++t) {
+            for (int rel = 0; rel < 2 && rel < nx; ++rel) {
+                const int t = rel ^ chain0;
                 if (!warp_wait(bar(B_O_FULL + t), (o_ph >> t) & 1u, abort_flag, wl)) {
                     ok = false;
                     break;
@@ -596,7 +737,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int first = two ? t * tile_rows : 0;
                 const bool valid = r < min(all - first, tile_rows);
                 if (__any_sync(0xffffffffu, valid)) {
-                    float *to = a.part_o[kind] + (at + (two ? first : t * all) + r) * p.Dv;
+                    // (a warp's 32 rows lie side by side: every store is a run of 512 bytes)
+                    const long long row = at + (two ? first : rel * all) + r;
+                    float *to = a.part_o[kind] + (row >> 5) * 32 * p.Dv + (row & 31) * 4;
                     const uint32_t tO = tmem + lane_off + (uint32_t)(L::O_COL + t * DV);
 #pragma unroll
                     for (int cc = 0; cc < DV / 32; ++cc) {
@@ -606,12 +749,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
                             if (valid && cc * 32 + i * 4 < p.Dv)
-                                *reinterpret_cast<uint4 *>(to + cc * 32 + i * 4) =
+                                *reinterpret_cast<uint4 *>(to + (cc * 8 + i) * 128) =
                                     make_uint4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
                     }
                 }
                 tc_fence_before();
-                mbar_arrive(bar(B_O_EMPTY + t));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_O_EMPTY + t));
             }
         }
         if (!ok && lane == 0) raise_abort(abort_flag, p.status, kStatusTimeoutShared);
@@ -627,80 +771,104 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------ the join
 
-constexpr int kJoinWarps = 8;
+// A block joins eight rows: warp w takes columns 16 w .. 16 w + 15 of all of them, four
+// lanes a row, so that a load of the partials (rows side by side) is four runs of 128
+// bytes.  Every warp weighs the partials for itself.
+constexpr int kJoinRows = 8, kJoinUnroll = 4;
 
 template <typename T>
-__global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(const __grid_constant__ SharedArgs a) {
+__global__ void __launch_bounds__(256, 5) shared_join_kernel(const __grid_constant__ SharedArgs a) {
     const AttnParams &p = a.p;
-    const int lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    if (row >= (long long)p.B * p.Q * p.Hq) return;
+    const int lane = threadIdx.x & 31, quarter = lane & 3;
+    const int chunk = (threadIdx.x >> 5) * 4 + quarter;  // columns 4 chunk ..
+    const long long rows = (long long)p.B * p.Q * p.Hq;
+    const long long row0 = (long long)blockIdx.x * kJoinRows + (lane >> 2), row = min(row0, rows - 1);
     const int token = (int)(row / p.Hq), h = (int)(row - (long long)token * p.Hq);
-    const int b = token / p.Q;
-    const long long W = a.start[a.N + p.B];
-    const int n = a.group[b];
-    float M = -INFINITY, L = 0.f;
+    const int b = token / p.Q, i = token - b * p.Q;
+    // (before the wait: what the caller gave)
+    const int len = clamp_len(__ldg(p.seqlens_k + b), p.K);
+    const int Qb = p.seqlens_q ? clamp_len(__ldg(p.seqlens_q + b), p.Q) : p.Q;
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    const int4 in = a.info[b];
+    // where the partials of either job are: chains (one or two) of CTAs [first, last]
+    long long at[2];
+    int two[2], n[2];
+#pragma unroll
+    for (int kind = 0; kind < 2; ++kind) {
+        const SharedRow r = shared_row(a, kind, in.x, in.y, in.z, b, i, h, len, Qb);
+        int2 c = make_int2(0, -1);
+        if (r.some) c = a.span[kind][r.at];
+        // (a launch that gave up leaves them unwritten: never past the partials)
+        c.x = max(c.x, 0), c.y = min(c.y, a.ctas - 1);
+        two[kind] = r.ntok > a.tile_tokens ? 0 : r.ntok * p.G;  // rows from one chain to the other, or 0
+        n[kind] = max(c.y - c.x + 1, 0) << (two[kind] ? 1 : 0);
+        at[kind] = shared_base(r.at, p.G, c.x) + r.lr;
+    }
+    const float2 *ml0 = a.part_ml[0], *ml1 = a.part_ml[1];
+    const float *o0 = a.part_o[0], *o1 = a.part_o[1];
+    if (a.own_splits > 0) {  // the sequence's own keys: parts of them, from the other kernel
+        n[1] = 0;
+        if (i < Qb && len > in.z) {
+            const int per = own_part(in.z, len, a.own_splits);
+            n[1] = (len - (in.z & ~63) + per - 1) / per;
+        }
+        at[1] = row;
+    }
+    const long long part = a.own_splits > 0 ? rows : 256LL;  // from one part or CTA to the next
+    const int all = n[0] + n[1];
+    auto place = [&](int s) -> long long {  // of partial s, kind (s >= n[0])
+        const bool own = s >= n[0];
+        const int k = own ? s - n[0] : s;
+        if (own && a.own_splits > 0) return at[1] + k * part;
+        const int step = own ? two[1] : two[0];
+        return (own ? at[1] : at[0]) + (step ? (k >> 1) * 256LL + (k & 1) * step : k * 256LL);
+    };
+    // the largest maximum: four lanes a row
+    float M = -INFINITY;
+    for (int s = quarter; s < all; s += 4) {
+        const float2 ml = (s >= n[0] ? ml1 : ml0)[place(s)];
+        if (ml.y != 0.f) M = fmaxf(M, ml.x);
+    }
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 1));
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 2));
+    float L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    const bool mine = lane * 4 < p.Dv;
-    for (int kind = n >= 0 ? 0 : 1; kind < 2; ++kind) {
-        const int e = kind == 0 ? n : a.N + b;
-        const SharedRow r = shared_row(a, e, n, a.start[e], W, token, h);
-        if (r.x.nt == 0) continue;
-        const int slots = 2 * (r.c1 - r.c0 + 1);  // two chains of each CTA
-        for (int s0 = 0; s0 < slots; s0 += 32) {
-            const int s = s0 + lane;
-            float m = -INFINITY, l = 0.f;
-            long long at = s < slots ? shared_partial(a, r, W, r.c0 + (s >> 1), s & 1) : -1;
-            if (at >= 0) {
-                const float2 ml = a.part_ml[kind][at];
-                m = ml.x;
-                l = ml.y;
-                if (l == 0.f) at = -1;  // no key of this row (NaN stays)
-            }
-            uint32_t todo = __ballot_sync(0xffffffffu, at >= 0);
-            if (todo == 0) continue;
-            const float mnew = fmaxf(M, warp_max(at >= 0 ? m : -INFINITY));
-            const float keep = M == -INFINITY ? (L == 0.f ? 0.f : 1.f) : exp2f(M - mnew);
-            M = mnew;
-            acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
-            // (a sum that is NaN with no maximum poisons the row)
-            const float w = at >= 0 ? (m == -INFINITY ? 1.f : exp2f(m - M)) : 0.f;
-            L = L * keep + warp_sum(at >= 0 ? w * l : 0.f);
-            while (todo) {
-                float4 v[4];
-                float ws[4];
-                int cnt = 0;
+    for (int s0 = 0; s0 < all; s0 += kJoinUnroll) {
+        float2 ml[kJoinUnroll];
+        float4 v[kJoinUnroll];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    if (todo) {
-                        const int src = __ffs(todo) - 1;
-                        todo &= todo - 1;
-                        ws[u] = __shfl_sync(0xffffffffu, w, src);
-                        const long long from = __shfl_sync(0xffffffffu, at, src);
-                        if (mine) v[u] = *reinterpret_cast<const float4 *>(a.part_o[kind] + from * p.Dv + lane * 4);
-                        cnt = u + 1;
-                    }
-                }
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    if (u < cnt && mine) {
-                        acc.x = fmaf(ws[u], v[u].x, acc.x);
-                        acc.y = fmaf(ws[u], v[u].y, acc.y);
-                        acc.z = fmaf(ws[u], v[u].z, acc.z);
-                        acc.w = fmaf(ws[u], v[u].w, acc.w);
-                    }
+        for (int u = 0; u < kJoinUnroll; ++u) {
+            const int s = s0 + u;
+            ml[u] = make_float2(0.f, 0.f);
+            v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (s < all) {
+                const long long x = place(s);
+                ml[u] = (s >= n[0] ? ml1 : ml0)[x];
+                if (ml[u].y != 0.f)  // (0: no key of this row; NaN stays)
+                    v[u] = *reinterpret_cast<const float4 *>(
+                        s >= n[0] && a.own_splits > 0 ? o1 + x * p.Dv + chunk * 4
+                                                      : (s >= n[0] ? o1 : o0) + (x >> 5) * 32 * p.Dv + (chunk * 32 + (x & 31)) * 4);
             }
         }
+#pragma unroll
+        for (int u = 0; u < kJoinUnroll; ++u) {
+            if (ml[u].y == 0.f) continue;
+            // (a sum that is NaN without a maximum poisons the row)
+            const float w = ml[u].x == -INFINITY ? 1.f : exp2f(ml[u].x - M);
+            L = fmaf(w, ml[u].y, L);
+            acc.x = fmaf(w, v[u].x, acc.x);
+            acc.y = fmaf(w, v[u].y, acc.y);
+            acc.z = fmaf(w, v[u].z, acc.z);
+            acc.w = fmaf(w, v[u].w, acc.w);
+        }
     }
+    if (row0 >= rows) return;
     const float inv = L == 0.f ? 0.f : 1.f / L;
-    if (mine) {
-        uint2 o;
-        o.x = pack2<T>(L == 0.f ? 0.f : acc.x * inv, L == 0.f ? 0.f : acc.y * inv);
-        o.y = pack2<T>(L == 0.f ? 0.f : acc.z * inv, L == 0.f ? 0.f : acc.w * inv);
-        *reinterpret_cast<uint2 *>(static_cast<T *>(p.o) + row * p.Dv + lane * 4) = o;
-    }
-    if (lane == 0 && p.lse) p.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+    uint2 o;
+    o.x = pack2<T>(L == 0.f ? 0.f : acc.x * inv, L == 0.f ? 0.f : acc.y * inv);
+    o.y = pack2<T>(L == 0.f ? 0.f : acc.z * inv, L == 0.f ? 0.f : acc.w * inv);
+    *reinterpret_cast<uint2 *>(static_cast<T *>(p.o) + row * p.Dv + chunk * 4) = o;
+    if (chunk == 0 && p.lse) p.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
 // ------------------------------------------------------------------ host
@@ -717,12 +885,13 @@ unsigned long long layout(SharedArgs &a, void *ws) {
         n += round256(bytes);
         return q;
     };
-    a.start = reinterpret_cast<long long *>(take(8ull * (a.N + (long long)p.B + 1)));
-    a.group = reinterpret_cast<int32_t *>(take(4ull * p.B));
-    const unsigned long long rows = (unsigned long long)shared_rows(p, a.ctas);
+    a.info = reinterpret_cast<int4 *>(take(16ull * p.B));
+    for (int k = 0; k < 2; ++k) a.span[k] = reinterpret_cast<int2 *>(take(8ull * p.B * p.Q * p.Hkv));
+    const unsigned long long rows = ((unsigned long long)shared_rows(p, a.ctas) + 31) / 32 * 32;
     for (int k = 0; k < 2; ++k) {
-        a.part_ml[k] = reinterpret_cast<float2 *>(take(8ull * rows));
-        a.part_o[k] = reinterpret_cast<float *>(take(4ull * rows * p.Dv));
+        const unsigned long long r = k == 1 && a.own_splits > 0 ? (unsigned long long)a.own_splits * p.B * p.Q * p.Hq : rows;
+        a.part_ml[k] = reinterpret_cast<float2 *>(take(8ull * r));
+        a.part_o[k] = reinterpret_cast<float *>(take(4ull * r * p.Dv));
     }
     return n;
 }
@@ -737,6 +906,18 @@ void fill(SharedArgs &a, const AttnParams &p, const int32_t *cu_groups, const in
     a.own_blocks = (p.Q + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens);
     a.tile_align = p.page_size < 128 ? p.page_size : 128;
     a.ctas = nsm > 0 ? nsm : 1;
+    // A sequence's own keys for few rows: the decode's way (keys on M, four warps a unit)
+    // needs a fifth of the time of a tile of 128 rows that are nearly all empty, and none of
+    // its set-up (64 x 250 keys of 8 heads: 12 us).
+    a.own_splits = 0;
+    if (own_decode_supported(p)) {
+        const long long units = (long long)p.B * p.Hkv, want = (4LL * a.ctas + units - 1) / units;
+        const long long most = (p.K + kOwnKeys - 1) / kOwnKeys + 1;
+        a.own_splits = (int)(want < 1 ? 1 : want > 64 ? 64 : want);
+        if (a.own_splits > most) a.own_splits = (int)most;
+    }
+    a.entities = a.own_splits > 0 ? N : N + p.B;
+    a.cost_one = p.D > 64 || p.Dv > 64 ? kCostTile128 : kCostTile64;
 }
 
 template <typename T, int D, int DV>
@@ -767,10 +948,14 @@ int launch_t(SharedArgs &a, bool bf16, cudaStream_t stream) {
         return 3;
     }
     count_launch();
-    const long long rows = (long long)p.B * p.Q * p.Hq, blocks = (rows + kJoinWarps - 1) / kJoinWarps;
+    if (a.own_splits > 0) {
+        rc = launch_own_decode(a, bf16, stream);
+        if (rc) return rc;
+    }
+    const long long rows = (long long)p.B * p.Q * p.Hq, blocks = (rows + kJoinRows - 1) / kJoinRows;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(kJoinWarps * 32);
+    cfg.blockDim = dim3(p.Dv * 2);  // Dv / 16 warps
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

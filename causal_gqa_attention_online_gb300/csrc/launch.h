@@ -179,6 +179,11 @@ unsigned long long shared_tc_workspace(const AttnParams &p, int N, int nsm);
 int launch_shared_tc(const AttnParams &p, const int32_t *cu_groups, const int32_t *shared_lens, int N,
                      int dtype, int nsm, void *ws, cudaStream_t stream);
 
+// The sequences' own keys by the decode's kernel (Q * Hq / Hkv <= 16, widths of 64 or 128).
+struct SharedArgs;
+bool own_decode_supported(const AttnParams &p);
+int launch_own_decode(const SharedArgs &a, bool bf16, cudaStream_t stream);
+
 // ---- pages
 
 constexpr int kMaxPools = 64;  // pools one launch copies

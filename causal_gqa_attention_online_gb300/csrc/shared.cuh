@@ -15,9 +15,10 @@
 
 namespace attn {
 
-// Cost of a piece's start, and of a tile of keys for one and for two tiles of rows, in
-// units of about 0.4 us on one SM (measured: see kernel_shared_tc.cu).
-constexpr int kCostStart = 2, kCostTile = 3, kCostTwo = 4;
+// Costs, in units of about 100 cycles of an SM: of a job's start, and of a tile of keys
+// for one tile of rows (64 or 128 columns of K and V: the latter wait for memory) and for
+// two (measured: see kernel_shared_tc.cu).
+constexpr int kCostStart = 20, kCostTile64 = 20, kCostTile128 = 28, kCostTwo = 36;
 
 struct SharedArgs {
     AttnParams p;
@@ -28,19 +29,24 @@ struct SharedArgs {
     int own_blocks;    // blocks of query tokens of a sequence
     int tile_align;    // keys: tiles of a sequence's own keys start on multiples of it
     int ctas;
+    int entities;      // N + B, or N where another kernel takes the sequences' own keys
+    int own_splits;    // that kernel's parts of a sequence's own keys, or 0
+    int cost_one;      // of a tile of keys for one tile of rows
     float c_scale;     // |scale| * log2(e)  (> 0)
     uint32_t idesc_s, idesc_o;
     // workspace
-    float *part_o[2];  // [kind][rows][Dv]: shared keys, own keys
+    float *part_o[2];  // shared keys, own keys: [rows / 32][Dv / 4][32][4]; of own_splits
+                       // [part][B * Q * Hq][Dv]
     float2 *part_ml[2];  // maximum (log2 units), sum
-    long long *start;  // [N + B + 1] first cost of each entity; the last: W
-    int32_t *group;    // [B] group of each sequence, -1 for none
+    int4 *info;        // [B] of each sequence: its group's first, how many, shared keys
+    int2 *span[2];     // [kind][B * Q * Hkv] first and last CTA of the job that begins there
 };
 
 struct SharedEntity {
     int kind;      // 0 a group's shared keys, 1 a sequence's own
     int b0, s;     // first sequence, how many
     int lo, end;   // keys [lo, end)
+    int Qb;        // a sequence's query tokens
     int kv_start;  // first key of tile 0
     int nt;        // tiles of a job (the most, of a sequence's blocks)
     int blocks;    // of query tokens
@@ -49,43 +55,43 @@ struct SharedEntity {
     int cj;        // cost of a job
 };
 
-__host__ __device__ __forceinline__ int shared_at(const int32_t *p, long long i) {
-#ifdef __CUDA_ARCH__
-    return __ldg(p + i);
-#else
-    return p[i];
-#endif
+// The lengths that the entities depend on: the caller's arrays, or copies of them.
+struct SharedLens {
+    const int32_t *cu, *shared, *k, *q;  // q: null for Q of each
+};
+__host__ __device__ __forceinline__ SharedLens shared_lens_of(const SharedArgs &a) {
+    return {a.cu_groups, a.shared_lens, a.p.seqlens_k, a.p.seqlens_q};
 }
 
 // Group n's sequences [g0, g0 + s).
-__host__ __device__ __forceinline__ void shared_group(const SharedArgs &a, int n, int &g0, int &s) {
-    g0 = clamp_len(shared_at(a.cu_groups, n), a.p.B);
-    s = clamp_len(shared_at(a.cu_groups, n + 1), a.p.B) - g0;
+__host__ __device__ __forceinline__ void shared_group(const SharedArgs &a, const SharedLens &z, int n, int &g0, int &s) {
+    g0 = clamp_len(z.cu[n], a.p.B);
+    s = clamp_len(z.cu[n + 1], a.p.B) - g0;
     if (s < 0) s = 0;
 }
 
 // The keys that the members of a group attend to together: those of the first member,
-// whose table they are read through; none for less than two members.
-__host__ __device__ __forceinline__ int shared_keys(const SharedArgs &a, int n, int g0, int s) {
-    if (s < 2) return 0;
-    const int len = clamp_len(shared_at(a.p.seqlens_k, g0), a.p.K);
-    return clamp_len(shared_at(a.shared_lens, n), len);
+// whose table they are read through.
+__host__ __device__ __forceinline__ int shared_keys(const SharedArgs &a, const SharedLens &z, int n, int g0, int s) {
+    if (s < 1) return 0;
+    const int len = clamp_len(z.k[g0], a.p.K);
+    return clamp_len(z.shared[n], len);
 }
 
 // The group of sequence b, or -1.
-__host__ __device__ __forceinline__ int shared_group_of(const SharedArgs &a, int b) {
+__host__ __device__ __forceinline__ int shared_group_of(const SharedArgs &a, const SharedLens &z, int b) {
     int lo = 0, hi = a.N;  // the last group that begins at or before b
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
-        if (shared_at(a.cu_groups, mid) <= b) lo = mid + 1;
+        if (z.cu[mid] <= b) lo = mid + 1;
         else hi = mid;
     }
     if (lo == 0) return -1;
-    return b < shared_at(a.cu_groups, lo) ? lo - 1 : -1;
+    return b < z.cu[lo] ? lo - 1 : -1;
 }
 
 __host__ __device__ __forceinline__ void shared_cost(const SharedArgs &a, SharedEntity &e, bool two) {
-    e.w = two ? kCostTwo : kCostTile;
+    e.w = two ? kCostTwo : a.cost_one;
     if (e.nt == 0) {  // nothing to do: a little cost, so that no CTA passes over many
         e.jobs = 1;
         e.cj = 1;
@@ -96,14 +102,15 @@ __host__ __device__ __forceinline__ void shared_cost(const SharedArgs &a, Shared
 }
 
 // Entity e of N + B; n: the group of a sequence.
-__host__ __device__ __forceinline__ SharedEntity shared_entity(const SharedArgs &a, int e, int n) {
+__host__ __device__ __forceinline__ SharedEntity shared_entity(const SharedArgs &a, const SharedLens &z, int e, int n) {
     const AttnParams &p = a.p;
     SharedEntity x;
     if (e < a.N) {
         x.kind = 0;
-        shared_group(a, e, x.b0, x.s);
+        x.Qb = 0;
+        shared_group(a, z, e, x.b0, x.s);
         x.lo = 0;
-        x.end = shared_keys(a, e, x.b0, x.s);
+        x.end = shared_keys(a, z, e, x.b0, x.s);
         x.kv_start = 0;
         x.nt = (x.end + 127) >> 7;
         const int tokens = x.s * p.Q;
@@ -117,13 +124,13 @@ __host__ __device__ __forceinline__ SharedEntity shared_entity(const SharedArgs 
     x.lo = 0;
     if (n >= 0) {
         int g0, s;
-        shared_group(a, n, g0, s);
-        x.lo = shared_keys(a, n, g0, s);
+        shared_group(a, z, n, g0, s);
+        x.lo = shared_keys(a, z, n, g0, s);
     }
-    x.end = clamp_len(shared_at(p.seqlens_k, x.b0), p.K);
-    const int Qb = p.seqlens_q ? clamp_len(shared_at(p.seqlens_q, x.b0), p.Q) : p.Q;
+    x.end = clamp_len(z.k[x.b0], p.K);
+    x.Qb = z.q ? clamp_len(z.q[x.b0], p.Q) : p.Q;
     x.kv_start = x.lo & ~(a.tile_align - 1);
-    x.nt = x.end > x.lo && Qb > 0 ? (x.end - x.kv_start + 127) >> 7 : 0;
+    x.nt = x.end > x.lo && x.Qb > 0 ? (x.end - x.kv_start + 127) >> 7 : 0;
     x.blocks = a.own_blocks;
     shared_cost(a, x, p.Q > a.tile_tokens);
     return x;
@@ -132,25 +139,24 @@ __host__ __device__ __forceinline__ SharedEntity shared_entity(const SharedArgs 
 struct SharedJob {
     int kvh, tok0, ntok;  // first query token (of all B * Q), how many
     int nt, end;          // tiles of this block, end of the keys that its rows use
-    long long row0;       // first row among the rows of the entities of this kind
+    long long at;         // its first (token, KV head) among those of the entities of this kind
 };
 
 __host__ __device__ __forceinline__ SharedJob shared_job(const SharedArgs &a, const SharedEntity &x, int j) {
     const AttnParams &p = a.p;
     SharedJob k;
-    k.kvh = j / x.blocks;
+    k.kvh = x.blocks == 1 ? j : j / x.blocks;
     const int first = (j - k.kvh * x.blocks) * 2 * a.tile_tokens, tokens = x.s * p.Q;
     k.tok0 = x.b0 * p.Q + first;
     k.ntok = tokens - first < 2 * a.tile_tokens ? tokens - first : 2 * a.tile_tokens;
     k.nt = x.nt;
     k.end = x.end;
     if (x.kind == 1) {  // the last real token of the block bounds its keys
-        const int Qb = p.seqlens_q ? clamp_len(shared_at(p.seqlens_q, x.b0), p.Q) : p.Q;
-        const int last = (first + k.ntok < Qb ? first + k.ntok : Qb) - 1;
-        k.end = last < first ? 0 : x.end - Qb + last + 1;
+        const int last = (first + k.ntok < x.Qb ? first + k.ntok : x.Qb) - 1;
+        k.end = last < first ? 0 : x.end - x.Qb + last + 1;
         k.nt = k.end > x.lo ? (k.end - x.kv_start + 127) >> 7 : 0;
     }
-    k.row0 = (long long)x.b0 * p.Q * p.Hq + ((long long)k.kvh * tokens + first) * p.G;
+    k.at = (long long)x.b0 * p.Q * p.Hkv + (long long)k.kvh * tokens + first;
     return k;
 }
 
@@ -158,67 +164,103 @@ __host__ __device__ __forceinline__ SharedJob shared_job(const SharedArgs &a, co
 __host__ __device__ __forceinline__ int shared_cut(long long x, long long js, int w, int nt) {
     const long long d = x - js - kCostStart;
     if (d <= 0) return 0;
-    const long long t = d / w;
-    return t < nt ? (int)t : nt;
+    if (d >= (long long)w * nt) return nt;
+    return (int)((uint32_t)d / (uint32_t)w);
 }
 
+// CTAs that get a share: each share is at least a tile, so that every CTA between a
+// job's first piece and its last has one.
+__host__ __device__ __forceinline__ int shared_ctas(long long W, int ctas) {
+    const long long n = W / kCostTwo;
+    return n < 1 ? 1 : n < ctas ? (int)n : ctas;
+}
+// Where CTA c's share begins, of n (W from the last one's end on).
 __host__ __device__ __forceinline__ long long shared_bound(long long W, int c, int n) {
+    if (c >= n) return W;
+    if (W < (1LL << 22) && n < 1024) return (uint32_t)W * (uint32_t)c / (uint32_t)n;
     return W * c / n;
 }
 
 // A piece's rows in the partials: pieces that follow one another on the axis advance
 // the job, the CTA or both, so none of them overlap (at most 256 rows a piece, and
 // twice a job's rows where tiles alternate between two chains).
-__host__ __device__ __forceinline__ long long shared_base(long long row0, int c) {
-    return 2 * row0 + 256LL * c;
+__host__ __device__ __forceinline__ long long shared_base(long long at, int G, int c) {
+    return 2 * at * G + 256LL * c;
 }
 __host__ __device__ __forceinline__ long long shared_rows(const AttnParams &p, int ctas) {
     return 2LL * p.B * p.Q * p.Hq + 256LL * ctas;
 }
 
+// Where a share begins: the entity at its first cost, where that one begins, its group
+// (-1 for none) and the group's members.
+struct SharedBegin {
+    long long es;
+    int e, n, g0, g1;
+    SharedEntity x;
+};
+__host__ __device__ __forceinline__ SharedBegin shared_begin(const SharedArgs &a, const SharedLens &z, int e, int n,
+                                                             long long es) {
+    SharedBegin s;
+    s.es = es;
+    s.e = e;
+    s.n = n;
+    s.g0 = s.g1 = 0;
+    if (e >= a.N) {
+        s.g0 = e - a.N;
+        s.g1 = s.g0 + 1;
+        if (n >= 0) {
+            int m;
+            shared_group(a, z, n, s.g0, m);
+            s.g1 = s.g0 + m;
+        }
+    }
+    s.x = shared_entity(a, z, e, n);
+    return s;
+}
+
 // The pieces of a CTA's share, one after the other (every lane of a warp alike).
 struct SharedWalker {
     const SharedArgs &a;
-    long long x0, x1, es;  // share, first cost of the entity
-    int e, j;              // entity, job
-    int n;                 // group of a sequence, -1 for none
-    SharedEntity x;
+    long long x0, x1;  // share
+    int j;             // job of the entity
     bool done;
+    SharedBegin s;     // the entity
 
-    // (es0: the first cost of entity e0, where the share begins; x0 < x1)
+    // (from == to, or an entity past the last: an empty share)
     __host__ __device__ __forceinline__ SharedWalker(const SharedArgs &args, long long from, long long to,
-                                                     long long es0, int e0)
-        : a(args), x0(from), x1(to), es(es0), e(e0), j(0), n(-1), x(), done(from >= to) {
+                                                     const SharedBegin &begin)
+        : a(args), x0(from), x1(to), j(0), done(from >= to || begin.e >= args.entities), s(begin) {
         if (done) return;
-        load();
-        if (!done) j = (int)((x0 - es) / x.cj);
+        const long long d = x0 - s.es;
+        j = d < (1LL << 31) ? (int)((uint32_t)d / (uint32_t)s.x.cj) : (int)(d / s.x.cj);
     }
     __host__ __device__ __forceinline__ void load() {
-        if (e >= a.N + a.p.B || es >= x1) {
+        if (s.e >= a.entities || s.es >= x1) {
             done = true;
             return;
         }
-        n = e >= a.N ? shared_group_of(a, e - a.N) : -1;
-        x = shared_entity(a, e, n);
+        const SharedLens z = shared_lens_of(a);
+        const int b = s.e - a.N;
+        if (b >= 0 && (b < s.g0 || b >= s.g1)) s = shared_begin(a, z, s.e, shared_group_of(a, z, b), s.es);
+        else s.x = shared_entity(a, z, s.e, s.n);
     }
     // the next piece with tiles [t0, t1) of job k; false: no more
     __host__ __device__ __forceinline__ bool next(SharedJob &k, int &t0, int &t1) {
         while (!done) {
-            const long long js = es + (long long)j * x.cj;
-            if (j >= x.jobs) {
-                es += (long long)x.jobs * x.cj;
+            const long long js = s.es + (long long)j * s.x.cj;
+            if (j >= s.x.jobs) {
+                s.es += (long long)s.x.jobs * s.x.cj;
                 j = 0;
-                ++e;
+                ++s.e;
                 load();
                 continue;
             }
             if (js >= x1) break;
-            if (x.nt > 0) {
-                k = shared_job(a, x, j);
-                t0 = shared_cut(x0, js, x.w, k.nt);
-                t1 = shared_cut(x1, js, x.w, k.nt);
-            } else {
-                t0 = t1 = 0;
+            t0 = t1 = 0;
+            if (s.x.nt > 0) {
+                k = shared_job(a, s.x, j);
+                t0 = shared_cut(x0, js, s.x.w, k.nt);
+                t1 = shared_cut(x1, js, s.x.w, k.nt);
             }
             ++j;
             if (t1 > t0) return true;
@@ -228,39 +270,45 @@ struct SharedWalker {
     }
 };
 
-// The partials of a row: of its entity's job, from CTAs [c0, c1], two chains each.
-struct SharedRow {
-    SharedEntity x;
-    SharedJob k;
-    long long js;  // cost where the job begins
-    int lr;        // row of the job
-    int c0, c1;
-    bool two;
-};
-__host__ __device__ __forceinline__ SharedRow shared_row(const SharedArgs &a, int e, int n, long long es,
-                                                         long long W, int token, int h) {
-    SharedRow r;
-    r.x = shared_entity(a, e, n);
-    if (r.x.nt == 0) return r;
-    const int kvh = h / a.p.G, off = token - r.x.b0 * a.p.Q, blk = off / (2 * a.tile_tokens);
-    const int j = kvh * r.x.blocks + blk;
-    r.k = shared_job(a, r.x, j);
-    r.two = r.k.ntok > a.tile_tokens;
-    r.lr = (off - blk * 2 * a.tile_tokens) * a.p.G + (h - kvh * a.p.G);
-    r.js = es + (long long)j * r.x.cj;
-    // the first CTA whose share ends behind js, the last one whose share begins before
-    // the job's end (bounds round down)
-    r.c0 = (int)(((r.js + 1) * a.ctas + W - 1) / W) - 1;
-    r.c1 = (int)(((r.js + r.x.cj) * a.ctas + W - 1) / W) - 1;
-    return r;
+// Part s of the keys [lo, end) that a sequence has alone, in whole tiles of 64 and at
+// least kOwnKeys of them; empty where beg >= fin.
+constexpr int kOwnKeys = 256;
+__host__ __device__ __forceinline__ int own_part(int lo, int end, int splits) {
+    const int base = lo & ~63, per = ((end - base + splits - 1) / splits + 63) & ~63;
+    return per < kOwnKeys ? kOwnKeys : per;
 }
-// Where CTA c's chain left the row's partial, or -1.
-__host__ __device__ __forceinline__ long long shared_partial(const SharedArgs &a, const SharedRow &r,
-                                                             long long W, int c, int chain) {
-    const int t0 = shared_cut(shared_bound(W, c, a.ctas), r.js, r.x.w, r.k.nt);
-    const int t1 = shared_cut(shared_bound(W, c + 1, a.ctas), r.js, r.x.w, r.k.nt);
-    if (r.two ? (t1 <= t0 || chain > 0) : t1 - t0 <= chain) return -1;
-    return shared_base(r.k.row0, c) + (r.two ? 0 : chain * r.k.ntok * a.p.G) + r.lr;
+__host__ __device__ __forceinline__ void own_split(int lo, int end, int splits, int s, int &beg, int &fin) {
+    beg = fin = 0;
+    if (end <= lo) return;
+    const int base = lo & ~63;
+    const long long per = own_part(lo, end, splits), b0 = base + s * per;
+    if (b0 >= end) return;
+    beg = s == 0 ? lo : (int)b0;
+    fin = b0 + per < end ? (int)(b0 + per) : end;
+}
+
+// A row's job of either kind, from what the sequence's info says.
+struct SharedRow {
+    long long at;    // the job's first (token, KV head)
+    int ntok, lr;    // its tokens; the row's place among its rows
+    bool some;       // whether the job has a tile
+};
+__host__ __device__ __forceinline__ SharedRow shared_row(const SharedArgs &a, int kind, int g0, int s, int keys,
+                                                         int b, int i, int h, int len, int Qb) {
+    const AttnParams &p = a.p;
+    const int kvh = h / p.G, two = 2 * a.tile_tokens;
+    const int b0 = kind == 0 ? g0 : b, tokens = kind == 0 ? s * p.Q : p.Q, off = (b - b0) * p.Q + i;
+    const int first = off / two * two;
+    SharedRow r;
+    r.ntok = tokens - first < two ? tokens - first : two;
+    r.lr = (off - first) * p.G + (h - kvh * p.G);
+    r.at = (long long)b0 * p.Q * p.Hkv + (long long)kvh * tokens + first;
+    r.some = keys > 0;
+    if (kind == 1) {  // (as shared_job)
+        const int last = (first + r.ntok < Qb ? first + r.ntok : Qb) - 1;
+        r.some = last >= first && len - Qb + last + 1 > keys;
+    }
+    return r;
 }
 
 }  // namespace attn

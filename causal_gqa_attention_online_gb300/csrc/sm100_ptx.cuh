@@ -212,6 +212,115 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
         : "memory");
 }
 
+// For a whole warp to execute: one elected lane (the same one every time) issues.
+// Without a branch around them, and with the steps of a product in one statement, the
+// addresses and descriptors are computed in uniform registers, where the instructions
+// take them from (a lane's own branch cost 80 to 110 cycles an MMA, this 50).
+
+// D[tmem] = A[smem] . B[smem]^T over KSTEPS x 16 columns of K-major operands in chunks of
+// 64 columns, 16 KB apart.
+template <int KSTEPS>
+__device__ __forceinline__ void warp_mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc);
+template <>
+__device__ __forceinline__ void warp_mma_ss<8>(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
+    asm volatile(
+        "{\n"
+        " .reg .pred p, e;\n"
+        " .reg .b64 a, b;\n"
+        " elect.sync _|e, 0xffffffff;\n"
+        " setp.ne.b32 p, 0, 0;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+        " setp.eq.b32 p, 0, 0;\n"
+        " add.s64 a, %1, 2;\n"
+        " add.s64 b, %2, 2;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n"
+        " add.s64 a, %1, 4;\n"
+        " add.s64 b, %2, 4;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n"
+        " add.s64 a, %1, 6;\n"
+        " add.s64 b, %2, 6;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n"
+        " add.s64 a, %1, 1024;\n"
+        " add.s64 b, %2, 1024;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n"
+        " add.s64 a, %1, 1026;\n"
+        " add.s64 b, %2, 1026;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n"
+        " add.s64 a, %1, 1028;\n"
+        " add.s64 b, %2, 1028;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n"
+        " add.s64 a, %1, 1030;\n"
+        " add.s64 b, %2, 1030;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n"
+        "}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc)
+        : "memory");
+}
+template <>
+__device__ __forceinline__ void warp_mma_ss<4>(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
+    asm volatile(
+        "{\n"
+        " .reg .pred p, e;\n"
+        " .reg .b64 a, b;\n"
+        " elect.sync _|e, 0xffffffff;\n"
+        " setp.ne.b32 p, 0, 0;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+        " setp.eq.b32 p, 0, 0;\n"
+        " add.s64 a, %1, 2;\n"
+        " add.s64 b, %2, 2;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n"
+        " add.s64 a, %1, 4;\n"
+        " add.s64 b, %2, 4;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n"
+        " add.s64 a, %1, 6;\n"
+        " add.s64 b, %2, 6;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n"
+        "}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc)
+        : "memory");
+}
+// D[tmem] (+)= A[tmem] . B[smem] over 16 rows of an MN-major operand ...
+__device__ __forceinline__ void warp_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// ... and over 64 of them.
+__device__ __forceinline__ void warp_mma_ts4(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n"
+        " .reg .pred p, e;\n"
+        " .reg .b64 b;\n"
+        " .reg .b32 a;\n"
+        " elect.sync _|e, 0xffffffff;\n"
+        " setp.ne.b32 p, %4, 0;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+        " setp.eq.b32 p, 0, 0;\n"
+        " add.s32 a, %1, 8;\n"
+        " add.s64 b, %2, 128;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n"
+        " add.s32 a, %1, 16;\n"
+        " add.s64 b, %2, 256;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n"
+        " add.s32 a, %1, 24;\n"
+        " add.s64 b, %2, 384;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n"
+        "}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void warp_mma_commit(uint32_t bar) {
+    asm volatile(
+        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
+            bar)
+        : "memory");
+}
+
 // The mbarrier completes one arrival when every tcgen05 operation this thread
 // issued before the commit has completed.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {

@@ -124,45 +124,63 @@ int main() {
         a.tile_tokens = 128 / G;
         a.own_blocks = (Q + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens);
         a.tile_align = page < 128 ? page : 128;
+        a.cost_one = kCostTile128;
+        a.entities = N + B;
+        const SharedLens z = shared_lens_of(a);
         std::vector<long long> start(N + B + 1);
-        std::vector<int> group(B);
+        std::vector<int> info(3 * B);
+        std::vector<int> span[2] = {std::vector<int>(2 * B * Q * Hkv, -1), std::vector<int>(2 * B * Q * Hkv, -1)};
         long long W = 0;
         for (int e = 0; e < N + B; ++e) {
-            const int n = e >= N ? shared_group_of(a, e - N) : -1;
-            if (e >= N) group[e - N] = n;
+            const int n = e >= N ? shared_group_of(a, z, e - N) : -1;
             start[e] = W;
-            const SharedEntity x = shared_entity(a, e, n);
+            const SharedEntity x = shared_entity(a, z, e, n);
             W += (long long)x.jobs * x.cj;
+            if (e >= N) {
+                int g0 = x.b0, s = 1;
+                if (n >= 0) shared_group(a, z, n, g0, s);
+                info[3 * (e - N)] = g0;
+                info[3 * (e - N) + 1] = s;
+                info[3 * (e - N) + 2] = x.lo;
+            }
         }
         start[N + B] = W;
         printf("c %lld %lld\n", W, shared_rows(a.p, ctas));
+        const int shares = shared_ctas(W, ctas);
         for (int c = 0; c < ctas; ++c) {
-            const long long x0 = shared_bound(W, c, ctas), x1 = shared_bound(W, c + 1, ctas);
+            const long long x0 = shared_bound(W, c, shares), x1 = shared_bound(W, c + 1, shares);
             int e = 0;
             while (x0 < x1 && !(start[e] <= x0 && x0 < start[e + 1])) ++e;
-            SharedWalker wk(a, x0, x1, start[e], e);
+            const int n = e >= N && e < N + B ? shared_group_of(a, z, e - N) : -1;
+            SharedBegin begin = {};
+            begin.e = e;
+            if (e < N + B) begin = shared_begin(a, z, e, n, start[e]);
+            SharedWalker wk(a, x0, x1, begin);
             SharedJob k;
             int t0, t1;
             while (wk.next(k, t0, t1)) {
-                const int key0 = wk.x.kv_start + t0 * 128;
-                const int end = k.end < wk.x.kv_start + t1 * 128 ? k.end : wk.x.kv_start + t1 * 128;
-                printf("p %d %d %d %d %d %d %d %d %d %d %lld %d\n", c, wk.x.kind, wk.x.b0, k.kvh, k.tok0, k.ntok,
-                       wk.x.lo, wk.x.end, key0, end, shared_base(k.row0, c), t1 - t0);
+                const int key0 = wk.s.x.kv_start + t0 * 128;
+                const int end = k.end < wk.s.x.kv_start + t1 * 128 ? k.end : wk.s.x.kv_start + t1 * 128;
+                printf("p %d %d %d %d %d %d %d %d %d %d %lld %d\n", c, wk.s.x.kind, wk.s.x.b0, k.kvh, k.tok0, k.ntok,
+                       wk.s.x.lo, wk.s.x.end, key0, end, shared_base(k.at, G, c), t1 - t0);
+                if (t0 == 0) span[wk.s.x.kind][2 * k.at] = c;
+                if (t1 == k.nt) span[wk.s.x.kind][2 * k.at + 1] = c;
             }
         }
         for (int token = 0; rows && token < B * Q; ++token)
             for (int h = 0; h < Hkv * G; ++h) {
                 printf("r %d %d", token, h);
-                const int b = token / Q, n = group[b];
-                for (int kind = n >= 0 ? 0 : 1; kind < 2; ++kind) {
-                    const int e = kind == 0 ? n : N + b;
-                    const SharedRow r = shared_row(a, e, n, start[e], W, token, h);
-                    if (r.x.nt == 0) continue;
-                    for (int c = r.c0; c <= r.c1; ++c)
-                        for (int ch = 0; ch < 2; ++ch) {
-                            const long long at = shared_partial(a, r, W, c, ch);
-                            if (at >= 0) printf(" %d:%lld", kind, at);
-                        }
+                const int b = token / Q;
+                const int len = clamp_len(lens[b], K), Qb = clamp_len(sq[b], Q);
+                for (int kind = 0; kind < 2; ++kind) {
+                    const SharedRow r = shared_row(a, kind, info[3 * b], info[3 * b + 1], info[3 * b + 2], b, token - b * Q,
+                                                   h, len, Qb);
+                    if (!r.some) continue;
+                    const int *sp = &span[kind][2 * r.at];
+                    if (sp[0] < 0 || sp[1] < sp[0]) printf(" bad:0");
+                    for (int c = sp[0]; c <= sp[1]; ++c)
+                        for (int ch = 0; ch < (r.ntok > a.tile_tokens ? 1 : 2); ++ch)
+                            printf(" %d:%lld", kind, shared_base(r.at, G, c) + ch * r.ntok * G + r.lr);
                 }
                 printf("\n");
             }
@@ -218,7 +236,7 @@ def test_shares_cover_every_row_and_key_once(prog):
         # what each sequence shares, and with whom
         shared = np.zeros(B, int)
         for n in range(N):
-            if cu[n + 1] - cu[n] >= 2:
+            if cu[n + 1] > cu[n]:
                 shared[cu[n]: cu[n + 1]] = min(pre[n], lens[cu[n]])
         seen = {}     # (token, head) -> keys met
         where = {}    # partial row -> (token, head) that wrote it
@@ -238,7 +256,7 @@ def test_shares_cover_every_row_and_key_once(prog):
                 assert lo == 0 or (kind == 1 and lo == shared[b])
                 hi = min(lens[b] - sq[b] + i + 1, end) if i < sq[b] else 0
                 keys = range(max(lo, key0), max(lo, key0, min(hi, key_end)))
-                for chain in range(1 if two else min(2, nt)):
+                for chain in range(1 if two else 2):  # (of one tile, the second says that it has none)
                     at = (kind, base + (0 if two else chain * ntok * G) + r)
                     assert at[1] < rows and at not in where
                     where[at] = (token, h)
@@ -301,6 +319,4 @@ def test_groups_that_break_the_rules_stay_in_bounds(prog):
                 _, kind, b0, kvh, tok0, ntok, lo, end, key0, key_end, base, nt = map(int, f[1:])
                 assert 0 <= b0 < c[0] and 0 <= kvh < 2 and 0 <= tok0 and tok0 + ntok <= c[0] * 3
                 assert 0 <= key0 < key_end <= 512 and base >= 0
-                assert base + ntok * 4 * (1 if ntok > 32 else min(2, nt)) <= rows
-            else:
-                assert all(0 <= int(x.split(":")[1]) < rows for x in f[3:])
+                assert base + ntok * 4 * (1 if ntok > 32 else 2) <= rows
