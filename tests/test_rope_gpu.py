@@ -381,3 +381,98 @@ def test_append_in_a_graph():
         same(out, want)
         for a, b in zip(pools, other):
             same(a, b)
+
+
+# Many rows go through shared memory, by other kernels than few.  Each must give what the
+# calls for a few of its rows at a time give, bit for bit.
+
+MANY = [(4, 1501, 8, 4, 96, 48), (1, 4099, 3, 1, 64, 64), (2, 1301, 40, 8, 256, 64), (1, 401, 100, 4, 512, 512),
+        (3, 2001, 6, 2, 80, 40), (1, 6007, 14, 2, 72, 24)]
+
+
+@pytest.mark.parametrize("dtype,pairs", [("bf16", "half"), ("f16", "adjacent"), ("f32", "half"), ("f32", "adjacent")])
+@pytest.mark.parametrize("shape", MANY)
+def test_rope_of_many_rows(shape, dtype, pairs):
+    B, N, Hq, Hkv, D, rot = shape
+    g = np.random.default_rng(sum(shape))
+    x = rows(g, (B, N, (Hq + Hkv) * D), dtype).to(DEV)
+    q, k = (t.unflatten(-1, (-1, D)) for t in x.split([Hq * D, Hkv * D], -1))
+    cos, sin = (torch.from_numpy(t).to(DEV) for t in rope_ref.angles(N, rot))
+    pos = i32(g.integers(-1, N + 1, (B, N)))
+    for f in (attn.attn_rope, attn.attn_rope_bwd):
+        got = f(q, k, cos, sin, positions=pos, pairs=pairs)
+        only = f(q, None, cos, sin, positions=pos, pairs=pairs)
+        same(only[0] if isinstance(only, tuple) else only, got[0])
+        for a in range(0, N, 700):
+            for b in range(B):
+                at = (slice(b, b + 1), slice(a, min(N, a + 700, a + 311000 // (Hq * D) + 1)))
+                want = f(q[at], k[at], cos, sin, positions=pos[at].contiguous(), pairs=pairs)
+                same(got[0][at], want[0]), same(got[1][at], want[1])
+    # in place
+    q, k = q.contiguous(), k.contiguous()
+    want = attn.attn_rope(q, k, cos, sin, positions=pos, pairs=pairs)
+    attn.attn_rope(q, k, cos, sin, q, k, positions=pos, pairs=pairs)
+    same(q, want[0]), same(k, want[1])
+
+
+# lens, new, page, Hq, Hkv, D, Dv, rot
+MANY_APPENDS = [([0, 70, 3000, 5], [3001, 0, 1400, 1], 64, 32, 8, 128, 128, 128),
+                ([1, 16, 99], [2001, 2000, 3], 16, 4, 3, 96, 64, 48),
+                ([7] * 40, [301] * 20 + [17] * 20, 128, 8, 2, 128, 256, 64)]
+
+
+def one_sequence(st, b, n0, n1):
+    """Rows n0 .. n1 of sequence b as a batch of their own."""
+    one = Step.__new__(Step)
+    one.__dict__.update(st.__dict__)
+    at = slice(int(st.cu[b]) + n0, int(st.cu[b]) + n1) if st.packed else (b, slice(n0, n1))
+    one.q, one.k, one.v = (t[at].contiguous()[None] for t in (st.q, st.k, st.v))
+    one.positions = None if st.positions is None else st.positions[at][None]
+    one.packed, one.B, one.N = False, 1, n1 - n0
+    one.lens, one.new, one.table = [st.lens[b] + n0], [n1 - n0], st.table[b: b + 1]
+    return one
+
+
+@pytest.mark.parametrize("variant", ["plain", "packed", "positions", "fused", "packed fused"])
+@pytest.mark.parametrize("kind,dtype,pairs", [("none", "bf16", "half"), ("none", "f16", "adjacent"), ("none", "f32", "half"),
+                                              ("int8", "bf16", "adjacent"), ("e4m3", "f16", "half"), ("int8", "f32", "half")])
+@pytest.mark.parametrize("case", range(len(MANY_APPENDS)))
+def test_append_of_many_rows(case, kind, dtype, pairs, variant):
+    lens, new, page, Hq, Hkv, D, Dv, rot = MANY_APPENDS[case]
+    g = np.random.default_rng(case)
+    st = Step(g, lens, new, page, Hq, Hkv, D, Dv, rot, dtype, "packed" in variant, variant == "positions",
+              "fused" in variant, slack=9 if "packed" in variant else 0)
+    st.table[0, 2] = -1  # a page that is not there
+    st.cos, st.sin = st.cos[:-40], st.sin[:-40]  # the longest sequence runs past the angles
+    for block in ((0,) if kind == "none" else (16, page)):
+        pools = []
+        for _ in range(2):
+            if kind == "none":
+                pools.append([torch.full((st.P, page, Hkv, w), 3.0, dtype=DT[dtype], device=DEV) for w in (D, Dv)])
+            else:
+                pools.append([torch.full((st.P, page, Hkv, w), 5, dtype=torch.uint8, device=DEV).view(
+                    cache_ref.TORCH_CODE[kind]) for w in (D, Dv)])
+                pools[-1] += [torch.full((st.P, page // block, Hkv), 2.0 ** -9, device=DEV) for _ in "kv"]
+        canary = torch.full(st.q.shape, 7.0, dtype=st.q.dtype, device=DEV)
+        got = st.call(pools[0], pairs, q_out=canary)
+        for b, n in enumerate(new):
+            # (8-bit blocks take all their new rows at once)
+            step = max(n, 1) if kind != "none" else max(1, 300000 // ((Hq + Hkv) * max(D, Dv)))
+            for a in range(0, n, step):
+                e = min(n, a + step)
+                want = one_sequence(st, b, a, e).call(pools[1], pairs)
+                c = int(st.cu[b])
+                same(got[c + a: c + e] if st.packed else got[b, a:e], want[0])
+            if not st.packed:
+                assert not got[b, n:].float().any() and not torch.signbit(got[b, n:].float()).any()
+        if st.packed:
+            assert (got[sum(new):] == 7).all()
+        for x, y in zip(*pools):
+            same(x, y)
+        again = [p.clone() for p in pools[0]]  # and without q, over what is there now
+        st.call(pools[0], pairs, q=False)
+        for b, n in enumerate(new):
+            if n:
+                one_sequence(st, b, 0, n).call(again, pairs, q=False)
+        for x, y in zip(pools[0], again):
+            same(x, y)
