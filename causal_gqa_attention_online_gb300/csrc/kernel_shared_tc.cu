@@ -771,104 +771,178 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------ the join
 
-// A block joins eight rows: warp w takes columns 16 w .. 16 w + 15 of all of them, four
+// A block joins R rows.  Its first warp finds and weighs their partials, 32 / R lanes a row,
+// and leaves a list of them; then warp w adds up columns 16 w .. 16 w + 15 of all rows, four
 // lanes a row, so that a load of the partials (rows side by side) is four runs of 128
-// bytes.  Every warp weighs the partials for itself.
-constexpr int kJoinRows = 8, kJoinUnroll = 4;
+// bytes.  What a block takes is latency, of the chain from the lengths to the partials
+// (4 us), so many rows want blocks of 32 of them, few rows and many partials blocks of 8.
+constexpr int kJoinMost = 8;  // partials a lane finds at a time
 
-template <typename T>
-__global__ void __launch_bounds__(256, 5) shared_join_kernel(const __grid_constant__ SharedArgs a) {
+struct JoinEntry {
+    const float *o;
+    float w;
+    int chunk;         // floats from one chunk of four columns to the next
+};
+
+template <typename T, int R>
+__global__ void __launch_bounds__(256, R == 8 ? 2 : 4) shared_join_kernel(const __grid_constant__ SharedArgs a) {
+    constexpr int kLanes = 32 / R, kList = kLanes * kJoinMost, kUnroll = R == 8 ? 12 : 3;
+    __shared__ JoinEntry list[R][kList];
+    __shared__ float max_of[R], sum_of[R];
+    __shared__ int live_of[R], most_all;
     const AttnParams &p = a.p;
-    const int lane = threadIdx.x & 31, quarter = lane & 3;
-    const int chunk = (threadIdx.x >> 5) * 4 + quarter;  // columns 4 chunk ..
-    const long long rows = (long long)p.B * p.Q * p.Hq;
-    const long long row0 = (long long)blockIdx.x * kJoinRows + (lane >> 2), row = min(row0, rows - 1);
-    const int token = (int)(row / p.Hq), h = (int)(row - (long long)token * p.Hq);
-    const int b = token / p.Q, i = token - b * p.Q;
-    // (before the wait: what the caller gave)
-    const int len = clamp_len(__ldg(p.seqlens_k + b), p.K);
-    const int Qb = p.seqlens_q ? clamp_len(__ldg(p.seqlens_q + b), p.Q) : p.Q;
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    const int4 in = a.info[b];
-    // where the partials of either job are: chains (one or two) of CTAs [first, last]
-    long long at[2];
-    int two[2], n[2];
-#pragma unroll
-    for (int kind = 0; kind < 2; ++kind) {
-        const SharedRow r = shared_row(a, kind, in.x, in.y, in.z, b, i, h, len, Qb);
-        int2 c = make_int2(0, -1);
-        if (r.some) c = a.span[kind][r.at];
-        // (a launch that gave up leaves them unwritten: never past the partials)
-        c.x = max(c.x, 0), c.y = min(c.y, a.ctas - 1);
-        two[kind] = r.ntok > a.tile_tokens ? 0 : r.ntok * p.G;  // rows from one chain to the other, or 0
-        n[kind] = max(c.y - c.x + 1, 0) << (two[kind] ? 1 : 0);
-        at[kind] = shared_base(r.at, p.G, c.x) + r.lr;
-    }
-    const float2 *ml0 = a.part_ml[0], *ml1 = a.part_ml[1];
-    const float *o0 = a.part_o[0], *o1 = a.part_o[1];
-    if (a.own_splits > 0) {  // the sequence's own keys: parts of them, from the other kernel
-        n[1] = 0;
-        if (i < Qb && len > in.z) {
-            const int per = own_part(in.z, len, a.own_splits);
-            n[1] = (len - (in.z & ~63) + per - 1) / per;
-        }
-        at[1] = row;
-    }
-    const long long part = a.own_splits > 0 ? rows : 256LL;  // from one part or CTA to the next
-    const int all = n[0] + n[1];
-    auto place = [&](int s) -> long long {  // of partial s, kind (s >= n[0])
-        const bool own = s >= n[0];
-        const int k = own ? s - n[0] : s;
-        if (own && a.own_splits > 0) return at[1] + k * part;
-        const int step = own ? two[1] : two[0];
-        return (own ? at[1] : at[0]) + (step ? (k >> 1) * 256LL + (k & 1) * step : k * 256LL);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long rows = (long long)p.B * p.Q * p.Hq, row_base = (long long)blockIdx.x * R;
+    const bool own = a.own_splits > 0;
+    // the first warp's: partials s < n0 of the shared keys, s < all of both
+    const int mine = lane / kLanes, part = lane % kLanes;
+    int n0 = 0, all = 0, most = 0, two0 = 0, two1 = 0;
+    long long at0 = 0, at1 = row_base + mine;
+    float M = -INFINITY, sum = 0.f;
+    auto place = [&](int s) -> long long {
+        if (s < n0) return at0 + (two0 ? (s >> 1) * 256LL + (s & 1) * two0 : s * 256LL);
+        s -= n0;
+        if (own) return at1 + s * rows;
+        return at1 + (two1 ? (s >> 1) * 256LL + (s & 1) * two1 : s * 256LL);
     };
-    // the largest maximum: four lanes a row
-    float M = -INFINITY;
-    for (int s = quarter; s < all; s += 4) {
-        const float2 ml = (s >= n[0] ? ml1 : ml0)[place(s)];
-        if (ml.y != 0.f) M = fmaxf(M, ml.x);
-    }
-    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 1));
-    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 2));
-    float L = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < all; s0 += kJoinUnroll) {
-        float2 ml[kJoinUnroll];
-        float4 v[kJoinUnroll];
-#pragma unroll
-        for (int u = 0; u < kJoinUnroll; ++u) {
-            const int s = s0 + u;
-            ml[u] = make_float2(0.f, 0.f);
-            v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (s < all) {
-                const long long x = place(s);
-                ml[u] = (s >= n[0] ? ml1 : ml0)[x];
-                if (ml[u].y != 0.f)  // (0: no key of this row; NaN stays)
-                    v[u] = *reinterpret_cast<const float4 *>(
-                        s >= n[0] && a.own_splits > 0 ? o1 + x * p.Dv + chunk * 4
-                                                      : (s >= n[0] ? o1 : o0) + (x >> 5) * 32 * p.Dv + (chunk * 32 + (x & 31)) * 4);
+    auto weigh = [&](int s) -> float2 {
+        return s < all ? (s < n0 ? a.part_ml[0] : a.part_ml[1])[place(s)] : make_float2(0.f, 0.f);
+    };
+    if (warp == 0) {
+        const long long row = row_base + mine;
+        int len = 0, Qb = 0, b = 0, i = 0, h = 0;
+        if (row < rows) {  // (before the wait: what the caller gave)
+            const int token = rows >> 31 ? (int)(row / p.Hq) : (int)((uint32_t)row / (uint32_t)p.Hq);
+            h = (int)(row - (long long)token * p.Hq);
+            b = (int)((uint32_t)token / (uint32_t)p.Q);
+            i = token - b * p.Q;
+            len = clamp_len(__ldg(p.seqlens_k + b), p.K);
+            Qb = p.seqlens_q ? clamp_len(__ldg(p.seqlens_q + b), p.Q) : p.Q;
+        }
+        asm volatile("griddepcontrol.wait;\n" ::: "memory");
+        if (row < rows) {
+            const int4 in = a.info[b];
+            // where the partials of a job are: chains (one or two) of CTAs [x, y]
+            auto find = [&](int kind, int &two, long long &at) -> int {
+                const SharedRow r = shared_row(a, kind, in.x, in.y, in.z, b, i, h, len, Qb);
+                if (!r.some) return 0;
+                int2 c = a.span[kind][r.at];
+                // (a launch that gave up leaves them unwritten: never past the partials)
+                c.x = max(c.x, 0), c.y = min(c.y, a.ctas - 1);
+                two = r.ntok > a.tile_tokens ? 0 : r.ntok * p.G;  // rows between the chains, or 0
+                at = shared_base(r.at, p.G, c.x) + r.lr;
+                return max(c.y - c.x + 1, 0) << (two ? 1 : 0);
+            };
+            n0 = find(0, two0, at0);
+            if (!own) {
+                all = n0 + find(1, two1, at1);
+            } else if (i < Qb && len > in.z) {  // parts of the sequence's own keys, from the other kernel
+                const int per = own_part(in.z, len, a.own_splits);
+                all = n0 + (len - (in.z & ~63) + per - 1) / per;
+            } else {
+                all = n0;
             }
         }
-#pragma unroll
-        for (int u = 0; u < kJoinUnroll; ++u) {
-            if (ml[u].y == 0.f) continue;
-            // (a sum that is NaN without a maximum poisons the row)
-            const float w = ml[u].x == -INFINITY ? 1.f : exp2f(ml[u].x - M);
-            L = fmaf(w, ml[u].y, L);
-            acc.x = fmaf(w, v[u].x, acc.x);
-            acc.y = fmaf(w, v[u].y, acc.y);
-            acc.z = fmaf(w, v[u].z, acc.z);
-            acc.w = fmaf(w, v[u].w, acc.w);
-        }
+        most = __reduce_max_sync(0xffffffffu, all);
+        if (lane == 0) most_all = most;
     }
-    if (row0 >= rows) return;
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    uint2 o;
-    o.x = pack2<T>(L == 0.f ? 0.f : acc.x * inv, L == 0.f ? 0.f : acc.y * inv);
-    o.y = pack2<T>(L == 0.f ? 0.f : acc.z * inv, L == 0.f ? 0.f : acc.w * inv);
-    *reinterpret_cast<uint2 *>(static_cast<T *>(p.o) + row * p.Dv + chunk * 4) = o;
-    if (chunk == 0 && p.lse) p.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+    float4 acc[R / 8];
+#pragma unroll
+    for (int g = 0; g < R / 8; ++g) acc[g] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int quarter = lane & 3, chunk = warp * 4 + quarter;  // columns 4 chunk ..
+    for (int s0 = 0; s0 == 0 || s0 < most; s0 += kList) {
+        if (warp == 0) {
+            float2 ml[kJoinMost];
+#pragma unroll
+            for (int k = 0; k < kJoinMost; ++k) ml[k] = weigh(s0 + part + k * kLanes);
+            if (s0 == 0) {  // the largest maximum of all
+#pragma unroll
+                for (int k = 0; k < kJoinMost; ++k)
+                    if (ml[k].y != 0.f) M = fmaxf(M, ml[k].x);
+                for (int s = kList + part; s < all; s += kLanes) {
+                    const float2 x = weigh(s);
+                    if (x.y != 0.f) M = fmaxf(M, x.x);
+                }
+#pragma unroll
+                for (int x = 1; x < kLanes; x <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+                if (part == 0) max_of[mine] = M;
+            }
+            int live = 0;
+#pragma unroll
+            for (int k = 0; k < kJoinMost; ++k) {
+                const int s = s0 + part + k * kLanes;
+                const bool some = ml[k].y != 0.f;  // (0: no key of this row; NaN stays)
+                const uint32_t bits = (__ballot_sync(0xffffffffu, some) >> (lane - part)) & ((1u << kLanes) - 1u);
+                if (some) {
+                    const bool flat = s >= n0 && own;
+                    const long long x = place(s);
+                    JoinEntry e;
+                    e.o = flat ? a.part_o[1] + x * p.Dv
+                               : (s < n0 ? a.part_o[0] : a.part_o[1]) + (x >> 5) * 32 * p.Dv + (x & 31) * 4;
+                    e.chunk = flat ? 4 : 128;
+                    // (a sum that is NaN without a maximum poisons the row)
+                    e.w = ml[k].x == -INFINITY ? 1.f : exp2f(ml[k].x - M);
+                    list[mine][live + __popc(bits & ((1u << part) - 1u))] = e;
+                    sum = fmaf(e.w, ml[k].y, sum);
+                }
+                live += __popc(bits);
+            }
+            float l = sum;
+#pragma unroll
+            for (int x = 1; x < kLanes; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+            if (part == 0) {
+                live_of[mine] = live;
+                sum_of[mine] = l;
+            }
+        }
+        __syncthreads();
+        most = most_all;
+        int live[R / 8], longest = 0;
+#pragma unroll
+        for (int g = 0; g < R / 8; ++g) {
+            live[g] = live_of[g * 8 + (lane >> 2)];
+            longest = max(longest, live[g]);
+        }
+#pragma unroll 1
+        for (int k0 = 0; k0 < longest; k0 += kUnroll) {
+            float4 v[kUnroll][R / 8];
+            float w[kUnroll][R / 8];
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k)
+#pragma unroll
+                for (int g = 0; g < R / 8; ++g) {
+                    v[k][g] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    w[k][g] = 0.f;
+                    if (k0 + k >= live[g]) continue;
+                    const JoinEntry e = list[g * 8 + (lane >> 2)][k0 + k];
+                    w[k][g] = e.w;
+                    v[k][g] = *reinterpret_cast<const float4 *>(e.o + chunk * e.chunk);
+                }
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k)
+#pragma unroll
+                for (int g = 0; g < R / 8; ++g) {
+                    acc[g].x = fmaf(w[k][g], v[k][g].x, acc[g].x);
+                    acc[g].y = fmaf(w[k][g], v[k][g].y, acc[g].y);
+                    acc[g].z = fmaf(w[k][g], v[k][g].z, acc[g].z);
+                    acc[g].w = fmaf(w[k][g], v[k][g].w, acc[g].w);
+                }
+        }
+        if (s0 + kList < most) __syncthreads();
+    }
+#pragma unroll
+    for (int g = 0; g < R / 8; ++g) {
+        const int r = g * 8 + (lane >> 2);
+        const long long row = row_base + r;
+        if (row >= rows) continue;
+        const float L = sum_of[r], inv = L == 0.f ? 0.f : 1.f / L;
+        const float4 x = acc[g];
+        uint2 o;
+        o.x = pack2<T>(L == 0.f ? 0.f : x.x * inv, L == 0.f ? 0.f : x.y * inv);
+        o.y = pack2<T>(L == 0.f ? 0.f : x.z * inv, L == 0.f ? 0.f : x.w * inv);
+        *reinterpret_cast<uint2 *>(static_cast<T *>(p.o) + row * p.Dv + chunk * 4) = o;
+        if (chunk == 0 && p.lse) p.lse[row] = L == 0.f ? -INFINITY : (max_of[r] + log2f(L)) * kLn2;
+    }
 }
 
 // ------------------------------------------------------------------ host
@@ -952,9 +1026,10 @@ int launch_t(SharedArgs &a, bool bf16, cudaStream_t stream) {
         rc = launch_own_decode(a, bf16, stream);
         if (rc) return rc;
     }
-    const long long rows = (long long)p.B * p.Q * p.Hq, blocks = (rows + kJoinRows - 1) / kJoinRows;
+    const long long rows = (long long)p.B * p.Q * p.Hq;
+    const bool many = rows >= 64LL * a.ctas;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.gridDim = dim3((unsigned)(many ? (rows + 31) / 32 : (rows + 7) / 8));
     cfg.blockDim = dim3(p.Dv * 2);  // Dv / 16 warps
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -962,7 +1037,7 @@ int launch_t(SharedArgs &a, bool bf16, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, shared_join_kernel<T>, a);
+    e = cudaLaunchKernelEx(&cfg, many ? shared_join_kernel<T, 32> : shared_join_kernel<T, 8>, a);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) {
         set_error("shared-prefix join launch: %s", cudaGetErrorString(e));
