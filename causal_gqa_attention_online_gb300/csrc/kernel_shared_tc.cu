@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int e = e0; e < e1; ++e) {
         n = e >= a.N ? shared_group_of(a, z, e - a.N) : -1;
         const SharedEntity x = shared_entity(a, z, e, n);
-        mine += (long long)x.jobs * x.cj;
+        mine += x.jobs * x.cj;
     }
     long long incl = mine;
 #pragma unroll
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (;; ++e) {
                 n = e >= a.N ? shared_group_of(a, z, e - a.N) : -1;
                 const SharedEntity x = shared_entity(a, z, e, n);
-                const long long c = (long long)x.jobs * x.cj;
+                const long long c = x.jobs * x.cj;
                 if (x0 < at + c) break;
                 at += c;
             }
@@ -977,7 +977,6 @@ void fill(SharedArgs &a, const AttnParams &p, const int32_t *cu_groups, const in
     a.shared_lens = shared_lens;
     a.N = N;
     a.tile_tokens = 128 / p.G;
-    a.own_blocks = (p.Q + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens);
     a.tile_align = p.page_size < 128 ? p.page_size : 128;
     a.ctas = nsm > 0 ? nsm : 1;
     // A sequence's own keys for few rows: the decode's way (keys on M, four warps a unit)

@@ -3,8 +3,8 @@
 // them, and tests on the host.
 //
 // Entities are the groups (their shared keys, for the rows of all members together),
-// then the sequences (the keys that are theirs alone).  An entity has `jobs` jobs of
-// equal cost: KV heads times blocks of at most two tiles of query tokens; a job walks
+// then the sequences (the keys that are theirs alone).  An entity has a job for each KV
+// head and each block of at most two tiles of query tokens; a job walks
 // `nt` tiles of 128 keys.  Jobs lie one behind the other on an axis of cost, and CTA c
 // of n takes the part [c * W / n, (c + 1) * W / n) of it: whole jobs, and pieces of the
 // first and the last.  A piece leaves, for each of its rows, an unnormalised output
@@ -15,10 +15,12 @@
 
 namespace attn {
 
-// Costs, in units of about 100 cycles of an SM: of a job's start, and of a tile of keys
-// for one tile of rows (64 or 128 columns of K and V: the latter wait for memory) and for
-// two (measured: see kernel_shared_tc.cu).
-constexpr int kCostStart = 20, kCostTile64 = 20, kCostTile128 = 28, kCostTwo = 36;
+// Costs, in units of about 100 cycles of an SM: of a tile of keys for one tile of rows (64
+// or 128 columns of K and V: the latter wait for memory) and for two, and what a job costs
+// besides, the most of it for its partials on their way out (measured: 3600 cycles a tile
+// for two tiles of rows, and 11000 a piece, in jobs of 7 to 32 tiles).
+constexpr int kCostTile64 = 20, kCostTile128 = 28, kCostTwo = 36;
+constexpr int kCostStart = 50, kCostStartTwo = 110;
 
 struct SharedArgs {
     AttnParams p;
@@ -26,7 +28,6 @@ struct SharedArgs {
     const int32_t *shared_lens;  // [N]
     int N;
     int tile_tokens;   // query tokens of a tile of rows: 128 / G
-    int own_blocks;    // blocks of query tokens of a sequence
     int tile_align;    // keys: tiles of a sequence's own keys start on multiples of it
     int ctas;
     int entities;      // N + B, or N where another kernel takes the sequences' own keys
@@ -50,9 +51,11 @@ struct SharedEntity {
     int kv_start;  // first key of tile 0
     int nt;        // tiles of a job (the most, of a sequence's blocks)
     int blocks;    // of query tokens
-    int w;         // cost of a tile
-    int jobs;      // KV heads x blocks
-    int cj;        // cost of a job
+    bool two[2];   // two tiles of rows: a block but the last, the last
+    int w[2];      // cost of a tile in either
+    int cb;        // cost of a block but the last
+    int jobs;      // KV heads, `blocks` jobs each
+    long long cj;  // cost of a head's
 };
 
 // The lengths that the entities depend on: the caller's arrays, or copies of them.
@@ -90,15 +93,22 @@ __host__ __device__ __forceinline__ int shared_group_of(const SharedArgs &a, con
     return b < z.cu[lo] ? lo - 1 : -1;
 }
 
-__host__ __device__ __forceinline__ void shared_cost(const SharedArgs &a, SharedEntity &e, bool two) {
-    e.w = two ? kCostTwo : a.cost_one;
+__host__ __device__ __forceinline__ int shared_start(bool two) { return two ? kCostStartTwo : kCostStart; }
+
+// (tokens: of all blocks together)
+__host__ __device__ __forceinline__ void shared_cost(const SharedArgs &a, SharedEntity &e, int tokens) {
+    const int last = tokens - (e.blocks - 1) * 2 * a.tile_tokens;
+    e.two[0] = true;
+    e.two[1] = last > a.tile_tokens;
+    for (int i = 0; i < 2; ++i) e.w[i] = e.two[i] ? kCostTwo : a.cost_one;
     if (e.nt == 0) {  // nothing to do: a little cost, so that no CTA passes over many
-        e.jobs = 1;
-        e.cj = 1;
+        e.jobs = e.blocks = 1;
+        e.cj = e.cb = 1;
         return;
     }
-    e.jobs = a.p.Hkv * e.blocks;
-    e.cj = kCostStart + e.w * e.nt;
+    e.jobs = a.p.Hkv;
+    e.cb = shared_start(true) + e.w[0] * e.nt;
+    e.cj = (e.blocks - 1) * (long long)e.cb + shared_start(e.two[1]) + e.w[1] * e.nt;
 }
 
 // Entity e of N + B; n: the group of a sequence.
@@ -115,7 +125,7 @@ __host__ __device__ __forceinline__ SharedEntity shared_entity(const SharedArgs 
         x.nt = (x.end + 127) >> 7;
         const int tokens = x.s * p.Q;
         x.blocks = (tokens + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens);
-        shared_cost(a, x, tokens > a.tile_tokens);
+        shared_cost(a, x, tokens);
         return x;
     }
     x.kind = 1;
@@ -131,8 +141,10 @@ __host__ __device__ __forceinline__ SharedEntity shared_entity(const SharedArgs 
     x.Qb = z.q ? clamp_len(z.q[x.b0], p.Q) : p.Q;
     x.kv_start = x.lo & ~(a.tile_align - 1);
     x.nt = x.end > x.lo && x.Qb > 0 ? (x.end - x.kv_start + 127) >> 7 : 0;
-    x.blocks = a.own_blocks;
-    shared_cost(a, x, p.Q > a.tile_tokens);
+    // (blocks of padded tokens alone have no keys)
+    const int two = 2 * a.tile_tokens;
+    x.blocks = x.Qb > two ? (x.Qb + two - 1) / two : 1;
+    shared_cost(a, x, p.Q < x.blocks * two ? p.Q : x.blocks * two);
     return x;
 }
 
@@ -142,11 +154,12 @@ struct SharedJob {
     long long at;         // its first (token, KV head) among those of the entities of this kind
 };
 
-__host__ __device__ __forceinline__ SharedJob shared_job(const SharedArgs &a, const SharedEntity &x, int j) {
+// Block `block` of KV head kvh.
+__host__ __device__ __forceinline__ SharedJob shared_job(const SharedArgs &a, const SharedEntity &x, int kvh, int block) {
     const AttnParams &p = a.p;
     SharedJob k;
-    k.kvh = x.blocks == 1 ? j : j / x.blocks;
-    const int first = (j - k.kvh * x.blocks) * 2 * a.tile_tokens, tokens = x.s * p.Q;
+    k.kvh = kvh;
+    const int first = block * 2 * a.tile_tokens, tokens = x.s * p.Q;
     k.tok0 = x.b0 * p.Q + first;
     k.ntok = tokens - first < 2 * a.tile_tokens ? tokens - first : 2 * a.tile_tokens;
     k.nt = x.nt;
@@ -160,9 +173,9 @@ __host__ __device__ __forceinline__ SharedJob shared_job(const SharedArgs &a, co
     return k;
 }
 
-// Tiles of a job (its start at cost js) before cost x.
+// Tiles of a job (the first at cost js) before cost x.
 __host__ __device__ __forceinline__ int shared_cut(long long x, long long js, int w, int nt) {
-    const long long d = x - js - kCostStart;
+    const long long d = x - js;
     if (d <= 0) return 0;
     if (d >= (long long)w * nt) return nt;
     return (int)((uint32_t)d / (uint32_t)w);
@@ -222,17 +235,23 @@ __host__ __device__ __forceinline__ SharedBegin shared_begin(const SharedArgs &a
 struct SharedWalker {
     const SharedArgs &a;
     long long x0, x1;  // share
-    int j;             // job of the entity
+    int kvh, block;    // job of the entity
+    long long js;      // where it begins
     bool done;
     SharedBegin s;     // the entity
 
     // (from == to, or an entity past the last: an empty share)
     __host__ __device__ __forceinline__ SharedWalker(const SharedArgs &args, long long from, long long to,
                                                      const SharedBegin &begin)
-        : a(args), x0(from), x1(to), j(0), done(from >= to || begin.e >= args.entities), s(begin) {
+        : a(args), x0(from), x1(to), kvh(0), block(0), js(begin.es), done(from >= to || begin.e >= args.entities), s(begin) {
         if (done) return;
         const long long d = x0 - s.es;
-        j = d < (1LL << 31) ? (int)((uint32_t)d / (uint32_t)s.x.cj) : (int)(d / s.x.cj);
+        const bool small = ((d | s.x.cj) >> 31) == 0;
+        kvh = small ? (int)((uint32_t)d / (uint32_t)s.x.cj) : (int)(d / s.x.cj);
+        const long long in = d - kvh * s.x.cj;
+        const int at = (in >> 31) == 0 ? (int)((uint32_t)in / (uint32_t)s.x.cb) : (int)(in / s.x.cb);
+        block = at < s.x.blocks ? at : s.x.blocks - 1;
+        js += kvh * s.x.cj + (long long)block * s.x.cb;
     }
     __host__ __device__ __forceinline__ void load() {
         if (s.e >= a.entities || s.es >= x1) {
@@ -247,22 +266,31 @@ struct SharedWalker {
     // the next piece with tiles [t0, t1) of job k; false: no more
     __host__ __device__ __forceinline__ bool next(SharedJob &k, int &t0, int &t1) {
         while (!done) {
-            const long long js = s.es + (long long)j * s.x.cj;
-            if (j >= s.x.jobs) {
-                s.es += (long long)s.x.jobs * s.x.cj;
-                j = 0;
+            if (kvh >= s.x.jobs) {
+                s.es += s.x.jobs * s.x.cj;
+                js = s.es;
+                kvh = block = 0;
                 ++s.e;
                 load();
                 continue;
             }
             if (js >= x1) break;
             t0 = t1 = 0;
+            const bool last = block == s.x.blocks - 1;
             if (s.x.nt > 0) {
-                k = shared_job(a, s.x, j);
-                t0 = shared_cut(x0, js, s.x.w, k.nt);
-                t1 = shared_cut(x1, js, s.x.w, k.nt);
+                k = shared_job(a, s.x, kvh, block);
+                const int w = last ? s.x.w[1] : s.x.w[0];
+                const long long first = js + shared_start(last ? s.x.two[1] : s.x.two[0]);
+                t0 = shared_cut(x0, first, w, k.nt);
+                t1 = shared_cut(x1, first, w, k.nt);
             }
-            ++j;
+            if (last) {
+                js = s.es + ++kvh * s.x.cj;
+                block = 0;
+            } else {
+                js += s.x.cb;
+                ++block;
+            }
             if (t1 > t0) return true;
         }
         done = true;

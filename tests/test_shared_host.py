@@ -122,7 +122,6 @@ int main() {
         a.p.seqlens_k = lens.data(); a.p.seqlens_q = sq.data();
         a.cu_groups = cu.data(); a.shared_lens = pre.data(); a.N = N; a.ctas = ctas;
         a.tile_tokens = 128 / G;
-        a.own_blocks = (Q + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens);
         a.tile_align = page < 128 ? page : 128;
         a.cost_one = kCostTile128;
         a.entities = N + B;
