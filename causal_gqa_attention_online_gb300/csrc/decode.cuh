@@ -55,6 +55,10 @@ namespace {
 
 constexpr int kTK = 64;      // keys per tile (4 warps x 16)
 constexpr int kStages = 3;
+// OWN: parts are short, and blocks more of a chain of lookups than of copies: three blocks an
+// SM of two stages (256 sequences of up to 64 keys of 8 heads, behind their shared keys:
+// 166 us in all; two blocks of three stages 170)
+constexpr int kOwnStages = 2, kOwnBlocks = 3;
 constexpr int kDecodeThreads = 128;
 
 // How K / V tiles come in.  kLoadTma: one thread issues TMA copies of 64-row
@@ -94,18 +98,19 @@ __device__ __forceinline__ int own_first_key(const SharedArgs &a, int b) {
 }
 
 template <typename T, int D, int DV, int NT, int LOAD, bool OWN>
-__global__ void __launch_bounds__(kDecodeThreads, 2)
+__global__ void __launch_bounds__(kDecodeThreads, OWN ? kOwnBlocks : 2)
     decode_kernel(const __grid_constant__ DecodeArgsOf<OWN> args, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV) {
     const AttnParams &p = args.p;
     constexpr bool PAGED = LOAD == kLoadAsyncPaged;
     constexpr bool TMA = LOAD == kLoadTma;
+    constexpr int NS = OWN ? kOwnStages : kStages;
     constexpr int R = NT * 8;               // query rows of a (sequence, KV head)
     constexpr int KROW = D * 2, VROW = DV * 2;
     constexpr int KTILE = kTK * KROW, VTILE = kTK * VROW;
     constexpr int STAGE = KTILE + VTILE;
     constexpr int OPITCH = DV + 4;          // fp32 merge buffer row pitch
-    static_assert(4 * R * OPITCH * 4 + 8 * 4 * R * 4 <= kStages * STAGE, "merge buffer");
+    static_assert(4 * R * OPITCH * 4 + 8 * 4 * R * 4 <= NS * STAGE, "merge buffer");
     extern __shared__ __align__(128) uint8_t smem[];
 
     const int split = blockIdx.x;
@@ -163,10 +168,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     const T *kg = static_cast<const T *>(p.k);
     const T *vg = static_cast<const T *>(p.v);
     const uint32_t sbase = smem_u32(smem);
-    const uint32_t fbar = sbase + kStages * STAGE;  // TMA: one full barrier a stage
+    const uint32_t fbar = sbase + NS * STAGE;  // TMA: one full barrier a stage
     if (TMA) {
         if (tid == 0) {
-            for (int s = 0; s < kStages; ++s) sm100::mbar_init(fbar + 8u * s, 1);
+            for (int s = 0; s < NS; ++s) sm100::mbar_init(fbar + 8u * s, 1);
             sm100::fence_mbar_init();
         }
         __syncthreads();
@@ -207,11 +212,11 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     uint32_t armed = 0, armed_ph = 0;  // TMA: stages with a copy in flight, its phase
     auto load_tile = [&](int t) {
         const int key0 = kbeg + t * kTK;
-        const uint32_t st = sbase + (t % kStages) * STAGE;
+        const uint32_t st = sbase + (t % NS) * STAGE;
         if constexpr (TMA) {
             if (tid == 0) {
                 const int row = (int)kv_row(p, si, b, key0);
-                const uint32_t fb = fbar + 8u * (t % kStages);
+                const uint32_t fb = fbar + 8u * (t % NS);
                 sm100::mbar_arrive_expect_tx(fb, KTILE + VTILE);
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c)
@@ -219,9 +224,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
 #pragma unroll
                 for (int c = 0; c < DV / 64; ++c)
                     sm100::tma_load_4d(st + KTILE + c * kTK * 128, &tmV, fb, c * 64, kvh, row, 0);
-                armed |= 1u << (t % kStages);
-                armed_ph = (armed_ph & ~(1u << (t % kStages))) |
-                           (((uint32_t)(t / kStages) & 1u) << (t % kStages));
+                armed |= 1u << (t % NS);
+                armed_ph = (armed_ph & ~(1u << (t % NS))) |
+                           (((uint32_t)(t / NS) & 1u) << (t % NS));
             }
             return;
         }
@@ -264,7 +269,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     }
 
 #pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) {
+    for (int s = 0; s < NS - 1; ++s) {
         if (s < ntiles) load_tile(s);
         if (!TMA) cp_async_commit();
     }
@@ -274,18 +279,18 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
         if constexpr (TMA) {
             // tile t has landed (a bounded wait: a copy that never lands records
             // a status, and the block stops with its outputs unwritten)
-            const bool got = sm100::mbar_wait_drain(fbar + 8u * (t % kStages),
-                                             (uint32_t)(t / kStages) & 1u, p.wait_ns);
+            const bool got = sm100::mbar_wait_drain(fbar + 8u * (t % NS),
+                                             (uint32_t)(t / NS) & 1u, p.wait_ns);
             if (!__syncthreads_and(got)) {
                 ok = false;
                 break;
             }
-            armed &= ~(1u << (t % kStages));
+            armed &= ~(1u << (t % NS));
             // V rows past the split's last key may hold anything (NaN included):
             // their P is 0, and 0 * NaN must not reach O
             const int nreal = kend - (kbeg + t * kTK);
             if (nreal < kTK) {
-                uint8_t *vt = smem + (t % kStages) * STAGE + KTILE;
+                uint8_t *vt = smem + (t % NS) * STAGE + KTILE;
                 const int nz = (kTK - nreal) * 8;  // 16-byte chunks a box
                 for (int i = tid; i < nz * (DV / 64); i += kDecodeThreads) {
                     const int bx = i / nz, j = i % nz;
@@ -295,15 +300,15 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
                 sm100::fence_proxy_async_smem();
             }
             __syncthreads();  // tile t visible to all; tile t-1's stage is free
-            if (t + kStages - 1 < ntiles) load_tile(t + kStages - 1);
+            if (t + NS - 1 < ntiles) load_tile(t + NS - 1);
         } else {
-            cp_async_wait<kStages - 2>();
+            cp_async_wait<NS - 2>();
             __syncthreads();  // tile t visible to all; tile t-1's stage is free
-            if (t + kStages - 1 < ntiles) load_tile(t + kStages - 1);
+            if (t + NS - 1 < ntiles) load_tile(t + NS - 1);
             cp_async_commit();
         }
 
-        const uint32_t ks = sbase + (t % kStages) * STAGE;
+        const uint32_t ks = sbase + (t % NS) * STAGE;
         const uint32_t vs = ks + KTILE;
         const int kw0 = warp * 16;
         const int key_a = kbeg + t * kTK + kw0 + g, key_b = key_a + 8;
@@ -374,7 +379,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
         // ignores the abort: they always land); the outputs stay unwritten
         if (tid == 0) {
             report_status(p.status, kStatusTimeoutDecode);
-            for (int s2 = 0; s2 < kStages; ++s2)
+            for (int s2 = 0; s2 < NS; ++s2)
                 if (armed & (1u << s2)) sm100::mbar_wait_drain(fbar + 8u * s2, (armed_ph >> s2) & 1u);
         }
         if (OWN) asm volatile("griddepcontrol.wait;\n" ::: "memory");

@@ -13,7 +13,7 @@ namespace attn {
 namespace {
 
 template <typename T, int D, int DV, int NT> int launch_t(const SharedArgs &a, bool bf16, cudaStream_t stream) {
-    constexpr int smem = kStages * kTK * (D + DV) * 2 + 64;  // ring + TMA barriers
+    constexpr int smem = kOwnStages * kTK * (D + DV) * 2 + 64;  // ring + TMA barriers
     const AttnParams &p = a.p;
     const uint64_t rows = (uint64_t)p.num_pages * p.page_size;
     CUtensorMap tk, tv;

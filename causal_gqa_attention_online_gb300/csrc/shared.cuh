@@ -17,10 +17,12 @@ namespace attn {
 
 // Costs, in units of about 100 cycles of an SM: of a tile of keys for one tile of rows (64
 // or 128 columns of K and V: the latter wait for memory) and for two, and what a job costs
-// besides, the most of it for its partials on their way out (measured: 3600 cycles a tile
-// for two tiles of rows, and 11000 a piece, in jobs of 7 to 32 tiles).
-constexpr int kCostTile64 = 20, kCostTile128 = 28, kCostTwo = 36;
-constexpr int kCostStart = 50, kCostStartTwo = 110;
+// besides, the most of it for the partials of two tiles of rows on their way out (a fit of
+// the CTAs' clocks in 2 x 12 sequences of 130 tokens: 3200 cycles a tile, 16000 a piece.
+// That call takes 277 us with 20 and 36 for a job's start and its tiles, 225 with 110 and
+// 36, 210 with 190 and 33.)
+constexpr int kCostTile64 = 22, kCostTile128 = 28, kCostTwo = 33;
+constexpr int kCostStart = 20, kCostStartTwo = 190;
 
 struct SharedArgs {
     AttnParams p;
