@@ -79,7 +79,7 @@ extern "C" int attn_fwd_paged_shared(const void *q, const void *k_pages, const v
     const bool tc = shared_tc_supported(p, dtype);
     if (algo == ATTN_ALGO_TCGEN05 && !tc) {
         set_error("the shared-prefix kernel takes bf16/fp16, D and Dv multiples of 16 in [64, 128], "
-                  "Hq / Hkv <= 128, pages of 8 rows or more and fewer than 2^30 rows");
+                  "Hq / Hkv <= 128, pages of 8 rows or more, and fewer than 2^30 rows and keys");
         return ATTN_ERR_UNSUPPORTED;
     }
     // the other kernels read every sequence's own table; without groups nothing is shared

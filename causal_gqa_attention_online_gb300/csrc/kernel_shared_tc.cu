@@ -837,8 +837,7 @@ __global__ void __launch_bounds__(256, R == 8 ? 2 : 4) shared_join_kernel(const 
             if (!own) {
                 all = n0 + find(1, two1, at1);
             } else if (i < Qb && len > in.z) {  // parts of the sequence's own keys, from the other kernel
-                const int per = own_part(in.z, len, a.own_splits);
-                all = n0 + (len - (in.z & ~63) + per - 1) / per;
+                all = n0 + own_parts(in.z, len, a.own_splits);
             } else {
                 all = n0;
             }
@@ -1061,8 +1060,8 @@ bool shared_tc_supported(const AttnParams &p, int dtype) {
     if (p.D < 64 || p.D > 128 || p.D % 16 || p.Dv < 64 || p.Dv > 128 || p.Dv % 16) return false;
     // a tile of rows holds whole tokens; a box of a page fills whole swizzle atoms
     if (p.G > 128 || p.page_size < 8) return false;
-    // rows and tokens are counted in 32 bits, two partials of each
-    return (long long)p.B * p.Q * p.Hq < (1LL << 30);
+    // rows, tokens and keys are counted in 32 bits, two partials of each row
+    return (long long)p.B * p.Q * p.Hq < (1LL << 30) && p.K < (1 << 30);
 }
 
 unsigned long long shared_tc_workspace(const AttnParams &p, int N, int nsm) {

@@ -304,14 +304,19 @@ struct SharedWalker {
 // least kOwnKeys of them; empty where beg >= fin.
 constexpr int kOwnKeys = 256;
 __host__ __device__ __forceinline__ int own_part(int lo, int end, int splits) {
-    const int base = lo & ~63, per = ((end - base + splits - 1) / splits + 63) & ~63;
-    return per < kOwnKeys ? kOwnKeys : per;
+    const uint32_t keys = (uint32_t)(end - (lo & ~63));
+    const uint32_t per = (keys / (uint32_t)splits + (keys % (uint32_t)splits != 0) + 63u) & ~63u;
+    return per < (uint32_t)kOwnKeys ? kOwnKeys : (int)per;
+}
+// How many of them have keys (end > lo).
+__host__ __device__ __forceinline__ int own_parts(int lo, int end, int splits) {
+    const uint32_t keys = (uint32_t)(end - (lo & ~63)), per = (uint32_t)own_part(lo, end, splits);
+    return (int)((keys - 1) / per) + 1;
 }
 __host__ __device__ __forceinline__ void own_split(int lo, int end, int splits, int s, int &beg, int &fin) {
     beg = fin = 0;
     if (end <= lo) return;
-    const int base = lo & ~63;
-    const long long per = own_part(lo, end, splits), b0 = base + s * per;
+    const long long per = own_part(lo, end, splits), b0 = (lo & ~63) + s * per;
     if (b0 >= end) return;
     beg = s == 0 ? lo : (int)b0;
     fin = b0 + per < end ? (int)(b0 + per) : end;

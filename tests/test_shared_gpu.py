@@ -170,6 +170,12 @@ CASES = {
     "long chunk": ([2], [200], [300, 517], 300, 4, 1, 64, 64, 128),
     "alone": ([1, 1], [64, 100], [20, 30], 1, 4, 2, 128, 128, 16),
     "long": ([4], [20000], [3, 700, 129, 1], 1, 8, 2, 128, 128, 64),
+    "long tails": ([3, 1], [128, 70], [3001, 1, 64, 1500], 1, 8, 2, 128, 128, 64),
+    "long tails, two tokens": ([2], [77], [2500, 2], 2, 16, 2, 128, 64, 128),
+    "long tails of small pages": ([3], [90], [900, 3, 258], 4, 4, 1, 64, 128, 16),
+    "many rows": ([14], [300], [130 + 3 * i for i in range(14)], 130, 6, 2, 64, 64, 64),
+    "many rows and partials": ([2, 12], [30000, 64], [131 + i for i in range(14)], 130, 6, 2, 128, 80, 64),
+    "many rows of one token": ([600], [257], [i % 5 + 1 for i in range(600)], 1, 20, 2, 64, 64, 16),
     "many groups": ([2] * 40, [64 * (n % 5) for n in range(40)], [n % 70 for n in range(80)], 1, 4, 2, 64, 64, 64),
 }
 

@@ -319,3 +319,51 @@ def test_groups_that_break_the_rules_stay_in_bounds(prog):
                 assert 0 <= b0 < c[0] and 0 <= kvh < 2 and 0 <= tok0 and tok0 + ntok <= c[0] * 3
                 assert 0 <= key0 < key_end <= 512 and base >= 0
                 assert base + ntok * 4 * (1 if ntok > 32 else 2) <= rows
+
+
+# ------------------------------------------------------------------ a sequence's own keys in parts
+
+OWN = r'''
+#include <cstdio>
+#include "shared.cuh"
+using namespace attn;
+int main() {
+    int lo, end, splits;
+    while (scanf("%d %d %d", &lo, &end, &splits) == 3) {
+        printf("%d", end > lo ? own_parts(lo, end, splits) : 0);
+        for (int s = 0; s < splits; ++s) {
+            int b, e;
+            own_split(lo, end, splits, s, b, e);
+            printf(" %d %d", b, e);
+        }
+        printf("\n");
+    }
+}
+'''
+
+
+def test_parts_of_own_keys(tmp_path):
+    nvcc = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
+    if not os.path.exists(nvcc):
+        pytest.skip("nvcc not available")
+    (tmp_path / "own.cu").write_text(OWN)
+    subprocess.run([nvcc, "-std=c++17", "-I", CSRC, "-o", str(tmp_path / "own"), str(tmp_path / "own.cu")], check=True)
+    g = np.random.default_rng(5)
+    cases = [(lo, lo + n, s) for lo in (0, 1, 63, 64, 1000) for n in (0, 1, 2, 64, 65, 255, 256, 257, 100001) for s in (1, 2, 5, 64)]
+    cases += [(2 ** 31 - 70, 2 ** 31 - 1, 7), (5, 2 ** 31 - 1, 64), (9, 3, 4)]
+    cases += [(int(g.integers(0, 5000)), int(g.integers(0, 50000)), int(g.integers(1, 65))) for _ in range(300)]
+    out = subprocess.run([str(tmp_path / "own")], input="\n".join(" ".join(map(str, c)) for c in cases),
+                         capture_output=True, text=True, timeout=60).stdout.splitlines()
+    for (lo, end, splits), line in zip(cases, out, strict=True):
+        n, *x = map(int, line.split())
+        parts = [(b, e) for b, e in zip(x[::2], x[1::2]) if e > b]
+        if end <= lo:
+            assert not parts
+            continue
+        assert all(e - b >= 256 - 63 for b, e in parts[:-1])
+        # from lo to end without a gap, the inner bounds on tiles of 64 keys
+        assert parts[0][0] == lo and parts[-1][1] == end
+        assert all(a[1] == b[0] and a[1] % 64 == 0 for a, b in zip(parts, parts[1:]))
+        # the first ones, as many as the join looks for
+        assert parts == list(zip(x[::2], x[1::2]))[: len(parts)]
+        assert len(parts) == n
