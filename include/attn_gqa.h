@@ -556,8 +556,8 @@ ATTN_API int attn_pages_compact(void *const *pools, const long long *page_bytes,
  * rows of a block as attn_cache_append writes them, for the rotated keys in fp32
  * (not rounded to `dtype` first).
  * Widths in [1, 512].  Return ATTN_OK, ATTN_ERR_INVALID, ATTN_ERR_UNSUPPORTED (2^31
- * or more blocks of rows in a sequence) or ATTN_ERR_CUDA; one launch, no workspace;
- * asynchronous on `stream`.
+ * or more blocks of rows in a sequence) or ATTN_ERR_CUDA; one launch (the 8-bit append
+ * of many queries: two), no workspace; asynchronous on `stream`.
  */
 enum attn_rope_pairs { ATTN_ROPE_HALF = 0, ATTN_ROPE_ADJACENT = 1 };
 ATTN_API int attn_rope(const void *q, const void *k, void *q_out, void *k_out, const float *cos,
@@ -603,15 +603,20 @@ ATTN_API int attn_rope_append_q8(const void *q, const void *k, const void *v, vo
  *   scale        finite
  * Kernels (`algo`): ATTN_ALGO_AUTO and ATTN_ALGO_TCGEN05 take bf16/fp16, D and Dv
  * multiples of 16 in [64, 128], Hq / Hkv <= 128, pages of 8 rows or more and fewer
- * than 2^30 rows (B * Q * Hq), with at least one group for AUTO.  AUTO runs other
+ * than 2^30 rows (B * Q * Hq) and keys (max_pages * page_size), with at least one group
+ * for AUTO.  AUTO runs other
  * problems, and the other values of algo run all of theirs, on the kernels of
  * attn_fwd_paged, which read each sequence's own table for every key.  The tcgen05
  * kernel rounds probabilities to q's type before the product with V, as attn_fwd
  * does; partial results are joined in fp32 in a fixed order, so that results do not
  * depend on timing.  A NaN or infinite value of a key that some row of the batch's
  * tile attends to may, as in attn_fwd, give NaN to rows of the tile that do not;
- * scores that are NaN give NaN.  Workspace (about 8 * (Dv + 2) * (2 * B * Q * Hq +
- * 256 * SMs) bytes) from the library's pool.  Groups that overlap or descend give
+ * scores that are NaN give NaN.  The keys that a sequence has alone go through the same
+ * kernel, or, for Q * Hq / Hkv <= 16 and widths of 64 and 128, through the decode's.
+ * Workspace from the library's pool: about 8 * (Dv + 2) * (2 * B * Q * Hq + 256 * SMs)
+ * bytes; with the decode's kernel 4 * (Dv + 2) bytes for each of these rows once, and
+ * for each row and part of its own keys (up to 64 where B * Hkv is small, one where it
+ * is 4 * SMs).  Groups that overlap or descend give
  * wrong results, never a bad address.  Return codes as attn_fwd.
  */
 ATTN_API int attn_fwd_paged_shared(const void *q, const void *k_pages, const void *v_pages,
