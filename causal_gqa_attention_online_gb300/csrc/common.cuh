@@ -21,7 +21,7 @@ enum : int {
     kStatusTimeoutQ = 0x106,
     kStatusTimeoutShared = 0x107,
     kStatusTimeoutDecode = 0x201,
-    kStatusTimeoutRope = 0x301,
+    kStatusTimeoutRope = 0x401,
 };
 
 // One attention problem.  Element strides are in elements of the storage type.

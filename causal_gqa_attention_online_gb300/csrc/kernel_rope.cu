@@ -77,6 +77,7 @@ template <typename T, int VEC> int launch_vec(const RopeArgs &a, cudaStream_t st
             RopeArgs x = a;
             const int rs = status_ptr(dev, &x.status);
             if (rs) return rs;
+            x.wait_ns = wait_limit_ns();
             if (a.adjacent) return a.block_table ? launch_stream<T, VEC, true, true>(x, s, nsm, stream)
                                                  : launch_stream<T, VEC, true, false>(x, s, nsm, stream);
             return a.block_table ? launch_stream<T, VEC, false, true>(x, s, nsm, stream)

@@ -32,6 +32,7 @@ struct RopeArgs {
     const int32_t *seqlens_new, *seqlens_k, *block_table;
     int max_pages, page_shift, num_pages;
     int *status;                // device status word
+    unsigned long long wait_ns; // limit of a wait for a copy
 };
 
 // Sequence b's rows: the first one in the buffers, how many are real, and how many

@@ -90,6 +90,8 @@ def _rope(q, k, cos, sin, q_out, k_out, positions, pairs, stream, inverse):
             raise ValueError(f"k: shape {tuple(k.shape)}, expected {lead + ('Hkv', D)}")
         Hkv = k.shape[-2]
         kx, ks = _rows("k", k, lead + (Hkv, D), q.dtype, i)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
     cx, sx, P, rot = _angles(cos, sin, i)
     px = None if positions is None else _tensor("positions", positions, torch.int32, lead, i)
     if not _here(i, stream):

@@ -638,7 +638,8 @@ ATTN_API int attn_device_status(int *detail);
 
 /*
  * Sets the time limit of the mbarrier waits inside the tcgen05 kernels
- * (prefill, backward) for launches made after the call, in nanoseconds, for
+ * (prefill, backward, shared beginnings) and of the rotations of many rows
+ * for launches made after the call, in nanoseconds, for
  * every thread and device of the process; 0 restores the default of 2 s.
  * Returns the previous limit.  A wait that runs out records ATTN_ERR_TIMEOUT
  * and a detail code in the device status word (attn_device_status), and the

@@ -476,3 +476,50 @@ def test_append_of_many_rows(case, kind, dtype, pairs, variant):
                 one_sequence(st, b, 0, n).call(again, pairs, q=False)
         for x, y in zip(pools[0], again):
             same(x, y)
+
+
+@pytest.mark.parametrize("kind", ["none", "e4m3"])
+def test_many_rows_in_two_graphs_at_once(kind):
+    # two captured appends over pools of their own, replayed on two streams at once, with rows
+    # and lengths that change between replays
+    g = np.random.default_rng(6)
+    lens, new, page = [0] * 6, [2001, 300, 1, 777, 0, 1290], 64
+    steps = [Step(g, lens, new, page, 16, 4, 128, 128, 128, "bf16", False) for _ in range(2)]
+    keep, graphs = [], []
+    for st in steps:
+        if kind == "none":
+            pools = [torch.zeros((st.P, page, 4, 128), dtype=torch.bfloat16, device=DEV) for _ in "kv"]
+        else:
+            pools = [torch.zeros((st.P, page, 4, 128), dtype=cache_ref.TORCH_CODE[kind], device=DEV) for _ in "kv"]
+            pools += [torch.zeros((st.P, 1, 4), device=DEV) for _ in "kv"]
+        x = [t.to(DEV) for t in (st.q, st.k, st.v)]
+        n, out = i32(new), torch.empty_like(x[0])
+        f = attn.attn_rope_append if kind == "none" else attn.attn_rope_append_q8
+        args = (*x, *st.angles(), *pools, i32(st.table), i32(lens))
+        call = lambda f=f, args=args, out=out, n=n: f(*args, out, seqlens_new=n)  # noqa: E731
+        call()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        graphs.append(graph)
+        keep.append((x, n, out, pools, args, f))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for turn in range(3):
+        for x, n, out, pools, args, f in keep:
+            n.copy_(i32(np.minimum(new, g.integers(0, 2002, 6))))
+            x[1].copy_(torch.randn_like(x[1]))
+            out.fill_(3)
+            for p in pools:
+                p.zero_()
+        torch.cuda.synchronize()
+        for graph, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        for x, n, out, pools, args, f in keep:
+            other = [torch.zeros_like(p) for p in pools]
+            want = f(*x, *args[3:5], *other, *args[-2:], seqlens_new=n)
+            same(out, want)
+            for a, b in zip(pools, other):
+                same(a, b)

@@ -193,6 +193,8 @@ def test_binding_checks():
         call(q, k, v, cos, sin, kp, vp_, table, lens[:1])
     with pytest.raises(ValueError, match="k: shape"):
         attn.attn_rope_append_varlen(q, k, v, lens, 3, cos, sin, kp, vp_, table, lens)
+    with pytest.raises(ValueError, match="k_out without k"):
+        attn.attn_rope(q, None, cos, sin, None, k)
     with pytest.raises(TypeError, match="int8"):
         attn.attn_rope_append_q8(q, k, v, cos, sin, kp, vp_, cos, sin, table, lens)
 
