@@ -67,13 +67,16 @@ template <typename T, int VEC> int launch_vec(const RopeArgs &a, cudaStream_t st
     const int rc = current_device(&dev);
     if (rc) return rc;
     const int nsm = sm_count(dev);
-    // many rows: more than the resident threads of rope_kernel take at once, four heads each
     const long long work = (long long)a.B * a.N * rope_items<VEC>(a.D, a.rot) *
                            ((a.qo ? a.Hq : 0) + (a.ko ? a.Hkv : 0));
+    // few: no more than the resident threads of rope_kernel take at once, four heads each
     const bool few = work < 2LL * nsm * kRopeThreads * kRopeUnroll;
+    // many: enough to make up for the stages' start (40 heads of 128 in bf16, on the GPU: 1500
+    // tokens 8.3 us and 6.7 with rope_kernel, 2400 tokens 8.5 and 12.1)
+    const bool many = work >= 4LL * nsm * kRopeThreads * kRopeUnroll;
     if constexpr (VEC * sizeof(T) == 16) {
         StreamShape s;
-        if (!few && stream_shape<T, VEC>(a, kStreamBytes, kStreamWarps, nsm, s)) {
+        if (many && stream_shape<T, VEC>(a, kStreamBytes, kStreamWarps, nsm, s)) {
             RopeArgs x = a;
             const int rs = status_ptr(dev, &x.status);
             if (rs) return rs;

@@ -19,12 +19,18 @@
 // Pieces are handed to the roles through a ring of descriptors, so that loads of the
 // next piece run ahead.  K/V tiles stream through a ring of shared-memory stages.
 //
+// Where few query rows attend to a sequence's own keys, the decode's kernel takes these
+// (kernel_shared_own.cu), as a programmatic dependent.
+//
 // shared_join_kernel adds up each row's partials (at most two chains of each CTA that its
 // jobs' shares touch) in a fixed order: results do not depend on timing.
 //
 // Bound: HBM for the keys while a group has few rows (a tile of 128 keys for both K and
 // V, D = 128, is 64 KB: 1.5 us of an SM's share of the bandwidth), the softmax and the
-// tensor core from about 256 rows on.
+// tensor core from about 256 rows on.  32 groups of 8 over up to 8192 keys of 8 heads of 128:
+// 140 us, 5.8 TB/s; 64 sequences of 4 rows over 32768: 47 us, 3600 cycles a tile of keys (the
+// tensor core is busy for 2050) and 17000 a CTA besides; 24 sequences of 130 tokens, 6 rows each,
+// over 4096 + 700: 163 us, the tensor core busy for 46%.
 #include <cuda.h>
 
 #include <cmath>
@@ -775,7 +781,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // and leaves a list of them; then warp w adds up columns 16 w .. 16 w + 15 of all rows, four
 // lanes a row, so that a load of the partials (rows side by side) is four runs of 128
 // bytes.  What a block takes is latency, of the chain from the lengths to the partials
-// (4 us), so many rows want blocks of 32 of them, few rows and many partials blocks of 8.
+// (4 us), so many rows want blocks of 32 of them, few rows and many partials blocks of 8
+// (74880 rows: 41 us and 61; 10500 rows of 2 x 12 sequences, the whole call, 38.0 and 43.2, 6300
+// rows 44.6 and 34.5).
 constexpr int kJoinMost = 8;  // partials a lane finds at a time
 
 struct JoinEntry {
@@ -980,7 +988,7 @@ void fill(SharedArgs &a, const AttnParams &p, const int32_t *cu_groups, const in
     a.ctas = nsm > 0 ? nsm : 1;
     // A sequence's own keys for few rows: the decode's way (keys on M, four warps a unit)
     // needs a fifth of the time of a tile of 128 rows that are nearly all empty, and none of
-    // its set-up (64 x 250 keys of 8 heads: 12 us).
+    // its set-up (64 x 250 keys of 8 heads took 12 us more there).
     a.own_splits = 0;
     if (own_decode_supported(p)) {
         const long long units = (long long)p.B * p.Hkv, want = (4LL * a.ctas + units - 1) / units;

@@ -387,7 +387,8 @@ def test_append_in_a_graph():
 # calls for a few of its rows at a time give, bit for bit.
 
 MANY = [(4, 1501, 8, 4, 96, 48), (1, 4099, 3, 1, 64, 64), (2, 1301, 40, 8, 256, 64), (1, 401, 100, 4, 512, 512),
-        (3, 2001, 6, 2, 80, 40), (1, 6007, 14, 2, 72, 24)]
+        (3, 2001, 6, 2, 80, 40), (1, 6007, 14, 2, 72, 24), (3, 4001, 8, 4, 96, 48),
+        (1, 20011, 3, 1, 128, 128)]
 
 
 @pytest.mark.parametrize("dtype,pairs", [("bf16", "half"), ("f16", "adjacent"), ("f32", "half"), ("f32", "adjacent")])
