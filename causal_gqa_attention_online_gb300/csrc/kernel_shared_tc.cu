@@ -167,7 +167,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     SharedLens z = shared_lens_of(a);
     if (a.N < kCopied && p.B <= kCopied) {
         int32_t *to = reinterpret_cast<int32_t *>(gbase + L::KV_OFF);
-        for (int i = tid; i <= a.N; i += kThreads) {
+        // (without groups both of their arrays may be null)
+        for (int i = tid; a.N > 0 && i <= a.N; i += kThreads) {
             to[i] = z.cu[i];
             if (i < a.N) to[kCopied + i] = z.shared[i];
         }

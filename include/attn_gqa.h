@@ -594,7 +594,7 @@ ATTN_API int attn_rope_append_q8(const void *q, const void *k, const void *v, vo
  *   lse as in attn_fwd_paged (seqlens_k counts all keys of a sequence)
  *   cu_groups    int32 [num_groups + 1] on the device, ascending: group n is the
  *                sequences [cu_groups[n], cu_groups[n + 1]) of the batch; the others
- *                share nothing
+ *                share nothing (with num_groups 0 it and shared_lens may be NULL)
  *   shared_lens  int32 [num_groups] on the device: the first shared_lens[n] keys of
  *                the members are the same -- their table entries name the same pages,
  *                or pages of equal contents (a partly filled page copied for each, as

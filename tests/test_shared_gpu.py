@@ -396,3 +396,26 @@ def test_a_serving_run(cached):
             # bf16: P and O round by 2^-8 of values up to 4.5; int8: half a step, 2^-7 of
             # the largest, in each element (as in the 8-bit cache's own tests)
             assert err <= (0.1 if eight else 4.5 * 4 * HALF["bf16"])
+
+
+def c_call(b, N, cu, pre, algo, k=None, v=None, table=None, M=None):
+    """The C entry point over b's tensors, with what a C program may pass beside them."""
+    o = torch.full((b.B, b.Q, b.Hq, b.Dv), 3.0, dtype=DT[b.dtype], device=DEV)
+    lse = torch.full((b.B, b.Q, b.Hq), 3.0, device=DEV)
+    lens = i32(b.lens)
+    rc = attn.load_library().attn_fwd_paged_shared(
+        b.q.data_ptr(), k, v, o.data_ptr(), lse.data_ptr(), b.B, b.Hq, b.Hkv, b.Q, b.D, b.Dv, table, M, b.page, b.P,
+        None, lens.data_ptr(), cu, pre, N, 1 / math.sqrt(b.D), {"f32": 0, "f16": 1, "bf16": 2}[b.dtype], algo,
+        torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    return rc, o, lse
+
+
+@pytest.mark.parametrize("D,Q", [(128, 1), (80, 1), (64, 30)])
+def test_no_groups_without_their_arrays(D, Q):
+    # num_groups 0 with NULL in place of cu_groups and shared_lens, own keys by either kernel
+    b = Batch(21, [1, 1, 1], [0, 0, 0], [90, 1, 200], Q, 8, 2, D, D, 16, "bf16")
+    table = i32(b.table)
+    rc, o, lse = c_call(b, 0, None, None, 2, b.k.data_ptr(), b.v.data_ptr(), table.data_ptr(), b.M)
+    assert rc == 0, attn.last_error()
+    b.compare(o, lse)
