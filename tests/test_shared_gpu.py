@@ -419,3 +419,15 @@ def test_no_groups_without_their_arrays(D, Q):
     rc, o, lse = c_call(b, 0, None, None, 2, b.k.data_ptr(), b.v.data_ptr(), table.data_ptr(), b.M)
     assert rc == 0, attn.last_error()
     b.compare(o, lse)
+
+
+@pytest.mark.parametrize("algo", [0, 2])
+@pytest.mark.parametrize("D,Q", [(128, 1), (80, 3)])
+def test_tables_without_entries(D, Q, algo):
+    # max_pages 0: no sequence has a key, and pages and table may be NULL as in attn_fwd_paged
+    b = Batch(22, [2, 1], [0, 0], [0, 0, 0], Q, 8, 2, D, D, 16, "bf16")
+    b.lens[:] = 7  # clamped to the capacity
+    for pages in (None, b.k.data_ptr()):
+        rc, o, lse = c_call(b, 2, b.cu.data_ptr(), b.shared.data_ptr(), algo, pages, pages, None, 0)
+        assert rc == 0, attn.last_error()
+        assert not o.view(torch.int16).any() and (lse == -math.inf).all()
