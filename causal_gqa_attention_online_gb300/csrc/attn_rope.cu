@@ -66,14 +66,19 @@ int validate_rope(const RopeArgs &a, int pairs, int dtype) {
     return ATTN_OK;
 }
 
+// Whether `a` of na bytes and `b` of nb share none.
+bool disjoint(const void *a, long long na, const void *b, long long nb) {
+    if (a == nullptr || b == nullptr || na == 0 || nb == 0) return true;
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+    return a0 + (uintptr_t)na <= b0 || b0 + (uintptr_t)nb <= a0;
+}
+
 // Whether rows of `width` elements, `stride` apart, share no byte with the dense rows
 // (of `out_width`) at `out`.
 bool apart(const void *in, long long stride, long long width, const void *out, long long out_width,
            long long rows, int es) {
-    if (in == nullptr || out == nullptr || rows == 0 || width == 0 || out_width == 0) return true;
-    const uintptr_t i0 = reinterpret_cast<uintptr_t>(in), o0 = reinterpret_cast<uintptr_t>(out);
-    return i0 + (uintptr_t)(((rows - 1) * stride + width) * es) <= o0 ||
-           o0 + (uintptr_t)(rows * out_width * es) <= i0;
+    if (rows == 0 || width == 0) return true;
+    return disjoint(in, ((rows - 1) * stride + width) * es, out, rows * out_width * es);
 }
 
 int overlap_error(const char *what) {
@@ -95,8 +100,10 @@ int validate_pages(int page_size, int max_pages, int num_pages) {
     return ATTN_OK;
 }
 
-// What both appends check beyond the cache itself; *none: there is nothing to do.
-int validate_rows(const RopeArgs &a, int total_new, int pairs, int dtype, bool *none) {
+// What both appends check beyond the cache itself; *none: there is nothing to do.  code_size,
+// nblk: bytes of an element of the pages, blocks of scales of a page (or 0).
+int validate_rows(const RopeArgs &a, const float *k_scale, const float *v_scale, int code_size, int nblk,
+                  int total_new, int pairs, int dtype, bool *none) {
     *none = false;
     int rc = validate_rope(a, pairs, dtype);
     if (rc) return rc;
@@ -127,6 +134,13 @@ int validate_rows(const RopeArgs &a, int total_new, int pairs, int dtype, bool *
         !apart(a.k, a.k_stride, (long long)a.Hkv * a.D, a.qo, qw, rows, es) ||
         !apart(a.v, a.v_stride, (long long)a.Hkv * a.Dv, a.qo, qw, rows, es))
         return overlap_error("q_out");
+    const long long out = rows * qw * es, heads = (long long)a.num_pages * a.Hkv;
+    const long long scales = heads * nblk * 4, row = heads * code_size << a.page_shift;
+    if (!disjoint(a.qo, out, a.ko, row * a.D) || !disjoint(a.qo, out, a.vo, row * a.Dv) ||
+        !disjoint(a.qo, out, k_scale, scales) || !disjoint(a.qo, out, v_scale, scales)) {
+        set_error("q_out overlaps the cache");
+        return ATTN_ERR_INVALID;
+    }
     return ATTN_OK;
 }
 
@@ -178,6 +192,10 @@ int attn_rope(const void *q, const void *k, void *q_out, void *k_out, const floa
     if ((!(k == k_out && k_stride == kw) && !apart(k, k_stride, kw, k_out, kw, rows, es)) ||
         !apart(q, q_stride, qw, k_out, kw, rows, es))
         return overlap_error("k_out");
+    if (!apart(q_out, qw, qw, k_out, kw, rows, es)) {
+        set_error("q_out and k_out overlap");
+        return ATTN_ERR_INVALID;
+    }
     if (rows == 0 || Hq + (long long)Hkv == 0) return ATTN_OK;
     if (Hq == 0) a.q = a.qo = nullptr;
     if (Hkv == 0) a.k = a.ko = nullptr;
@@ -208,7 +226,7 @@ int attn_rope_append(const void *q, const void *k, const void *v, void *q_out, v
                   total_new, seqlens_new, seqlens_k, block_table, max_pages, shift_of(page_size),
                   num_pages};
     bool none = false;
-    rc = validate_rows(a, total_new, pairs, dtype, &none);
+    rc = validate_rows(a, nullptr, nullptr, dtype == ATTN_F32 ? 4 : 2, 0, total_new, pairs, dtype, &none);
     if (rc || none) return rc;
     return launch_rope(a, dtype, reinterpret_cast<cudaStream_t>(stream));
 }
@@ -231,7 +249,7 @@ int attn_rope_append_q8(const void *q, const void *k, const void *v, void *q_out
                   total_new, seqlens_new, seqlens_k, block_table, max_pages, shift_of(page_size),
                   num_pages};
     bool none = false;
-    rc = validate_rows(a, total_new, pairs, dtype, &none);
+    rc = validate_rows(a, k_scale, v_scale, 1, page_size / block_size, total_new, pairs, dtype, &none);
     if (rc || none) return rc;
     return launch_rope_q8(a, k_scale, v_scale, page_size / block_size, shift_of(block_size),
                           cache_dtype, dtype, reinterpret_cast<cudaStream_t>(stream));

@@ -538,7 +538,8 @@ ATTN_API int attn_pages_compact(void *const *pools, const long long *page_bytes,
  * the new rows to it).  Row i of sequence b goes to its row seqlens_k[b] + i, and
  * that is its position too unless `positions` says otherwise.
  *   q [B, N, Hq, D], k [B, N, Hkv, D], v [B, N, Hkv, Dv]   rows, strides as above
- *                (q and q_out may be NULL together, with Hq 0)
+ *                (q and q_out may be NULL together, with Hq 0; q_out may be q itself
+ *                where that is dense, and overlaps neither other rows nor the cache)
  *   seqlens_new  int32 [B], new rows of each sequence (clamped to [0, N]), or NULL
  *                for N of each; q_out gets +0 in the other rows
  *   cu_seqlens_new   NULL, or int32 [B + 1]: the rows are packed [total_new, ..],

@@ -524,3 +524,33 @@ def test_many_rows_in_two_graphs_at_once(kind):
             same(out, want)
             for a, b in zip(pools, other):
                 same(a, b)
+
+
+@pytest.mark.parametrize("kind", ["none", "int8"])
+def test_outputs_side_by_side(kind):
+    # outputs that touch, without a byte in common, are taken
+    g = np.random.default_rng(11)
+    q, k, v = (rows(g, (2, 5, h, 64), "bf16").to(DEV) for h in (4, 2, 2))
+    cos, sin = (torch.from_numpy(t).to(DEV) for t in rope_ref.angles(9, 64))
+    want = attn.attn_rope(q, k, cos, sin)
+    x = torch.empty(q.numel() + k.numel(), dtype=q.dtype, device=DEV)
+    got = attn.attn_rope(q, k, cos, sin, x[: q.numel()].view(q.shape), x[q.numel():].view(k.shape))
+    same(got[0], want[0]), same(got[1], want[1])
+    got = attn.attn_rope(q, k, cos, sin, x[k.numel():].view(q.shape), x[: k.numel()].view(k.shape))
+    same(got[0], want[0]), same(got[1], want[1])
+    # q's rows, then k's pages, then the scales, v's pages, and q's again
+    code = torch.bfloat16 if kind == "none" else torch.int8
+    n, size = 2 * 16 * 2 * 64, code.itemsize
+    at, parts = 0, []
+    mem = torch.zeros(2 * q.numel() * 2 + 2 * n * size + 2 * 32, dtype=torch.uint8, device=DEV)
+    for b, t, shape in ((q.numel() * 2, q.dtype, q.shape), (n * size, code, (2, 16, 2, 64)), (32, torch.float32, (2, 2, 2)),
+                        (32, torch.float32, (2, 2, 2)), (n * size, code, (2, 16, 2, 64)), (q.numel() * 2, q.dtype, q.shape)):
+        parts.append(mem[at: at + b].view(t).view(shape))
+        at += b
+    for out in (parts[0], parts[5]):
+        where = (i32([[1], [0]]), i32([0, 3]))
+        if kind == "none":
+            y = attn.attn_rope_append(q, k, v, cos, sin, parts[1], parts[4], *where, out)
+        else:
+            y = attn.attn_rope_append_q8(q, k, v, cos, sin, parts[1], parts[4], *parts[2:4], *where, out)
+        same(y, attn.attn_rope(q, None, cos, sin, positions=i32(np.arange(5) + [[0], [3]]))[0])
