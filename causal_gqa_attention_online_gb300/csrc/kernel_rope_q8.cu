@@ -307,11 +307,11 @@ __global__ void __launch_bounds__(128, 3) rope_q8_stream_kernel(const __grid_con
         if (pos[r] >= 0) tr.load_from(c, c + half, 1.f);
         else tr.set_nan();
     };
-    bool ok = half == 0 || mbar_wait_drain(bar(2), 0, a.wait_ns);
+    bool ok = half == 0 || mbar_wait_within(bar(2), 0, a.wait_ns);
     int n = 0;
     for (; n < count; ++n) {
         const int h = n * kHeads + (int)threadIdx.x / TG, heads = min(kHeads, a.Hkv - n * kHeads);
-        ok &= mbar_wait_drain(bar(n & 1), (uint32_t)(n >> 1) & 1u, a.wait_ns);
+        ok &= mbar_wait_within(bar(n & 1), (uint32_t)(n >> 1) & 1u, a.wait_ns);
         RopeQ8Unit<T, CODE, TG, VEC, ADJ> unit(g, sq, span, page, which, h < a.Hkv ? h : 0);
         const T *tile = reinterpret_cast<const T *>(smem + (n & 1) * g.stage) + (int)threadIdx.x / TG * W;
         uint32_t mx = 0;

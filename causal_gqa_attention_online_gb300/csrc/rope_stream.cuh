@@ -115,7 +115,7 @@ __device__ __forceinline__ void rope_stream(const RopeArgs &a, const StreamShape
     for (int n = 0; n < count; ++n) {
         const int s = n % g.stages;
         // (a wait that runs out: nothing more is computed, and the copies are waited for)
-        ok = __all_sync(0xffffffffu, mbar_wait_drain(bar(s), (uint32_t)(n / g.stages) & 1u, a.wait_ns));
+        ok = __all_sync(0xffffffffu, mbar_wait_within(bar(s), (uint32_t)(n / g.stages) & 1u, a.wait_ns));
         if (!ok) break;
         uint8_t *part = ring + (size_t)s * g.tokens * g.row;
         for (int k = 0; k < g.tokens; ++k) {

@@ -51,6 +51,18 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
     return done != 0;
 }
 
+// The same without a suspension.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
 __device__ __forceinline__ uint64_t globaltimer_ns() {
     uint64_t t;
     asm volatile("mov.u64 %0, %globaltimer;\n" : "=l"(t));
@@ -84,6 +96,18 @@ __device__ __forceinline__ bool mbar_wait_drain(uint32_t bar, uint32_t parity,
     const uint64_t t0 = globaltimer_ns();
     for (;;) {
         if (mbar_try_wait(bar, parity)) return true;
+        if (globaltimer_ns() - t0 > limit_ns) return false;
+    }
+}
+
+// A wait for copies, which a correct kernel's try_wait hardly ever sees return "not yet": with
+// a limit below the suspension (a hint of 1 ns does not shorten it) the barrier is polled, so
+// that such a limit counts, too.
+__device__ __forceinline__ bool mbar_wait_within(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+    if (limit_ns >= kSuspendHintNs) return mbar_wait_drain(bar, parity, limit_ns);
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+        if (mbar_test_wait(bar, parity)) return true;
         if (globaltimer_ns() - t0 > limit_ns) return false;
     }
 }

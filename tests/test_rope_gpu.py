@@ -554,3 +554,39 @@ def test_outputs_side_by_side(kind):
         else:
             y = attn.attn_rope_append_q8(q, k, v, cos, sin, parts[1], parts[4], *parts[2:4], *where, out)
         same(y, attn.attn_rope(q, None, cos, sin, positions=i32(np.arange(5) + [[0], [3]]))[0])
+
+
+@pytest.mark.parametrize("kind,with_q", [("rows", True), ("none", True), ("e4m3", True), ("e4m3", False)])
+def test_waits_that_run_out_are_reported(kind, with_q):
+    # A wait for a copy gives up once the limit has passed.  The first stage of a warp, or of
+    # a block, comes from global memory, hundreds of ns away, so with a limit of 1 ns some
+    # wait runs out; the launch ends, and the next one is right.
+    st = Step(np.random.default_rng(15), [0, 70, 3000, 5], [3001, 0, 1400, 1], 64, 32, 8, 128, 128, 128, "bf16", False)
+    cos, sin = st.angles()
+    q, k = st.q.to(DEV), st.k.to(DEV)
+
+    def call():
+        if kind == "rows":
+            return list(attn.attn_rope(q, k, cos, sin))
+        code = torch.bfloat16 if kind == "none" else cache_ref.TORCH_CODE[kind]
+        pools = [torch.zeros((st.P, 64, 8, 128), dtype=code, device=DEV) for _ in "kv"]
+        if kind != "none":
+            pools += [torch.zeros((st.P, 1, 8), device=DEV) for _ in "kv"]
+        y = st.call(pools, "half", q=with_q)
+        return [y, *pools] if with_q else pools
+
+    want = call()
+    torch.cuda.synchronize()
+    attn.device_status()
+    before = attn.set_wait_limit(1)
+    try:
+        call()
+        torch.cuda.synchronize()
+        assert attn.device_status() == (4, 0x401)
+    finally:
+        attn.set_wait_limit(before)
+    got = call()
+    torch.cuda.synchronize()
+    assert attn.device_status()[0] == 0
+    for a, b in zip(got, want):
+        same(a, b)
