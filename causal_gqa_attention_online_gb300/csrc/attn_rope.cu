@@ -228,6 +228,7 @@ int attn_rope_append(const void *q, const void *k, const void *v, void *q_out, v
     bool none = false;
     rc = validate_rows(a, nullptr, nullptr, dtype == ATTN_F32 ? 4 : 2, 0, total_new, pairs, dtype, &none);
     if (rc || none) return rc;
+    if (a.cu != nullptr && total_new < a.N) a.N = total_new;  // (no sequence has more)
     return launch_rope(a, dtype, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -251,6 +252,7 @@ int attn_rope_append_q8(const void *q, const void *k, const void *v, void *q_out
     bool none = false;
     rc = validate_rows(a, k_scale, v_scale, 1, page_size / block_size, total_new, pairs, dtype, &none);
     if (rc || none) return rc;
+    if (a.cu != nullptr && total_new < a.N) a.N = total_new;  // (no sequence has more)
     return launch_rope_q8(a, k_scale, v_scale, page_size / block_size, shift_of(block_size),
                           cache_dtype, dtype, reinterpret_cast<cudaStream_t>(stream));
 }

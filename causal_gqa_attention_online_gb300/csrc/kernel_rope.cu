@@ -67,6 +67,9 @@ template <typename T, int VEC> int launch_vec(const RopeArgs &a, cudaStream_t st
     const int rc = current_device(&dev);
     if (rc) return rc;
     const int nsm = sm_count(dev);
+    // (Of packed rows, too, the places up to N of each sequence: rope_kernel has blocks for all
+    // of them, rope_stream_kernel for the rows that are there.  63 single rows and 500 more, N
+    // 500: 28 us and 7.)
     const long long work = (long long)a.B * a.N * rope_items<VEC>(a.D, a.rot) *
                            ((a.qo ? a.Hq : 0) + (a.ko ? a.Hkv : 0));
     // few: no more than the resident threads of rope_kernel take at once, four heads each

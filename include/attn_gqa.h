@@ -543,8 +543,9 @@ ATTN_API int attn_pages_compact(void *const *pools, const long long *page_bytes,
  *   seqlens_new  int32 [B], new rows of each sequence (clamped to [0, N]), or NULL
  *                for N of each; q_out gets +0 in the other rows
  *   cu_seqlens_new   NULL, or int32 [B + 1]: the rows are packed [total_new, ..],
- *                sequence b's are [cu[b], cu[b + 1]), at most N of them; rows of
- *                q_out outside every sequence are left as they were
+ *                sequence b's are [cu[b], cu[b + 1]), at most N of them (a bound
+ *                near the longest is the fastest); rows of q_out outside every
+ *                sequence are left as they were
  *   positions    int32, one for each row of the buffers, or NULL
  *   rot 0 (cos and sin may be NULL then) appends without a rotation
  *   k_pages [num_pages, page_size, Hkv, D], v_pages [.., Dv] in `dtype`,

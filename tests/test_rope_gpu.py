@@ -590,3 +590,22 @@ def test_waits_that_run_out_are_reported(kind, with_q):
     assert attn.device_status()[0] == 0
     for a, b in zip(got, want):
         same(a, b)
+
+
+@pytest.mark.parametrize("kind", ["none", "int8"])
+def test_max_new_beyond_the_rows(kind):
+    # max_new is a bound: one that no sequence can reach runs what a near one runs
+    st = Step(np.random.default_rng(16), [0, 70], [1, 1023], 64, 32, 8, 128, 128, 128, "bf16", True)
+    got, launches = [], []
+    for st.N in (1024, 1 << 20):
+        code = torch.bfloat16 if kind == "none" else cache_ref.TORCH_CODE[kind]
+        pools = [torch.zeros((st.P, 64, 8, 128), dtype=code, device=DEV) for _ in "kv"]
+        if kind != "none":
+            pools += [torch.zeros((st.P, 1, 8), device=DEV) for _ in "kv"]
+        before = attn.kernel_launches()
+        got.append([st.call(pools, "half"), *pools])
+        launches.append(attn.kernel_launches() - before)
+    st.check_q(got[0][0], "half")
+    for a, b in zip(*got):
+        same(a, b)
+    assert launches[0] == launches[1], launches
