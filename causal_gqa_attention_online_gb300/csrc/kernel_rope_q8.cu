@@ -11,9 +11,9 @@
 // single-token call is launch latency.
 //
 // rope_q8_kernel: a unit is one block of one head of K or V by one or four warps, as in
-// the append kernel; a thread keeps what it turned (64 floats) between the maximum and the
-// codes, and turns again (from L2) what is left over.  The blocks behind the units turn the
-// queries.
+// the append kernel; a thread keeps what it turned (64 floats, of single elements 16: eight
+// items) between the maximum and the codes, and turns again (from L2) what is left over.
+// The blocks behind the units turn the queries.
 //
 // rope_q8_stream_kernel, for many tokens in 16-byte vectors: a unit of 64 tokens is 16 KB and
 // some 1000 instructions a warp behind a chain of three loads (length, page, rows), 5 us of
@@ -33,7 +33,7 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kKeepFloats = 64;           // a thread keeps
+constexpr int kKeepFloats = 64;           // a thread keeps, in eight items at most
 constexpr int kTileRows = 128;            // of a block of tokens, at most
 constexpr int kTileBytes = 68 * 1024;     // of a block of threads: three an SM
 
@@ -73,7 +73,8 @@ __device__ __forceinline__ float largest(float a, float b, float c) {
 // finds the largest magnitude, put() writes their codes.
 template <typename T, int CODE, int TG, int VEC, bool ADJ> struct RopeQ8Unit {
     using Op = CodeOps<CODE>;
-    static constexpr int kKeep = kKeepFloats / (2 * VEC) < 8 ? kKeepFloats / (2 * VEC) : 8;  // items
+    // items (32 single ones: 29 us become 47 in the case at launch_size)
+    static constexpr int kKeep = kKeepFloats / (2 * VEC) < 8 ? kKeepFloats / (2 * VEC) : 8;
     struct Place {
         int r, c;
     };
@@ -414,9 +415,13 @@ template <typename T, int CODE, int TG, int VEC> int launch_t(RopeQ8Args g, int 
 }
 
 template <typename T, int CODE, int VEC> int launch_size(const RopeQ8Args &g, int nsm, cudaStream_t stream) {
-    // one warp a unit while its rows fit half of what one warp keeps, four otherwise
+    // One warp a unit while its rows fit half of what one warp keeps, four otherwise.  (Of
+    // single elements, an item of a plain column is one: with 1024 for them, too, most of a
+    // unit was read and turned twice.  16 x 1024 tokens of 8 + 4 heads of 20 in blocks of 32:
+    // 29 us, now 20; of 127 in blocks of 8: 136, now 120.)
+    constexpr int kWarp = 32 * RopeQ8Unit<T, CODE, 32, VEC, false>::kKeep * (VEC == 1 ? 1 : 2 * VEC);
     const long long most = g.r.N < (1 << g.blk_shift) ? g.r.N : (1 << g.blk_shift);
-    const bool small = most * (g.r.D > g.r.Dv ? g.r.D : g.r.Dv) <= 32 * kKeepFloats / 2;
+    const bool small = most * (g.r.D > g.r.Dv ? g.r.D : g.r.Dv) <= kWarp / 2;
     return small ? launch_t<T, CODE, 32, VEC>(g, nsm, stream) : launch_t<T, CODE, 128, VEC>(g, nsm, stream);
 }
 
