@@ -609,3 +609,24 @@ def test_max_new_beyond_the_rows(kind):
     for a, b in zip(*got):
         same(a, b)
     assert launches[0] == launches[1], launches
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("packed", [False, True])
+def test_many_rows_without_a_rotation(dtype, packed):
+    # rot 0: rows into pages of their type, and q, as they are
+    lens, new, page, D, Dv = [0, 70, 5], [3001, 0, 1400], 64, 128, 64
+    st = Step(np.random.default_rng(17), lens, new, page, 16, 8, D, Dv, 0, dtype, packed)
+    pools = [torch.full((st.P, page, 8, w), 3.0, dtype=DT[dtype], device=DEV) for w in (D, Dv)]
+    want = [p.cpu() for p in pools]
+    got = st.call(pools, "half").cpu()
+    for b, n in enumerate(new):
+        at = slice(int(st.cu[b]), int(st.cu[b]) + n) if packed else (b, slice(0, n))
+        same(got[at], st.q[at])
+        j = lens[b] + np.arange(n)
+        for w, x in zip(want, (st.k, st.v)):
+            w[torch.from_numpy(st.table[b][j // page]).long(), torch.from_numpy(j % page)] = x[at]
+    for p, w in zip(pools, want):
+        same(p, w)
+    x, _ = attn.attn_rope(st.q.to(DEV), None, None, None)
+    same(x, st.q)

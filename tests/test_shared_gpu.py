@@ -431,3 +431,13 @@ def test_tables_without_entries(D, Q, algo):
         rc, o, lse = c_call(b, 2, b.cu.data_ptr(), b.shared.data_ptr(), algo, pages, pages, None, 0)
         assert rc == 0, attn.last_error()
         assert not o.view(torch.int16).any() and (lse == -math.inf).all()
+
+
+@pytest.mark.parametrize("D", [64, 80])  # own keys by the decode's kernel, and by the tcgen05 one
+@pytest.mark.parametrize("sizes,pre", [([700, 1, 1399], [100, 0, 33]), ([1] * 2050, [16 * (n % 4) for n in range(2050)]),
+                                       ([2, 3] * 150, [n % 90 for n in range(300)])])
+def test_hundreds_and_thousands_of_sequences_and_groups(sizes, pre, D):
+    # more of them than are copied to shared memory (2048), or than a block's threads look at
+    # in one go (128 groups)
+    b = Batch(23, sizes, pre, [1 + i * 7 % 40 for i in range(sum(sizes))], 1, 2, 1, D, D, 16, "bf16")
+    b.check(algo="tcgen05")
