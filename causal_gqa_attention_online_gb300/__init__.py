@@ -25,5 +25,6 @@ __all__ = ["ALGOS", "MASKS", "ATTN_ALGO_AUTO", "ATTN_ALGO_DECODE", "ATTN_ALGO_GE
            "attn_fwd_paged", "attn_fwd_paged_q8", "attn_fwd_paged_shared", "attn_fwd_staged", "attn_fwd_varlen",
            "attn_lse_combine", "attn_pages_compact", "attn_pages_copy", "attn_pages_fork",
            "attn_rope", "attn_rope_append", "attn_rope_append_q8", "attn_rope_append_q8_varlen",
-           "attn_rope_append_varlen", "attn_rope_bwd", "device_status", "kernel_launches", "last_error", "library_path", "load_library",
+           "attn_rope_append_varlen", "attn_rope_bwd", "device_status", "kernel_launches",
+           "last_error", "library_path", "load_library",
            "pack_mask", "set_wait_limit"]

@@ -32,8 +32,8 @@ __global__ void __launch_bounds__(32 * kStreamWarps, 1)
 }
 
 template <typename T, int VEC, bool ADJ, bool PAGED>
-__global__ void __launch_bounds__(kRopeThreads, VEC * sizeof(T) == 16 ? 2 : 3) rope_kernel(const __grid_constant__ RopeArgs a,
-                                                               const RopeShape g) {
+__global__ void __launch_bounds__(kRopeThreads, VEC * sizeof(T) == 16 ? 2 : 3)
+    rope_kernel(const __grid_constant__ RopeArgs a, const RopeShape g) {
     rope_rows<T, VEC, ADJ, PAGED>(a, g, blockIdx.x, blockIdx.y + blockIdx.z * gridDim.y);
 }
 

@@ -118,7 +118,8 @@ template <typename T, int CODE, int TG, int VEC, bool ADJ> struct RopeQ8Unit {
     }
     // `src`, `stride`: the head's first new row; trig(row, pair, angles): its angles
     template <typename F>
-    __device__ __forceinline__ void fetch(const Place &p, const T *src, long long stride, F trig, float (&to)[2 * VEC]) {
+    __device__ __forceinline__ void fetch(const Place &p, const T *src, long long stride, F trig,
+                                          float (&to)[2 * VEC]) {
         const RopeItem<VEC> it = rope_item<VEC, ADJ>(p.c, rot);
         RowVec<T, VEC> x, w;
         x.load(src + p.r * stride + it.a);

@@ -26,11 +26,15 @@
 // jobs' shares touch) in a fixed order: results do not depend on timing.
 //
 // Bound: HBM for the keys while a group has few rows (a tile of 128 keys for both K and
-// V, D = 128, is 64 KB: 1.5 us of an SM's share of the bandwidth), the softmax and the
-// tensor core from about 256 rows on.  32 groups of 8 over up to 8192 keys of 8 heads of 128:
-// 140 us, 5.8 TB/s; 64 sequences of 4 rows over 32768: 47 us, 3600 cycles a tile of keys (the
-// tensor core is busy for 2050) and 17000 a CTA besides; 24 sequences of 130 tokens, 6 rows each,
-// over 4096 + 700: 163 us, the tensor core busy for 46%.
+// V, D = 128, is 64 KB: 1.5 us of an SM's share of the bandwidth); from about 256 rows on
+// the chain S -> maximum -> exponentials -> P -> PV -> next S, which is serial in each of the
+// two chains: neither the tensor core nor the exponentials are busy for half of it.  32 groups
+// of 8 over up to 8192 keys of 8 heads of 128: 140 us, 5.8 TB/s.  64 sequences of 4 rows over
+// 32768: 47 us at 1.94 GHz; an SM's CTA runs for 80000 cycles, for 13.5 tiles of keys by two of
+// rows, and its tensor core for 27600.  21 sequences of 4 tokens, 64-wide heads of 4 rows, over
+// 100000: 72 us, 125000 cycles for 20.6 tiles of keys by three of rows, 31600 of tensor core.
+// 24 sequences of 130 tokens, 6 rows each, over 4096 + 700: 162 us, 270000 cycles of 317000 (the
+// CTAs do not end together), the tensor core busy for 46%.
 #include <cuda.h>
 
 #include <cmath>
@@ -971,7 +975,8 @@ unsigned long long layout(SharedArgs &a, void *ws) {
     for (int k = 0; k < 2; ++k) a.span[k] = reinterpret_cast<int2 *>(take(8ull * p.B * p.Q * p.Hkv));
     const unsigned long long rows = ((unsigned long long)shared_rows(p, a.ctas) + 31) / 32 * 32;
     for (int k = 0; k < 2; ++k) {
-        const unsigned long long r = k == 1 && a.own_splits > 0 ? (unsigned long long)a.own_splits * p.B * p.Q * p.Hq : rows;
+        const bool own = k == 1 && a.own_splits > 0;
+        const unsigned long long r = own ? (unsigned long long)a.own_splits * p.B * p.Q * p.Hq : rows;
         a.part_ml[k] = reinterpret_cast<float2 *>(take(8ull * r));
         a.part_o[k] = reinterpret_cast<float *>(take(4ull * r * p.Dv));
     }
@@ -989,7 +994,9 @@ void fill(SharedArgs &a, const AttnParams &p, const int32_t *cu_groups, const in
     a.ctas = nsm > 0 ? nsm : 1;
     // A sequence's own keys for few rows: the decode's way (keys on M, four warps a unit)
     // needs a fifth of the time of a tile of 128 rows that are nearly all empty, and none of
-    // its set-up (64 x 250 keys of 8 heads took 12 us more there).
+    // its set-up (64 x 250 keys of 8 heads took 12 us more there; 74 sequences over 4096 shared
+    // keys and up to 250 of their own 83 us, now 68).  It is a launch more: 4 x 4 sequences of
+    // 320 + 40 keys 31 us a call for 29, on the GPU 18 either way.
     a.own_splits = 0;
     if (own_decode_supported(p)) {
         const long long units = (long long)p.B * p.Hkv, want = (4LL * a.ctas + units - 1) / units;

@@ -123,7 +123,8 @@ __device__ __forceinline__ void rope_stream(const RopeArgs &a, const StreamShape
             uint8_t *mine = part + k * g.row;
             if (t.kind == 0) continue;
             if (t.kind == 2) {  // zeros; a row of q is whole vectors of 16 bytes
-                for (int e = lane * 16; e < g.q; e += 512) *reinterpret_cast<uint4 *>(mine + e) = make_uint4(0, 0, 0, 0);
+                for (int e = lane * 16; e < g.q; e += 512)
+                    *reinterpret_cast<uint4 *>(mine + e) = make_uint4(0, 0, 0, 0);
                 continue;
             }
             if (h0 >= hstep) continue;
@@ -183,7 +184,8 @@ __device__ __forceinline__ void rope_stream(const RopeArgs &a, const StreamShape
 }
 
 // Stages of `blocks` blocks of up to `warps` warps with `bytes` each; false: rows too long.
-template <typename T, int VEC> bool stream_shape(const RopeArgs &a, long long bytes, int warps, int blocks, StreamShape &g) {
+template <typename T, int VEC>
+bool stream_shape(const RopeArgs &a, long long bytes, int warps, int blocks, StreamShape &g) {
     const long long es = sizeof(T);
     const long long q = a.qo ? a.Hq * (long long)a.D * es : 0, k = a.ko ? a.Hkv * (long long)a.D * es : 0;
     const long long v = a.vo ? a.Hkv * (long long)a.Dv * es : 0, trig = a.rot / 2 * 4LL;

@@ -18,9 +18,9 @@ namespace attn {
 // Costs, in units of about 100 cycles of an SM: of a tile of keys for one tile of rows (64
 // or 128 columns of K and V: the latter wait for memory) and for two, and what a job costs
 // besides, the most of it for the partials of two tiles of rows on their way out (a fit of
-// the CTAs' clocks in 2 x 12 sequences of 130 tokens: 3200 cycles a tile, 16000 a piece.
-// That call takes 277 us with 20 and 36 for a job's start and its tiles, 225 with 110 and
-// 36, 210 with 190 and 33.)
+// the CTAs' clocks in one call, 2 x 12 sequences of 130 tokens: 3200 cycles a tile, 16000 a
+// piece.  It takes 277 us with 20 and 36 for a job's start and its tiles, 225 with 110 and
+// 36, 210 with 190 and 33; no other call was fitted.)
 constexpr int kCostTile64 = 22, kCostTile128 = 28, kCostTwo = 33;
 constexpr int kCostStart = 20, kCostStartTwo = 190;
 
@@ -69,7 +69,8 @@ __host__ __device__ __forceinline__ SharedLens shared_lens_of(const SharedArgs &
 }
 
 // Group n's sequences [g0, g0 + s).
-__host__ __device__ __forceinline__ void shared_group(const SharedArgs &a, const SharedLens &z, int n, int &g0, int &s) {
+__host__ __device__ __forceinline__ void shared_group(const SharedArgs &a, const SharedLens &z, int n, int &g0,
+                                                      int &s) {
     g0 = clamp_len(z.cu[n], a.p.B);
     s = clamp_len(z.cu[n + 1], a.p.B) - g0;
     if (s < 0) s = 0;
@@ -157,7 +158,8 @@ struct SharedJob {
 };
 
 // Block `block` of KV head kvh.
-__host__ __device__ __forceinline__ SharedJob shared_job(const SharedArgs &a, const SharedEntity &x, int kvh, int block) {
+__host__ __device__ __forceinline__ SharedJob shared_job(const SharedArgs &a, const SharedEntity &x, int kvh,
+                                                         int block) {
     const AttnParams &p = a.p;
     SharedJob k;
     k.kvh = kvh;
@@ -245,7 +247,8 @@ struct SharedWalker {
     // (from == to, or an entity past the last: an empty share)
     __host__ __device__ __forceinline__ SharedWalker(const SharedArgs &args, long long from, long long to,
                                                      const SharedBegin &begin)
-        : a(args), x0(from), x1(to), kvh(0), block(0), js(begin.es), done(from >= to || begin.e >= args.entities), s(begin) {
+        : a(args), x0(from), x1(to), kvh(0), block(0), js(begin.es),
+          done(from >= to || begin.e >= args.entities), s(begin) {
         if (done) return;
         const long long d = x0 - s.es;
         const bool small = ((d | s.x.cj) >> 31) == 0;

@@ -252,10 +252,8 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
         : "memory");
 }
 
-// For a whole warp to execute: one elected lane (the same one every time) issues.
-// Without a branch around them, and with the steps of a product in one statement, the
-// addresses and descriptors are computed in uniform registers, where the instructions
-// take them from (a lane's own branch cost 80 to 110 cycles an MMA, this 50).
+// For a whole warp to execute: one elected lane (the same one every time) issues, with no
+// branch around the instructions and the steps of a product in one statement.
 
 // D[tmem] = A[smem] . B[smem]^T over KSTEPS x 16 columns of K-major operands in chunks of
 // 64 columns, 16 KB apart.

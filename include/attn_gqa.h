@@ -608,7 +608,9 @@ ATTN_API int attn_rope_append_q8(const void *q, const void *k, const void *v, vo
  * than 2^30 rows (B * Q * Hq) and keys (max_pages * page_size), with at least one group
  * for AUTO.  AUTO runs other
  * problems, and the other values of algo run all of theirs, on the kernels of
- * attn_fwd_paged, which read each sequence's own table for every key.  The tcgen05
+ * attn_fwd_paged, which read each sequence's own table for every key.  AUTO does not
+ * weigh the two: where few keys are shared (up to 8192 by four sequences of one
+ * token, up to 320 by 64), attn_fwd_paged itself is the faster call.  The tcgen05
  * kernel rounds probabilities to q's type before the product with V, as attn_fwd
  * does; partial results are joined in fp32 in a fixed order, so that results do not
  * depend on timing.  A NaN or infinite value of a key that some row of the batch's
