@@ -59,9 +59,12 @@ def test_rope_refuses(lib, kw, needle):
     assert needle in lib.attn_last_error().decode()
 
 
-@pytest.mark.parametrize("ko", [192 * MB, 192 * MB + 3070, 192 * MB - 1534])
+Q_BYTES, K_BYTES = 6 * 256 * 2, 6 * 128 * 2  # of q_out and k_out
+
+
+@pytest.mark.parametrize("ko", [192 * MB, 192 * MB + Q_BYTES - 2, 192 * MB - K_BYTES + 2])
 def test_rope_refuses_outputs_that_overlap(lib, ko):
-    # q_out is 6 x 256 elements, k_out 6 x 128: the same memory, the last and the first element in common
+    # the same memory; one element in common, at either end
     assert _rope(lib, ko=ko) == 1
     assert "q_out and k_out overlap" in lib.attn_last_error().decode()
 
@@ -143,12 +146,12 @@ def test_append_q8_refuses(lib, kw, needle):
     assert needle in lib.attn_last_error().decode()
 
 
-@pytest.mark.parametrize("call,kw", [(_append, dict(qo=512 * MB)), (_append, dict(qo=512 * MB - 3070)),
+@pytest.mark.parametrize("call,kw", [(_append, dict(qo=512 * MB)), (_append, dict(qo=512 * MB - Q_BYTES + 2)),
                                      (_append, dict(qo=768 * MB + 262142)), (_append_q8, dict(qo=512 * MB + 131070)),
                                      (_append_q8, dict(qo=768 * MB)), (_append_q8, dict(qo=5 * MB)),
                                      (_append_q8, dict(qo=6 * MB + 510))])
 def test_append_refuses_queries_in_the_cache(lib, call, kw):
-    # pages of 16 x 64 rows of 2 heads of 64 are 256 KB (8 bits: 128), scales 512 bytes, q_out 3072
+    # pages of 16 x 64 rows of 2 heads of 64 are 256 KB (8 bits: 128), scales 512 bytes
     assert call(lib, **kw) == 1
     assert "q_out overlaps the cache" in lib.attn_last_error().decode()
 
